@@ -329,8 +329,8 @@ def run(st):
                           w13s_scale=st["w13s_scale"], w2s_scale=st["w2s_scale"])
         return st["out"], st["idx"], st["w"]
     if op == "mxfp4":
-        B.moe_quantize_mxfp4(st["w"], st["q"], st["s"])
-        B.moe_dequantize_mxfp4(st["q"], st["s"], st["back"])
+        B.moe_quantize_mx(st["w"], st["q"], st["s"])
+        B.moe_dequantize_mx(st["q"], st["s"], st["back"])
         return st["back"], st["s"]
     if op == "norm":
         B.moe_norm_residual(cfg, st["h"], st["y"], st["gamma_post"], st["h_out"], EPS,
