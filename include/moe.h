@@ -68,10 +68,12 @@ typedef enum {
 
 typedef enum {
     MOE_DTYPE_BF16 = 0,              /* bf16 activations and weights, fp32 accumulation */
-    MOE_DTYPE_FP8_E4M3_BLOCK128 = 1  /* expert weights e4m3 (OCP FP8, 1 byte) with one fp32
+    MOE_DTYPE_FP8_E4M3_BLOCK128 = 1, /* expert weights e4m3 (OCP FP8, 1 byte) with one fp32
                                         scale per 128 x 128 block; expert-GEMM activations
                                         quantised to e4m3 per row and 128 columns
-                                        (moe_quantize_act); router stays bf16           */
+                                        (moe_quantize_act); router stays bf16          */
+    MOE_DTYPE_MXFP4_BLOCK32 = 2      /* expert weights MXFP4 (moe_quantize_mx): e2m1 codes with one
+                                        e8m0 scale per 32 columns; moe_forward_few only */
 } moe_dtype_t;
 
 /* Layer description.  Field names follow the Dots1 / DeepSeek-V3 config:
@@ -226,6 +228,25 @@ moe_status_t moe_expert_ffn(const moe_config_t* cfg, const void* x, const int32_
 moe_status_t moe_quantize_act(const void* x, int32_t rows, int32_t cols, uint8_t* q, float* scale,
                               moe_stream_t stream);
 
+/* MXFP4 weights (the microscaled 4-bit format of the OCP MX specification;
+ * the pages' weights are BF16 and FP8, 4 bits are this library's).  A matrix
+ * x bf16 [rows, cols] (cols a multiple of 32) becomes, per row and block of
+ * 32 columns, an e8m0 scale byte and 32 e2m1 codes:
+ *   scale byte s = floor(log2 amax) - 2 + 127, at least 0 (127 for an all-zero
+ *                  block, 255 with codes 0 for one holding an infinity or NaN)
+ *   code         = e2m1(x * 2^(127 - s)), round to nearest even, saturating at
+ *                  +-6; -0 keeps its sign
+ *   q     uint8 [rows, cols/2]   column 2i in the low, 2i+1 in the high half
+ *   scale uint8 [rows, cols/32]
+ * moe_dequantize_mx writes the bf16 values code * 2^(s - 127), which are
+ * exact for every scale moe_quantize_mx produces (a scale byte of 253 or 254
+ * can overflow to infinity; 255 gives NaN).  x and q 16-byte aligned; no
+ * workspace; rows or cols of 0 launch nothing.                            */
+moe_status_t moe_quantize_mx(const void* x, int32_t rows, int32_t cols, uint8_t* q, uint8_t* scale,
+                             moe_stream_t stream);
+moe_status_t moe_dequantize_mx(const uint8_t* q, const uint8_t* scale, int32_t rows, int32_t cols,
+                               void* x, moe_stream_t stream);
+
 /* Combine: step a9 (Deep Dive §3.3 "Weighted sum" then shared "add").
  * out_t = sum_{j=0..k-1} y[pos[t*k + j]] + y_shared_t, summed in fp32 in
  * that fixed order (no atomics: bitwise reproducible), rounded once to bf16.
@@ -275,6 +296,92 @@ moe_status_t moe_forward_block(const moe_config_t* cfg, const void* h, const voi
                                const float* w2_scale, const void* w13s, const float* w13s_scale,
                                const void* w2s, const float* w2s_scale, void* out, void* ws,
                                size_t ws_bytes, void* const* stage_events, moe_stream_t stream);
+
+/* The whole layer for a few tokens (decode of 1..MOE_FEW_MAX_T users), in one
+ * launch: the same steps a1-a9 as moe_forward, for batches so small that the
+ * weights of the touched experts are all the traffic.  Differences from
+ * moe_forward:
+ *   - T <= MOE_FEW_MAX_T (above it MOE_ERR_UNSUPPORTED: use moe_forward);
+ *   - dtype may also be MOE_DTYPE_MXFP4_BLOCK32, and activations stay bf16
+ *     for every weight type (no moe_quantize_act step: nothing here is bound
+ *     by the matrix rate);
+ *   - nothing is rounded between the steps: logits, scores, the choice and the
+ *     routing weights are computed in binary64 (topk_w is rounded to fp32
+ *     once; equal keys take the lower expert, NaN keys rank below numbers),
+ *     the SwiGLU outputs are carried with 16 significand bits, every sum is
+ *     fp32, and out is rounded once.  Where two keys lie within fp32 rounding
+ *     of each other moe_route may choose differently.
+ * Arguments as moe_forward, except:
+ *   *_scale   fp32 block scales (FP8), uint8 e8m0 scales (MXFP4: w13_scale
+ *             [E, 2I, H/32], w2_scale [E, H, I/32], w13s_scale [2Is, H/32],
+ *             w2s_scale [H, Is/32]), NULL for bf16; MXFP4 codes are
+ *             [E, 2I, H/2], [E, H, I/2], [2Is, H/2], [H, Is/2] bytes.  Weight
+ *             and MXFP4 scale pointers 16-byte aligned
+ *   topk_idx  int32 [T, k] out, or NULL    the choice, slot order
+ *   topk_w    fp32 [T, k] out, or NULL     its routing weights
+ *   ws        moe_few_workspace_size bytes, 256-byte aligned, zero-filled
+ *             before its first use (every completed call leaves its counters
+ *             at zero; after an error moe_check_device_status clears them)
+ * The result does not depend on scheduling: no float atomics, fixed order.
+ * The launch is cooperative (its blocks wait for one another, with a bounded
+ * wait), so it needs the whole GPU to itself while it starts; it can be
+ * captured.  T = 0 launches nothing.                                        */
+#define MOE_FEW_MAX_T 16
+size_t moe_few_workspace_size(const moe_config_t* cfg);
+moe_status_t moe_forward_few(const moe_config_t* cfg, const void* x, const void* w_router,
+                             const float* bias, const void* w13, const void* w13_scale,
+                             const void* w2, const void* w2_scale, const void* w13s,
+                             const void* w13s_scale, const void* w2s, const void* w2s_scale,
+                             void* out, int32_t* topk_idx, float* topk_w, void* ws,
+                             size_t ws_bytes, moe_stream_t stream);
+
+/* Norms around a block, fused with its gate and the residual scale: the
+ * boundary between a block's output y and the next block's input.  The pages'
+ * diagram has the norm before the block (moe_rmsnorm); the norm after it, the
+ * gate and the scale are this library's.
+ *   n  = gamma_post * y * rp,          rp = 1 / sqrt(mean(y^2) + eps)
+ *   h' = res_scale * h + gate * n
+ *   u  = gamma_pre * h' * rq,          rq = 1 / sqrt(mean(h'^2) + eps)
+ * all in fp32 with one bf16 rounding of h' and one of u (u is computed from
+ * the unrounded h').
+ *   h, y       bf16 [T, H]     residual stream, block output
+ *   gamma_post bf16 [H]
+ *   gate       by gate_mode: NULL (MOE_GATE_NONE: 1), bf16 [H]
+ *              (MOE_GATE_CHANNEL) or bf16 [T, H] (MOE_GATE_TOKEN)
+ *   gamma_pre  bf16 [H], or NULL with u NULL: no norm after the update
+ *   h_out      bf16 [T, H] out (may be h itself)
+ *   u          bf16 [T, H] out, or NULL (may be y itself, not h or h_out)
+ *   rstd       fp32 [2, T] out, or NULL: rp, then rq (row 1 is left alone
+ *              without u); the backward pass needs it
+ * Only cfg->T and cfg->H are read; H a multiple of 8, at most 16384.  bf16
+ * pointers 16-byte aligned.  Buffers overlap only where named above.        */
+#define MOE_GATE_NONE 0
+#define MOE_GATE_CHANNEL 1
+#define MOE_GATE_TOKEN 2
+moe_status_t moe_norm_residual(const moe_config_t* cfg, const void* h, const void* y,
+                               const void* gamma_post, const void* gate, int32_t gate_mode,
+                               float res_scale, float eps, const void* gamma_pre, void* h_out,
+                               void* u, float* rstd, moe_stream_t stream);
+
+/* Its gradients, for a loss with gradients dh_out at h' and du at u:
+ *   rstd        fp32 [2, T]     the forward's
+ *   dh_out      bf16 [T, H];  du bf16 [T, H], NULL exactly when gamma_pre is
+ *   dh, dy      bf16 [T, H] out (dh may be dh_out itself, dy may be du)
+ *   dgate       fp32 [H] out (channel: summed over the tokens), bf16 [T, H]
+ *               out (token; may be the gate itself), NULL without a gate
+ *   dgamma_post fp32 [H] out;  dgamma_pre fp32 [H] out, NULL without gamma_pre
+ *   ws          moe_norm_residual_workspace_size bytes, 256-byte aligned, no
+ *               zero-fill needed
+ * All outputs are overwritten; the column sums are taken in a fixed order.
+ * T = 0 writes zeros to dgamma_post, dgamma_pre and a channel dgate.        */
+size_t moe_norm_residual_workspace_size(const moe_config_t* cfg);
+moe_status_t moe_norm_residual_backward(const moe_config_t* cfg, const void* h, const void* y,
+                                        const void* gamma_post, const void* gate,
+                                        int32_t gate_mode, float res_scale, const void* gamma_pre,
+                                        const float* rstd, const void* dh_out, const void* du,
+                                        void* dh, void* dy, void* dgate, float* dgamma_post,
+                                        float* dgamma_pre, void* ws, size_t ws_bytes,
+                                        moe_stream_t stream);
 
 /* Device byte offsets, inside the workspace, of the intermediates that
  * moe_forward leaves there (for inspection and tests):

@@ -23,6 +23,9 @@ MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_CUD
     MOE_ERR_TIMEOUT = range(6)
 MOE_DTYPE_BF16 = 0
 MOE_DTYPE_FP8_E4M3_BLOCK128 = 1
+MOE_DTYPE_MXFP4_BLOCK32 = 2      # moe_forward_few only
+MOE_FEW_MAX_T = 16
+MOE_GATE_NONE, MOE_GATE_CHANNEL, MOE_GATE_TOKEN = range(3)
 MOE_NUM_STAGES = 6
 MOE_NUM_BWD_STAGES = 7
 BWD_STAGE_NAMES = ("dispatch", "gate_up_recompute", "down_backward", "router", "input_grads",
@@ -40,7 +43,9 @@ EXPORTED = ("moe_get_last_error", "moe_workspace_size", "moe_workspace_offset", 
             "moe_quantize_act", "moe_rmsnorm", "moe_forward_block",
             "moe_backward_workspace_size", "moe_backward", "moe_ep_pack",
             "moe_shared_expert", "moe_ep_expert_counts", "moe_ep_plan", "moe_ep_dispatch_peer",
-            "moe_ep_combine_peer",
+            "moe_ep_combine_peer", "moe_few_workspace_size", "moe_forward_few",
+            "moe_quantize_mx", "moe_dequantize_mx", "moe_norm_residual",
+            "moe_norm_residual_workspace_size", "moe_norm_residual_backward",
             "dsa_workspace_size", "dsa_workspace_scores_offset", "dsa_index_scores",
             "dsa_index_topk", "dsa_indexer")
 
@@ -156,6 +161,22 @@ _lib.moe_ep_dispatch_peer.argtypes = [_CFG, ctypes.c_int32, ctypes.c_int32] + [_
 _lib.moe_ep_combine_peer.restype = ctypes.c_int
 _lib.moe_ep_combine_peer.argtypes = [_CFG, ctypes.c_int32, ctypes.c_int32] + [_P] * 8 + [
     ctypes.c_int32, _P]
+_lib.moe_few_workspace_size.restype = ctypes.c_size_t
+_lib.moe_few_workspace_size.argtypes = [_CFG]
+_lib.moe_forward_few.restype = ctypes.c_int
+_lib.moe_forward_few.argtypes = [_CFG] + [_P] * 15 + [ctypes.c_size_t, _P]
+_lib.moe_quantize_mx.restype = ctypes.c_int
+_lib.moe_quantize_mx.argtypes = [_P, ctypes.c_int32, ctypes.c_int32, _P, _P, _P]
+_lib.moe_dequantize_mx.restype = ctypes.c_int
+_lib.moe_dequantize_mx.argtypes = [_P, _P, ctypes.c_int32, ctypes.c_int32, _P, _P]
+_lib.moe_norm_residual.restype = ctypes.c_int
+_lib.moe_norm_residual.argtypes = [_CFG, _P, _P, _P, _P, ctypes.c_int32, ctypes.c_float,
+                                   ctypes.c_float, _P, _P, _P, _P, _P]
+_lib.moe_norm_residual_workspace_size.restype = ctypes.c_size_t
+_lib.moe_norm_residual_workspace_size.argtypes = [_CFG]
+_lib.moe_norm_residual_backward.restype = ctypes.c_int
+_lib.moe_norm_residual_backward.argtypes = ([_CFG, _P, _P, _P, _P, ctypes.c_int32, ctypes.c_float]
+                                            + [_P] * 10 + [ctypes.c_size_t, _P])
 _lib.moe_check_device_status.restype = ctypes.c_int
 _lib.moe_check_device_status.argtypes = [_P, _P]
 
@@ -384,6 +405,151 @@ def moe_backward(cfg, x, w_router, logits, topk_idx, topk_w, w13, w2, w13s, w2s,
                              _ptr(w2s), _ptr(dout), _ptr(dx), _ptr(dw_router), _ptr(dw13),
                              _ptr(dw2), _ptr(dw13s), _ptr(dw2s), _ptr(dlogits), _ptr(ws),
                              ws.numel(), ev, _stream(stream)), "moe_backward")
+
+
+# The entry points below look their tensors over (type, size, dense layout,
+# current device) before they pass the pointers on: the C ABI sees none of it.
+def _want(where, name, t, dtype, numel, optional=False):
+    if t is None:
+        if optional:
+            return
+        raise ValueError("%s: %s is None" % (where, name))
+    if t.dtype is not dtype:
+        raise TypeError("%s: %s must be %s, is %s" % (where, name, dtype, t.dtype))
+    if t.numel() != numel:
+        raise ValueError("%s: %s has %d elements, needs %d" % (where, name, t.numel(), numel))
+    if not t.is_contiguous():
+        raise ValueError("%s: %s must be dense and row-major" % (where, name))
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        raise ValueError("%s: %s must be on the current CUDA device" % (where, name))
+
+
+def few_workspace_size(cfg: MoeConfig) -> int:
+    c = cfg.c()
+    n = _lib.moe_few_workspace_size(ctypes.byref(c))
+    if n == 0:
+        raise MoeError(MOE_ERR_INVALID_ARG, "moe_few_workspace_size")
+    return n
+
+
+def alloc_few_workspace(cfg: MoeConfig, device="cuda") -> torch.Tensor:
+    """A zeroed workspace of moe_few_workspace_size bytes (256-byte aligned)."""
+    return torch.zeros(few_workspace_size(cfg), dtype=torch.uint8, device=device)
+
+
+def moe_forward_few(cfg, x, w_router, bias, w13, w2, w13s, w2s, out, ws, topk_idx=None,
+                    topk_w=None, stream=None, w13_scale=None, w2_scale=None, w13s_scale=None,
+                    w2s_scale=None):
+    """The whole layer for T <= MOE_FEW_MAX_T tokens in one launch; weights bf16,
+    e4m3 (fp32 128x128 block scales) or MXFP4 (moe_quantize_mx)."""
+    c = cfg.c()
+    T, H, E, k, I, Is = cfg.T, cfg.H, cfg.E, cfg.k, cfg.I, cfg.Is
+    f = "moe_forward_few"
+    mx = cfg.dtype == MOE_DTYPE_MXFP4_BLOCK32
+    bf = torch.bfloat16
+    wt = bf if cfg.dtype == MOE_DTYPE_BF16 else torch.uint8
+    pack = 2 if mx else 1
+    _want(f, "x", x, bf, T * H)
+    _want(f, "out", out, bf, T * H)
+    _want(f, "w_router", w_router, bf, E * H)
+    _want(f, "bias", bias, torch.float32, E)
+    _want(f, "topk_idx", topk_idx, torch.int32, T * k, True)
+    _want(f, "topk_w", topk_w, torch.float32, T * k, True)
+    _want(f, "w13", w13, wt, E * 2 * I * H // pack)
+    _want(f, "w2", w2, wt, E * H * I // pack)
+    if Is:
+        _want(f, "w13s", w13s, wt, 2 * Is * H // pack)
+        _want(f, "w2s", w2s, wt, H * Is // pack)
+    if cfg.dtype != MOE_DTYPE_BF16:
+        st, block = (torch.uint8, 32) if mx else (torch.float32, 128 * 128)
+        _want(f, "w13_scale", w13_scale, st, E * 2 * I * H // block)
+        _want(f, "w2_scale", w2_scale, st, E * H * I // block)
+        if Is:
+            _want(f, "w13s_scale", w13s_scale, st, 2 * Is * H // block)
+            _want(f, "w2s_scale", w2s_scale, st, H * Is // block)
+    _check(_lib.moe_forward_few(ctypes.byref(c), _ptr(x), _ptr(w_router), _ptr(bias), _ptr(w13),
+                                _ptr(w13_scale), _ptr(w2), _ptr(w2_scale), _ptr(w13s),
+                                _ptr(w13s_scale), _ptr(w2s), _ptr(w2s_scale), _ptr(out),
+                                _ptr(topk_idx), _ptr(topk_w), _ptr(ws), ws.numel(),
+                                _stream(stream)), f)
+
+
+def moe_quantize_mx(x, q, scale, stream=None):
+    """bf16 x [rows, cols] -> MXFP4: codes q uint8 [rows, cols/2] and e8m0 scale
+    bytes uint8 [rows, cols/32]."""
+    rows, cols = x.shape
+    _want("moe_quantize_mx", "x", x, torch.bfloat16, rows * cols)
+    _want("moe_quantize_mx", "q", q, torch.uint8, rows * cols // 2)
+    _want("moe_quantize_mx", "scale", scale, torch.uint8, rows * cols // 32)
+    _check(_lib.moe_quantize_mx(_ptr(x), rows, cols, _ptr(q), _ptr(scale), _stream(stream)),
+           "moe_quantize_mx")
+
+
+def moe_dequantize_mx(q, scale, x, stream=None):
+    """MXFP4 codes and scales -> the bf16 values they stand for, x [rows, cols]."""
+    rows, cols = x.shape
+    _want("moe_dequantize_mx", "x", x, torch.bfloat16, rows * cols)
+    _want("moe_dequantize_mx", "q", q, torch.uint8, rows * cols // 2)
+    _want("moe_dequantize_mx", "scale", scale, torch.uint8, rows * cols // 32)
+    _check(_lib.moe_dequantize_mx(_ptr(q), _ptr(scale), rows, cols, _ptr(x), _stream(stream)),
+           "moe_dequantize_mx")
+
+
+def _gate_numel(cfg, gate_mode):
+    return cfg.T * cfg.H if gate_mode == MOE_GATE_TOKEN else cfg.H
+
+
+def moe_norm_residual(cfg, h, y, gamma_post, h_out, eps, gate=None, gate_mode=MOE_GATE_NONE,
+                      res_scale=1.0, gamma_pre=None, u=None, rstd=None, stream=None):
+    """h_out = res_scale * h + gate * norm(y); u = norm(h_out) (with gamma_pre)."""
+    c = cfg.c()
+    f, bf, n = "moe_norm_residual", torch.bfloat16, cfg.T * cfg.H
+    for name, t in (("h", h), ("y", y), ("h_out", h_out)):
+        _want(f, name, t, bf, n)
+    _want(f, "u", u, bf, n, True)
+    _want(f, "gamma_post", gamma_post, bf, cfg.H)
+    _want(f, "gamma_pre", gamma_pre, bf, cfg.H, True)
+    _want(f, "gate", gate, bf, _gate_numel(cfg, gate_mode), True)
+    _want(f, "rstd", rstd, torch.float32, 2 * cfg.T, True)
+    _check(_lib.moe_norm_residual(ctypes.byref(c), _ptr(h), _ptr(y), _ptr(gamma_post), _ptr(gate),
+                                  int(gate_mode), float(res_scale), float(eps), _ptr(gamma_pre),
+                                  _ptr(h_out), _ptr(u), _ptr(rstd), _stream(stream)), f)
+
+
+def norm_residual_workspace_size(cfg: MoeConfig) -> int:
+    c = cfg.c()
+    n = _lib.moe_norm_residual_workspace_size(ctypes.byref(c))
+    if n == 0:
+        raise MoeError(MOE_ERR_INVALID_ARG, "moe_norm_residual_workspace_size")
+    return n
+
+
+def alloc_norm_residual_workspace(cfg: MoeConfig, device="cuda") -> torch.Tensor:
+    return torch.empty(norm_residual_workspace_size(cfg), dtype=torch.uint8, device=device)
+
+
+def moe_norm_residual_backward(cfg, h, y, gamma_post, rstd, dh_out, dh, dy, dgamma_post, ws,
+                               gate=None, gate_mode=MOE_GATE_NONE, res_scale=1.0, gamma_pre=None,
+                               du=None, dgamma_pre=None, dgate=None, stream=None):
+    """Gradients of moe_norm_residual: dh, dy (bf16), dgamma_post, dgamma_pre (fp32)
+    and dgate (fp32 [H] for a gate per channel, bf16 [T, H] for one per token)."""
+    c = cfg.c()
+    f, bf, f32, n = "moe_norm_residual_backward", torch.bfloat16, torch.float32, cfg.T * cfg.H
+    for name, t in (("h", h), ("y", y), ("dh_out", dh_out), ("dh", dh), ("dy", dy)):
+        _want(f, name, t, bf, n)
+    _want(f, "du", du, bf, n, True)
+    _want(f, "rstd", rstd, f32, 2 * cfg.T)
+    _want(f, "gamma_post", gamma_post, bf, cfg.H)
+    _want(f, "gamma_pre", gamma_pre, bf, cfg.H, True)
+    _want(f, "dgamma_post", dgamma_post, f32, cfg.H)
+    _want(f, "dgamma_pre", dgamma_pre, f32, cfg.H, True)
+    _want(f, "gate", gate, bf, _gate_numel(cfg, gate_mode), True)
+    _want(f, "dgate", dgate, bf if gate_mode == MOE_GATE_TOKEN else f32,
+          _gate_numel(cfg, gate_mode), True)
+    _check(_lib.moe_norm_residual_backward(
+        ctypes.byref(c), _ptr(h), _ptr(y), _ptr(gamma_post), _ptr(gate), int(gate_mode),
+        float(res_scale), _ptr(gamma_pre), _ptr(rstd), _ptr(dh_out), _ptr(du), _ptr(dh), _ptr(dy),
+        _ptr(dgate), _ptr(dgamma_post), _ptr(dgamma_pre), _ptr(ws), ws.numel(), _stream(stream)), f)
 
 
 def moe_check_device_status(ws, stream=None):
