@@ -152,10 +152,10 @@ def test_nan_and_infinite_tokens_stay_in_their_rows(B):
     assert p["idx"][2].cpu().tolist() == [0, 1, 2, 3]
 
 
-@pytest.mark.parametrize("kind", ["fp8", "mxfp4"])
+@pytest.mark.parametrize("kind", KINDS)
 def test_nan_weights_are_seen(B, kind):
-    """A NaN code (e4m3 0x7f) or scale (e8m0 255) of a down projection row makes that output NaN
-    for the tokens of its expert, and no other."""
+    """A NaN weight, code (e4m3 0x7f) or scale (e8m0 255) of a down projection row makes that output
+    NaN for the tokens of its expert, and no other."""
     p = make(B, kind, 3, 256, 32, 2, 128, seed=11)
     clean = torch.empty_like(p["out"])
     call(B, p, out=clean)
@@ -163,6 +163,8 @@ def test_nan_weights_are_seen(B, kind):
     e = int(p["idx"][1, 0])
     if kind == "fp8":
         p["w2"][0][e, 77, 33] = 0xff
+    elif kind == "bf16":
+        p["w2"][0][e, 77, 33] = math.nan
     else:
         p["w2"][1][e, 77, 1] = 255
     call(B, p)
