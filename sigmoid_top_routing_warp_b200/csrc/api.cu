@@ -1182,6 +1182,28 @@ moe_status_t api_make_map_3d_bf16(CUtensorMap* m, const void* ptr, uint64_t d0, 
     return MOE_OK;
 }
 
+// Bytes as a tensor of `rank` dimensions (strides of all but the first, in
+// bytes), 64-byte swizzle.
+moe_status_t api_make_map_u8_sw64(CUtensorMap* m, const void* ptr, uint32_t rank, const uint64_t* dims,
+                                  const uint64_t* strides, const uint32_t* box, const char* what) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
+    if (!aligned16(ptr)) return fail(MOE_ERR_INVALID_ARG, "%s must be 16-byte aligned", what);
+    cuuint64_t d[5], st[4];
+    cuuint32_t b[5], estr[5];
+    for (uint32_t i = 0; i < rank; ++i) {
+        d[i] = dims[i];
+        b[i] = box[i];
+        estr[i] = 1;
+        if (i + 1 < rank) st[i] = strides[i];
+    }
+    CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void*>(ptr), d, st, b, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(MOE_ERR_CUDA, "tensor map for %s failed (%d)", what, (int)r);
+    return MOE_OK;
+}
+
 // Store map of an fp32 or bf16 3-D tensor {d0, d1, d2} (d0 contiguous; byte
 // strides of d1 and d2), box {b0, b1, 1}, no swizzle: a staged row-major
 // [b1][b0] tile in shared memory goes out in one bulk tensor store, clipped

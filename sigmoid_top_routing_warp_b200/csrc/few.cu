@@ -7,8 +7,8 @@
 // one block per SM, each block walking its share of the weight rows through a
 // shared-memory ring while the multiplications keep up behind it.
 //
-// Roles in a block (17 warps):
-//   warp 16     producer: bulk copies of weight rows and of the activations
+// Roles in a block (13 warps):
+//   warp 12     producer: bulk copies of weight rows and of the activations
 //               they meet, stage by stage, as far ahead as the ring is deep
 //   warps 0-7   consumers: m16n8k16 matrix instructions, 16 weight rows by 8
 //               tokens; the tokens are the short side, so the 128-row tiles
@@ -16,7 +16,7 @@
 //               (a decode token touches 1728 16-row units but 216 of 128
 //               rows), and 4- and 8-bit weights need their values widened in
 //               registers anyway
-//   warps 8-15  router: logits, choice and the plan of touched experts, while
+//   warps 8-11  router: logits, choice and the plan of touched experts, while
 //               the consumers already work on the shared expert, which needs
 //               no choice
 //
@@ -34,9 +34,9 @@
 //
 // 8- and 4-bit weights become bf16 by moving their bits into a bf16's sign,
 // exponent and mantissa fields (e4m3 as value * 2^-120, e2m1 as value *
-// 2^-126: subnormals stay subnormals, so no case is special); the activations
-// carry 2^64, and the products are brought back (2^56, 2^62) together with the
-// block scales, in fp32.  Nothing is rounded on the way.
+// 2^-126: subnormals stay subnormals, so no case is special) and one exact
+// bf16 product that brings them back; their block scales multiply the products
+// in fp32.  Nothing is rounded on the way.
 #include "moe.h"
 #include "kernels.cuh"
 #include "ptx.cuh"
@@ -46,49 +46,56 @@
 #include <cuda_runtime.h>
 
 #include <cstdio>
+#include <cstring>
 
 namespace moe {
 moe_status_t api_check_config(const moe_config_t* c);
 moe_status_t api_fail(moe_status_t st, const char* msg);
 void api_clear_error();
 moe_status_t api_sm_count(int* n);
+moe_status_t api_make_map_u8_sw64(CUtensorMap* m, const void* ptr, uint32_t rank, const uint64_t* dims,
+                                  const uint64_t* strides, const uint32_t* box, const char* what);
 }  // namespace moe
 
 namespace {
 
 constexpr int kT = MOE_FEW_MAX_T;
-constexpr int kWarps = 8;                        // consumers, and as many router warps
-constexpr int kGroup = kWarps * 32;
-constexpr int kThreads = 2 * kGroup + 32;
+constexpr int kWarps = 8;                        // consumers
+constexpr int kRouters = 4;
+constexpr int kGroup = kWarps * 32, kRouterGroup = kRouters * 32;
+constexpr int kThreads = kGroup + kRouterGroup + 32;
 constexpr int kChunk = 512;                      // K columns of a full stage
-constexpr int kXStride = kChunk * 2 + 64;        // bytes between activation rows of a stage
-constexpr int kXStrideHalf = kChunk + 64;        // the same of a 256-column stage
+constexpr int kBox = 256;                        // K columns of one tensor copy
+constexpr int kBoxBytes = 8192;                  // its bytes, for every weight type
+constexpr int kSlice = kChunk / kWarps;          // K columns of a warp in a stage
 constexpr int kMaxStages = 16;
 constexpr int kBarWord = moe::kSchedFirstWord;   // grid barriers (2) and the exit count, in the status block
-constexpr float kLift = 0x1p64f;                 // factor of the activations for 8- and 4-bit weights
 
-// Per weight type: rows of a unit, smem bytes between rows, bits per weight.
-// A stage holds about 17 KB of weights.  Row strides keep a fragment load's
-// lanes (8 rows x 4 lanes of 16, 8 or 4 bytes) on different banks.
+// Per weight type: rows of a unit, bits of a weight, bytes of a stage's
+// scales, and the activation rows' padding in a stage.  A stage holds 16 KB of
+// weights, as 64-byte pieces of 8 rows (512 bytes, 64-byte swizzle): a
+// fragment load's lanes (8 rows by four 16-byte pieces) then fall on different
+// banks.  The padding does the same for the activations (16 bytes a lane; 32
+// for e4m3, whose lanes hold 16 weights).
 template <int DT>
 struct Fmt;
 template <>
 struct Fmt<MOE_DTYPE_BF16> {
-    static constexpr int kRows = 16, kStride = 1024 + 64, kBits = 16, kScaleStride = 0;
+    static constexpr int kRows = 16, kBits = 16, kScaleBytes = 0, kPad = 64;
 };
 template <>
 struct Fmt<MOE_DTYPE_FP8_E4M3_BLOCK128> {
-    static constexpr int kRows = 32, kStride = 512 + 32, kBits = 8, kScaleStride = 0;
+    static constexpr int kRows = 32, kBits = 8, kScaleBytes = 128, kPad = 16;  // scales: [2][4] fp32
 };
 template <>
 struct Fmt<MOE_DTYPE_MXFP4_BLOCK32> {
-    static constexpr int kRows = 64, kStride = 256 + 16, kBits = 4, kScaleStride = 32;
+    static constexpr int kRows = 64, kBits = 4, kScaleBytes = 1024, kPad = 64;  // [64][16] e8m0
 };
 
 struct FewArgs {
+    CUtensorMap m13, m2, m13s, m2s;   // weights (see few_maps)
     const uint16_t *x, *w_router;
     const float* bias;
-    const uint8_t *w13, *w2, *w13s, *w2s;
     const void *s13, *s2, *s13s, *s2s;
     uint16_t* out;
     int32_t* idx;
@@ -101,7 +108,7 @@ struct FewArgs {
     int T, H, E, k, I, Is, n_group, topk_group, group_topn, norm, n_split, stall, ld_act;
     float rsf;
     // shared-memory layout (bytes)
-    int off_active, off_pairw, off_scratch, off_ring, stage_bytes, off_x, n_stages;
+    int off_active, off_pairw, off_scratch, off_red, off_ring, stage_bytes, n_stages;
 };
 
 // One touched expert: its tokens (bit mask), their number and its first
@@ -121,7 +128,7 @@ struct Plan {
 
 // Scratch of the router warps; the consumers' reduction buffer is apart.
 struct Scratch {
-    double* keys;      // [min(T, 8)][E]
+    double* keys;      // [min(T, kRouters)][E]
     int* sel;          // [T, k]
     float* selw;       // [T, k]
     uint32_t* emask;   // [E] tokens of each expert
@@ -137,35 +144,47 @@ __device__ __forceinline__ void unpack8(const uint4& v, float* f) {
     }
 }
 
-// Barrier of the `kGroup` threads of a role; true when any of them says `bad`.
+// Barrier of the consumers (id 1) or the router warps (id 2); true when any of
+// their threads says `bad`.
 __device__ __forceinline__ bool group_any(int id, bool bad) {
     int r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %2, 0;\n\t"
         "barrier.cta.red.or.pred q, %1, %3, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
         : "=r"(r)
-        : "r"(id), "r"((int)bad), "r"(kGroup)
+        : "r"(id), "r"((int)bad), "r"(id == 1 ? kGroup : kRouterGroup)
         : "memory");
     return r != 0;
 }
 
-__device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
-
-// Untiled bulk copy global -> shared (both 16-byte aligned, bytes a multiple
-// of 16), counted on `bar`.
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+// Tensor copies of one box, with an L2 policy.
+__device__ __forceinline__ void box_load_4d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int c2, int c3,
+                                            uint64_t policy) {
     asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-        "l"(src), "r"(bytes), "r"(bar)
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%3, %3, %4, %5}], [%2], %6;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(0), "r"(c2), "r"(c3), "l"(policy)
         : "memory");
 }
-__device__ __forceinline__ void bulk_load_hint(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar,
-                                               uint64_t policy) {
+__device__ __forceinline__ void box_load_5d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int c2, int c4,
+                                            uint64_t policy) {
     asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
-        " [%0], [%1], %2, [%3], %4;" ::"r"(dst),
-        "l"(src), "r"(bytes), "r"(bar), "l"(policy)
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%3, %3, %4, %3, %5}], [%2], %6;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(0), "r"(c2), "r"(c4), "l"(policy)
         : "memory");
+}
+
+// Asynchronous copies of 16 or 4 bytes by this thread, and its arrival on
+// `bar` once all of them have landed.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void arrive_copied(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(moe::smem_addr(bar)) : "memory");
 }
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -205,7 +224,7 @@ __device__ void router_phase(const FewArgs& a, int warp) {
     const int nch = a.H / 8;
     const int per = (nch + a.n_split - 1) / a.n_split;
     const int units = a.E * a.n_split;
-    for (int u = blockIdx.x * kWarps + warp; u < units; u += gridDim.x * kWarps) {
+    for (int u = blockIdx.x * kRouters + warp; u < units; u += gridDim.x * kRouters) {
         const int e = u / a.n_split, sp = u % a.n_split;
         const int c1 = min(nch, (sp + 1) * per);
         const uint4* wr = reinterpret_cast<const uint4*>(a.w_router + (size_t)e * a.H);
@@ -310,9 +329,9 @@ __device__ void choose(const FewArgs& a, int t, double* key, const Scratch& S) {
 // and pairs, from the choice.  All router threads; `tid` within them.
 __device__ void build_plan(const FewArgs& a, const Plan& P, const Scratch& S, int tid) {
     const int lane = tid & 31;
-    for (int e = tid; e < a.E; e += kGroup) S.emask[e] = 0;
+    for (int e = tid; e < a.E; e += kRouterGroup) S.emask[e] = 0;
     group_any(2, false);
-    for (int i = tid; i < a.T * a.k; i += kGroup) atomicOr(&S.emask[S.sel[i]], 1u << (i / a.k));
+    for (int i = tid; i < a.T * a.k; i += kRouterGroup) atomicOr(&S.emask[S.sel[i]], 1u << (i / a.k));
     group_any(2, false);
     if (tid < 32) {
         int n = 0, pairs = 0;
@@ -343,8 +362,8 @@ __device__ void build_plan(const FewArgs& a, const Plan& P, const Scratch& S, in
     }
     group_any(2, false);
     if (a.Is)
-        for (int t = tid; t < a.T; t += kGroup) P.pairw[t] = 1.0f;
-    for (int i = tid; i < a.T * a.k; i += kGroup) {
+        for (int t = tid; t < a.T; t += kRouterGroup) P.pairw[t] = 1.0f;
+    for (int i = tid; i < a.T * a.k; i += kRouterGroup) {
         const Active act = P.active[S.apos[S.sel[i]]];
         const int t = i / a.k;
         P.pairw[act.base + __popc(act.mask & ((1u << t) - 1u))] = S.selw[i];
@@ -367,10 +386,18 @@ struct Shares {
     __device__ int r_at(int c) const {
         return joint1 ? (int)((long long)c * (us + ur) / G) - s_at(c) : (int)((long long)c * ur / G);
     }
+    // a cut moves back to the start of its tensor copy (two steps)
     __device__ long long b_at(int c) const {
-        if (!joint2) return c * tot2 / G;
-        const long long tot = (long long)(us + ur) * ublk + tot2;
-        return c * tot / G - (long long)(s_at(c) + r_at(c)) * ublk;
+        long long b;
+        if (joint2) {
+            const long long tot = (long long)(us + ur) * ublk + tot2;
+            b = c * tot / G - (long long)(s_at(c) + r_at(c)) * ublk;
+        } else {
+            b = c * tot2 / G;
+        }
+        if (b >= tot2) return tot2;
+        const int off = (int)(b % wsum);
+        return b - ((off < ws ? off : (off - ws) % wi) & 1);
     }
 };
 
@@ -425,292 +452,285 @@ struct Item {
 // Columns of a stage: phase 2 keeps head and tail rows of every pair, and
 // above eight pairs they only fit with half the columns.
 __device__ __forceinline__ int chunk_cols(bool down, int count) {
-    return down && count > 8 ? kChunk / 2 : kChunk;
+    return down && count > 8 ? kBox : kChunk;
 }
-__device__ __forceinline__ int x_stride(bool down, int count) {
-    return down && count > 8 ? kXStrideHalf : kXStride;
+template <int DT>
+__device__ __forceinline__ int x_stride(int cols) {
+    return cols * 2 + Fmt<DT>::kPad;
+}
+template <int DT>
+__host__ __device__ constexpr int off_x() {
+    return 2 * kBoxBytes + Fmt<DT>::kScaleBytes;
 }
 
-template <int DT>
+// Row of its matrix that row r of the unit is: phase 1 alternates 8 gate rows
+// and the 8 up rows of the same features.
 __device__ __forceinline__ size_t weight_row(const Item& it, bool down, int H, int I, int r) {
     if (down) return (it.expert < 0 ? 0 : (size_t)it.expert * H) + it.first + r;
-    // 8 gate rows, then the 8 up rows of the same features, for each 16 rows
     const int f = it.first + (r >> 4) * 8 + (r & 7) + (r & 8 ? it.n : 0);
     return (it.expert < 0 ? 0 : (size_t)it.expert * 2 * I) + f;
 }
 
-// Producer, all lanes: the stage's weight rows (and MXFP4 scales).
+// Producer, all lanes: the stage's weights (one tensor copy for each 256
+// columns) and scales.
 template <int DT>
 __device__ void issue_weights(const FewArgs& a, const Item& it, bool down, const Ring& ring, uint64_t policy) {
     using F = Fmt<DT>;
     const int lane = threadIdx.x & 31;
-    const uint8_t* w = down ? (it.expert < 0 ? a.w2s : a.w2) : (it.expert < 0 ? a.w13s : a.w13);
-    const uint8_t* sc = static_cast<const uint8_t*>(down ? (it.expert < 0 ? a.s2s : a.s2)
-                                                         : (it.expert < 0 ? a.s13s : a.s13));
-    const uint32_t bar = moe::smem_addr(&ring.full[ring.slot]);
     const uint32_t dst = moe::smem_addr(ring.base + ring.slot * a.stage_bytes);
-    const uint32_t bytes = (uint32_t)it.kn * F::kBits / 8;
-    uint32_t total = F::kRows * bytes + (uint32_t)it.count * (down ? 2 : 1) * it.kn * 2;
-    if (F::kScaleStride) {
-        // a row's scales start at any multiple of 4 bytes: copy the 16-byte
-        // window around them (a matrix is a multiple of 128 rows, so the
-        // window never leaves it)
-        uint32_t len = 0;
-        for (int r = lane; r < F::kRows; r += 32) {
-            const size_t at = (weight_row<DT>(it, down, a.H, a.I, r) * it.K + it.k0) / 32;
-            len += (uint32_t)(((at + it.kn / 32 + 15) & ~(size_t)15) - (at & ~(size_t)15));
+    if (lane == 0) {
+        uint64_t* full = &ring.full[ring.slot];
+        const uint32_t bar = moe::smem_addr(full);
+        moe::mbar_arrive_expect_tx(full, it.kn > kBox ? 2 * kBoxBytes : kBoxBytes);
+        const int group = (int)(weight_row(it, down, a.H, a.I, 0) / 8);
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            if (b * kBox >= it.kn) break;
+            const int panel = (it.k0 + b * kBox) * F::kBits / 512;
+            if (down)
+                box_load_4d(dst + b * kBoxBytes, it.expert < 0 ? &a.m2s : &a.m2, bar, panel, group, policy);
+            else
+                box_load_5d(dst + b * kBoxBytes, it.expert < 0 ? &a.m13s : &a.m13, bar, panel, group, policy);
         }
-        total += __reduce_add_sync(0xffffffffu, len);
     }
-    if (lane == 0) moe::mbar_arrive_expect_tx(&ring.full[ring.slot], total);
     __syncwarp();
-    for (int r = lane; r < F::kRows; r += 32) {
-        const size_t at = weight_row<DT>(it, down, a.H, a.I, r) * it.K + it.k0;
-        bulk_load_hint(dst + r * F::kStride, w + at * F::kBits / 8, bytes, bar, policy);
-        if (F::kScaleStride) {
-            const size_t s0 = (at / 32) & ~(size_t)15, s1 = (at / 32 + it.kn / 32 + 15) & ~(size_t)15;
-            bulk_load(dst + F::kRows * F::kStride + r * F::kScaleStride, sc + s0, (uint32_t)(s1 - s0), bar);
+    const void* sc = down ? (it.expert < 0 ? a.s2s : a.s2) : (it.expert < 0 ? a.s13s : a.s13);
+    if (DT == MOE_DTYPE_FP8_E4M3_BLOCK128) {
+        // [gate, up][4 blocks of 128 columns]; phase 2 has one row block
+        if (lane < (down ? 4 : 8) && (lane & 3) * 128 < it.kn) {
+            const size_t row = weight_row(it, down, a.H, a.I, lane < 4 ? 0 : 8) / 128;
+            copy4(dst + 2 * kBoxBytes + lane * 4,
+                  static_cast<const float*>(sc) + row * (it.K / 128) + it.k0 / 128 + (lane & 3));
+        }
+    } else if (DT == MOE_DTYPE_MXFP4_BLOCK32) {
+        // 16 bytes a row; they start at a multiple of 16 when K / 32 is one
+        const uint8_t* s8 = static_cast<const uint8_t*>(sc);
+        if (it.K % 512 == 0 && it.kn == kChunk && it.k0 % 512 == 0) {
+#pragma unroll
+            for (int r = lane; r < F::kRows; r += 32)
+                copy16(dst + 2 * kBoxBytes + r * 16,
+                       s8 + (weight_row(it, down, a.H, a.I, r) * it.K + it.k0) / 32);
+        } else {
+#pragma unroll 4
+            for (int i = lane; i < F::kRows * 4; i += 32)
+                if ((i & 3) * 128 < it.kn)
+                    copy4(dst + 2 * kBoxBytes + i * 4,
+                          s8 + (weight_row(it, down, a.H, a.I, i >> 2) * it.K + it.k0) / 32 + (i & 3) * 4);
         }
     }
 }
 
-// Producer, all lanes: the activation rows of the stage in `slot`.
+// Producer, all lanes: the activation rows of the stage in `slot`, and the
+// lanes' arrival for it.
+template <int DT>
 __device__ void issue_acts(const FewArgs& a, bool down, uint32_t mask, int base, int count, int k0, int kn,
                            const Ring& ring, int slot) {
     const int lane = threadIdx.x & 31;
-    const uint32_t bar = moe::smem_addr(&ring.full[slot]);
-    const uint32_t dst = moe::smem_addr(ring.base + slot * a.stage_bytes + a.off_x);
+    const int xs = x_stride<DT>(chunk_cols(down, count));
+    uint32_t dst = moe::smem_addr(ring.base + slot * a.stage_bytes + off_x<DT>());
     if (down) {
-        if (lane < 2 * count) {
-            const int i = lane < count ? lane : lane - count;
-            const uint16_t* src = (lane < count ? a.act_hi : a.act_lo) + (size_t)(base + i) * a.ld_act + k0;
-            bulk_load(dst + lane * x_stride(true, count), src, kn * 2, bar);
+        for (int i = 0; i < 2 * count; ++i, dst += xs) {
+            const uint16_t* src = (i < count ? a.act_hi + (size_t)(base + i) * a.ld_act
+                                             : a.act_lo + (size_t)(base + i - count) * a.ld_act) + k0;
+            for (int c = lane * 8; c < kn; c += 256) copy16(dst + c * 2, src + c);
         }
-    } else if (mask >> lane & 1u) {
-        const int i = __popc(mask & ((1u << lane) - 1u));
-        bulk_load(dst + i * kXStride, a.x + (size_t)lane * a.H + k0, kn * 2, bar);
+    } else {
+        for (uint32_t m = mask; m; m &= m - 1, dst += xs) {
+            const uint16_t* src = a.x + (size_t)(__ffs(m) - 1) * a.H + k0;
+            for (int c = lane * 8; c < kn; c += 256) copy16(dst + c * 2, src + c);
+        }
     }
+    arrive_copied(&ring.full[slot]);
 }
 
 // ------------------------------------------------------------------ multiplication
-// bf16 pairs of the lane's 8 weights (k = 8 t .. 8 t + 7 of a 32-column
-// chunk), in the order the activations' words are put in by order_acts.
+// Weights become bf16 pairs whose order the activations' words follow: a
+// fragment of two registers, a[0] and a[1], pairs with two activation words.
+// (sign | magnitude bits) * 2^E, exact
+template <int E>
 __device__ __forceinline__ uint32_t merge_sign(uint32_t sign, uint32_t mag) {
-    return (sign & 0x80008000u) | mag;
-}
-template <int DT>
-struct Frag;
-template <>
-struct Frag<MOE_DTYPE_BF16> {
-    uint32_t r[4];
-    __device__ __forceinline__ void load(const uint8_t* row, int k) {
-        const uint4 v = *reinterpret_cast<const uint4*>(row + k * 2);
-        r[0] = v.x;
-        r[1] = v.y;
-        r[2] = v.z;
-        r[3] = v.w;
-    }
-    __device__ __forceinline__ uint32_t top() const { return 0; }
-};
-template <>
-struct Frag<MOE_DTYPE_FP8_E4M3_BLOCK128> {
-    uint32_t r[4], m[4];
-    // pairs (0, 2), (1, 3), (4, 6), (5, 7)
-    __device__ __forceinline__ void load(const uint8_t* row, int k) {
-        const uint2 v = *reinterpret_cast<const uint2*>(row + k);
-        const uint32_t c[2] = {v.x, v.y};
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            m[2 * i] = (c[i] << 4) & 0x07f007f0u;
-            m[2 * i + 1] = (c[i] >> 4) & 0x07f007f0u;
-            r[2 * i] = merge_sign(c[i] << 8, m[2 * i]);
-            r[2 * i + 1] = merge_sign(c[i], m[2 * i + 1]);
-        }
-    }
-    // the largest magnitude field: 0x7f0 is e4m3's NaN
-    __device__ __forceinline__ uint32_t top() const {
-        return __vmaxu2(__vmaxu2(m[0], m[1]), __vmaxu2(m[2], m[3]));
-    }
-};
-template <>
-struct Frag<MOE_DTYPE_MXFP4_BLOCK32> {
-    uint32_t r[4];
-    // pairs (0, 4), (1, 5), (2, 6), (3, 7)
-    __device__ __forceinline__ void load(const uint8_t* row, int k) {
-        const uint32_t v = *reinterpret_cast<const uint32_t*>(row + k / 2);
-        r[0] = merge_sign(v << 12, (v << 6) & 0x01c001c0u);
-        r[1] = merge_sign(v << 8, (v << 2) & 0x01c001c0u);
-        r[2] = merge_sign(v << 4, (v >> 2) & 0x01c001c0u);
-        r[3] = merge_sign(v, (v >> 6) & 0x01c001c0u);
-    }
-    __device__ __forceinline__ uint32_t top() const { return 0; }
-};
-
-template <int DT>
-__device__ __forceinline__ void order_acts(uint4& b) {
-    uint4 o;
-    if (DT == MOE_DTYPE_FP8_E4M3_BLOCK128) {
-        o.x = __byte_perm(b.x, b.y, 0x5410);
-        o.y = __byte_perm(b.x, b.y, 0x7632);
-        o.z = __byte_perm(b.z, b.w, 0x5410);
-        o.w = __byte_perm(b.z, b.w, 0x7632);
-        b = o;
-    } else if (DT == MOE_DTYPE_MXFP4_BLOCK32) {
-        o.x = __byte_perm(b.x, b.z, 0x5410);
-        o.y = __byte_perm(b.x, b.z, 0x7632);
-        o.z = __byte_perm(b.y, b.w, 0x5410);
-        o.w = __byte_perm(b.y, b.w, 0x7632);
-        b = o;
-    }
-}
-__device__ __forceinline__ uint32_t lift2(uint32_t v) {
-    const __nv_bfloat162 f = __floats2bfloat162_rn(kLift, kLift);
-    const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&v), f);
+    const uint32_t v = (sign & 0x80008000u) | mag;
+    constexpr uint32_t kFactor = (uint32_t)(E + 127) << 7 | (uint32_t)(E + 127) << 23;
+    const uint32_t f = kFactor;
+    const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&v),
+                                     *reinterpret_cast<const __nv_bfloat162*>(&f));
     return *reinterpret_cast<const uint32_t*>(&r);
 }
+// four e4m3 codes: pairs (0, 2) and (1, 3)
+__device__ __forceinline__ void widen_e4m3(uint32_t c, uint32_t& p0, uint32_t& p1, uint32_t& top) {
+    const uint32_t m0 = (c << 4) & 0x07f007f0u, m1 = (c >> 4) & 0x07f007f0u;
+    p0 = merge_sign<120>(c << 8, m0);
+    p1 = merge_sign<120>(c, m1);
+    top = __vmaxu2(top, __vmaxu2(m0, m1));   // 0x7f0 is e4m3's NaN
+}
+// eight e2m1 codes: pairs (0, 4), (1, 5), (2, 6), (3, 7)
+__device__ __forceinline__ void widen_e2m1(uint32_t v, uint32_t (&p)[4]) {
+    p[0] = merge_sign<126>(v << 12, (v << 6) & 0x01c001c0u);
+    p[1] = merge_sign<126>(v << 8, (v << 2) & 0x01c001c0u);
+    p[2] = merge_sign<126>(v << 4, (v >> 2) & 0x01c001c0u);
+    p[3] = merge_sign<126>(v, (v >> 6) & 0x01c001c0u);
+}
 
-// One warp's part of a stage: 16 rows by its K slice, for NT tiles of 8
-// columns.  xrow: the stage's activation row of this lane's column, or -1.
-// In phase 2 a column is a token, and only the expert's own tokens add the
-// stage's products: an infinity or a NaN among its weights reaches no other.
+// The lane's activations of its column for the warp's 64 columns of K, in
+// the weights' order.
+template <int DT>
+__device__ __forceinline__ void load_acts(const uint8_t* row, int t, uint32_t (&b)[8]) {
+    uint4 v[2];
+    if (DT == MOE_DTYPE_FP8_E4M3_BLOCK128) {
+        // lane t: columns 16 t .. 16 t + 15
+        v[0] = *reinterpret_cast<const uint4*>(row + t * 32);
+        v[1] = *reinterpret_cast<const uint4*>(row + t * 32 + 16);
+    } else {
+        // lane t: columns 8 t .. 8 t + 7 of each 32
+        v[0] = *reinterpret_cast<const uint4*>(row + t * 16);
+        v[1] = *reinterpret_cast<const uint4*>(row + 64 + t * 16);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint4 w = v[i];
+        uint32_t* o = b + 4 * i;
+        if (DT == MOE_DTYPE_BF16) {
+            o[0] = w.x;
+            o[1] = w.y;
+            o[2] = w.z;
+            o[3] = w.w;
+        } else if (DT == MOE_DTYPE_FP8_E4M3_BLOCK128) {
+            o[0] = __byte_perm(w.x, w.y, 0x5410);
+            o[1] = __byte_perm(w.x, w.y, 0x7632);
+            o[2] = __byte_perm(w.z, w.w, 0x5410);
+            o[3] = __byte_perm(w.z, w.w, 0x7632);
+        } else {
+            o[0] = __byte_perm(w.x, w.z, 0x5410);
+            o[1] = __byte_perm(w.x, w.z, 0x7632);
+            o[2] = __byte_perm(w.y, w.w, 0x5410);
+            o[3] = __byte_perm(w.y, w.w, 0x7632);
+        }
+    }
+}
+
+// One warp's part of a stage: all rows of the unit by its 64 columns of K, for
+// NT tiles of 8 tokens.  xrow: the stage's activation row of this lane's
+// column, or -1.  In phase 2 a column is a token, and only the expert's own
+// tokens add the stage's products: an infinity or a NaN among its weights
+// reaches no other.
 template <int DT, int NT, bool DOWN>
-__device__ __forceinline__ void mma_stage(const FewArgs& a, const Item& it, const uint8_t* stage, int mt, int kw,
-                                          const int (&xrow)[NT], bool tile1, const float (&fsc)[2][2],
-                                          float (&acc)[NT][4]) {
+__device__ __forceinline__ void mma_stage(const Item& it, const uint8_t* stage, int kw, const int (&xrow)[NT],
+                                          bool tile1, float (&acc)[Fmt<DT>::kRows / 16][NT][4]) {
     using F = Fmt<DT>;
-    constexpr int KW = kWarps / (F::kRows / 16);
+    constexpr int MT = F::kRows / 16;
+    constexpr int PB = kBox * F::kBits / 512;        // 64-byte pieces of a row in a box
+    if (kw * kSlice >= it.kn) return;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int per = (it.kn / KW + 31) & ~31;
-    const int klo = kw * per, khi = min(it.kn, klo + per);
-    const uint8_t* w0 = stage + (mt * 16 + g) * F::kStride;
-    const uint8_t* w1 = w0 + 8 * F::kStride;
-    const int xs = x_stride(DOWN, it.count);
-    const uint8_t* x = stage + a.off_x;
-    uint32_t top0 = 0, top1 = 0;
+    const int xs = x_stride<DT>(chunk_cols(DOWN, it.count));
+    const uint8_t* x = stage + off_x<DT>() + kw * kSlice * 2;
+    uint32_t b[NT][8], bl[NT][8];
     bool own[NT][2];
-    float part[NT][4];      // bf16: the stage's products
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         own[nt][0] = !DOWN || (it.mask >> (8 * nt + 2 * t) & 1u);
         own[nt][1] = !DOWN || (it.mask >> (8 * nt + 2 * t + 1) & 1u);
+        if (nt == 1 && !tile1) continue;
+        const uint8_t* xr = x + max(xrow[nt], 0) * xs;
+        load_acts<DT>(xr, t, b[nt]);
+        if (DOWN) load_acts<DT>(xr + it.count * xs, t, bl[nt]);
+    }
+    // this warp's columns in the boxes: first piece of 64 bytes
+    const int c0 = kw * kSlice;
+    const uint8_t* w = stage + (c0 / kBox) * kBoxBytes + (c0 % kBox) * F::kBits / 512 * 512 + g * 64;
+    const int sw = (g >> 1) & 3;                     // 64-byte swizzle of row g
+    const uint8_t* sc = stage + 2 * kBoxBytes;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) part[nt][j] = 0.0f;
-    }
-    // MXFP4 scale bytes of the lane's two rows, inside their 16-byte windows
-    const uint8_t *s0 = nullptr, *s1 = nullptr;
-    if (DT == MOE_DTYPE_MXFP4_BLOCK32) {
-        const uint8_t* sb = stage + F::kRows * F::kStride + (mt * 16 + g) * F::kScaleStride;
-        const uint32_t r0 = (uint32_t)weight_row<DT>(it, DOWN, a.H, a.I, mt * 16 + g);
-        const uint32_t r1 = (uint32_t)weight_row<DT>(it, DOWN, a.H, a.I, mt * 16 + g + 8);
-        s0 = sb + ((r0 * (uint32_t)(it.K / 32) + it.k0 / 32) & 15u);
-        s1 = sb + 8 * F::kScaleStride + ((r1 * (uint32_t)(it.K / 32) + it.k0 / 32) & 15u);
-    }
-#pragma unroll 2
-    for (int k = klo; k < khi; k += 32) {
-        Frag<DT> f0, f1;
-        f0.load(w0, k + 8 * t);
-        f1.load(w1, k + 8 * t);
-        const uint32_t m0[4] = {f0.r[0], f1.r[0], f0.r[1], f1.r[1]};
-        const uint32_t m1[4] = {f0.r[2], f1.r[2], f0.r[3], f1.r[3]};
-        float sc0 = 1.0f, sc1 = 1.0f;
-        if (DT == MOE_DTYPE_FP8_E4M3_BLOCK128) {
-            top0 = __vmaxu2(top0, f0.top());
-            top1 = __vmaxu2(top1, f1.top());
-            const bool second = (it.k0 + k) / 128 != (it.k0 + klo) / 128;
-            sc0 = second ? fsc[0][1] : fsc[0][0];
-            sc1 = second ? fsc[1][1] : fsc[1][0];
-        } else if (DT == MOE_DTYPE_MXFP4_BLOCK32) {
-            sc0 = e8m0(s0[k / 32]);
-            sc1 = e8m0(s1[k / 32]);
-        }
+    for (int mt = 0; mt < MT; ++mt) {
+        const uint8_t* w0 = w + (2 * mt) * PB * 512;
+        const uint8_t* w1 = w0 + PB * 512;
+        if (DT == MOE_DTYPE_BF16) {
+            float c[NT][4] = {};
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            if (nt == 1 && !tile1) continue;
-            const uint8_t* xr = x + max(xrow[nt], 0) * xs + (k + 8 * t) * 2;
-            uint4 b = *reinterpret_cast<const uint4*>(xr);
-            uint4 lo = make_uint4(0, 0, 0, 0);
-            if (DOWN) {
-                lo = *reinterpret_cast<const uint4*>(xr + it.count * xs);
-                if (xrow[nt] < 0) b = lo = make_uint4(0, 0, 0, 0);
-            }
-            order_acts<DT>(b);
-            if (DOWN) order_acts<DT>(lo);
-            if (DT == MOE_DTYPE_BF16) {
-                mma_bf16(part[nt], m0, b.x, b.y);
-                mma_bf16(part[nt], m1, b.z, b.w);
-                if (DOWN) {
-                    mma_bf16(part[nt], m0, lo.x, lo.y);
-                    mma_bf16(part[nt], m1, lo.z, lo.w);
-                }
-            } else {
-                if (!DOWN) b = make_uint4(lift2(b.x), lift2(b.y), lift2(b.z), lift2(b.w));
-                float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                mma_bf16(c, m0, b.x, b.y);
-                mma_bf16(c, m1, b.z, b.w);
-                if (DOWN) {
-                    mma_bf16(c, m0, lo.x, lo.y);
-                    mma_bf16(c, m1, lo.z, lo.w);
-                }
-                constexpr float kBack = DT == MOE_DTYPE_MXFP4_BLOCK32 ? 0x1p62f : 0x1p56f;
-                if (own[nt][0]) {
-                    acc[nt][0] = fmaf(c[0] * kBack, sc0, acc[nt][0]);
-                    acc[nt][2] = fmaf(c[2] * kBack, sc1, acc[nt][2]);
-                }
-                if (own[nt][1]) {
-                    acc[nt][1] = fmaf(c[1] * kBack, sc0, acc[nt][1]);
-                    acc[nt][3] = fmaf(c[3] * kBack, sc1, acc[nt][3]);
-                }
-            }
-        }
-    }
-    if (DT == MOE_DTYPE_BF16) {
+            for (int h = 0; h < 2; ++h) {
+                const uint4 p = *reinterpret_cast<const uint4*>(w0 + h * 512 + ((t ^ sw) << 4));
+                const uint4 q = *reinterpret_cast<const uint4*>(w1 + h * 512 + ((t ^ sw) << 4));
+                const uint32_t m0[4] = {p.x, q.x, p.y, q.y}, m1[4] = {p.z, q.z, p.w, q.w};
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            if (own[nt][0]) {
-                acc[nt][0] += part[nt][0];
-                acc[nt][2] += part[nt][2];
+                for (int nt = 0; nt < NT; ++nt) {
+                    if (nt == 1 && !tile1) continue;
+                    mma_bf16(c[nt], m0, b[nt][4 * h], b[nt][4 * h + 1]);
+                    mma_bf16(c[nt], m1, b[nt][4 * h + 2], b[nt][4 * h + 3]);
+                    if (DOWN) {
+                        mma_bf16(c[nt], m0, bl[nt][4 * h], bl[nt][4 * h + 1]);
+                        mma_bf16(c[nt], m1, bl[nt][4 * h + 2], bl[nt][4 * h + 3]);
+                    }
+                }
             }
-            if (own[nt][1]) {
-                acc[nt][1] += part[nt][1];
-                acc[nt][3] += part[nt][3];
-            }
-        }
-    }
-    if (DT == MOE_DTYPE_FP8_E4M3_BLOCK128) {
-        // a NaN code anywhere in a row makes its sums NaN
-        const uint32_t n0 = __vcmpeq2(top0, 0x07f007f0u), n1 = __vcmpeq2(top1, 0x07f007f0u);
-        if (__any_sync(0xffffffffu, n0 | n1)) {
-            const float nan = __int_as_float(0x7fc00000);
-            const bool r0 = __ballot_sync(0xffffffffu, n0 != 0) >> (lane & 28) & 15u;
-            const bool r1 = __ballot_sync(0xffffffffu, n1 != 0) >> (lane & 28) & 15u;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    if (own[nt][j]) {
-                        if (r0) acc[nt][j] = nan;
-                        if (r1) acc[nt][j + 2] = nan;
-                    }
-        }
-    }
-}
-
-// FP8 block scales of a warp's rows and K slice (at most two 128-column
-// blocks), fetched before the stage's data is waited for.
-template <int DT>
-__device__ __forceinline__ void fetch_scales(const FewArgs& a, const Item& it, bool down, int mt, int kw,
-                                             float (&fsc)[2][2]) {
-    if (DT != MOE_DTYPE_FP8_E4M3_BLOCK128) return;
-    constexpr int KW = kWarps / (Fmt<DT>::kRows / 16);
-    const float* s = static_cast<const float*>(down ? (it.expert < 0 ? a.s2s : a.s2)
-                                                    : (it.expert < 0 ? a.s13s : a.s13));
-    const int nb = it.K / 128, per = (it.kn / KW + 31) & ~31;
-    const int b0 = min((it.k0 + kw * per) / 128, nb - 1), b1 = min(b0 + 1, nb - 1);
+                for (int j = 0; j < 4; ++j)
+                    if (own[nt][j & 1]) acc[mt][nt][j] += c[nt][j];
+        } else if (DT == MOE_DTYPE_FP8_E4M3_BLOCK128) {
+            const uint4 p = *reinterpret_cast<const uint4*>(w0 + ((t ^ sw) << 4));
+            const uint4 q = *reinterpret_cast<const uint4*>(w1 + ((t ^ sw) << 4));
+            const uint32_t pc[4] = {p.x, p.y, p.z, p.w}, qc[4] = {q.x, q.y, q.z, q.w};
+            const float* fs = reinterpret_cast<const float*>(sc) + c0 / 128;
+            const float s0 = fs[0], s1 = DOWN ? s0 : fs[4];
+            uint32_t top0 = 0, top1 = 0;
+            float c[NT][4] = {};
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const size_t row = weight_row<DT>(it, down, a.H, a.I, mt * 16 + 8 * i) / 128;
-        fsc[i][0] = __ldg(s + row * nb + b0);
-        fsc[i][1] = __ldg(s + row * nb + b1);
+            for (int i = 0; i < 4; ++i) {
+                uint32_t m[4];
+                widen_e4m3(pc[i], m[0], m[2], top0);
+                widen_e4m3(qc[i], m[1], m[3], top1);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    if (nt == 1 && !tile1) continue;
+                    mma_bf16(c[nt], m, b[nt][2 * i], b[nt][2 * i + 1]);
+                    if (DOWN) mma_bf16(c[nt], m, bl[nt][2 * i], bl[nt][2 * i + 1]);
+                }
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (own[nt][j & 1]) acc[mt][nt][j] = fmaf(c[nt][j], j < 2 ? s0 : s1, acc[mt][nt][j]);
+            // a NaN code anywhere in a row makes its sums NaN
+            const uint32_t n0 = __vcmpeq2(top0, 0x07f007f0u), n1 = __vcmpeq2(top1, 0x07f007f0u);
+            if (__any_sync(0xffffffffu, n0 | n1)) {
+                const bool r0 = __ballot_sync(0xffffffffu, n0 != 0) >> (lane & 28) & 15u;
+                const bool r1 = __ballot_sync(0xffffffffu, n1 != 0) >> (lane & 28) & 15u;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (own[nt][j & 1] && (j < 2 ? r0 : r1)) acc[mt][nt][j] = __int_as_float(0x7fc00000);
+            }
+        } else {
+            const uint8_t* sr = sc + (mt * 16 + g) * 16 + kw * 2;
+            const uint32_t e0 = *reinterpret_cast<const uint16_t*>(sr);
+            const uint32_t e1 = *reinterpret_cast<const uint16_t*>(sr + 128);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                // 16-byte piece of the 32-column block, a word a lane
+                const int off = ((((c0 >> 5) + h & 3) ^ sw) << 4) + t * 4;
+                uint32_t p[4], q[4];
+                widen_e2m1(*reinterpret_cast<const uint32_t*>(w0 + off), p);
+                widen_e2m1(*reinterpret_cast<const uint32_t*>(w1 + off), q);
+                const uint32_t m0[4] = {p[0], q[0], p[1], q[1]}, m1[4] = {p[2], q[2], p[3], q[3]};
+                const float s0 = e8m0(e0 >> (8 * h) & 255u), s1 = e8m0(e1 >> (8 * h) & 255u);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    if (nt == 1 && !tile1) continue;
+                    float c[4] = {};
+                    mma_bf16(c, m0, b[nt][4 * h], b[nt][4 * h + 1]);
+                    mma_bf16(c, m1, b[nt][4 * h + 2], b[nt][4 * h + 3]);
+                    if (DOWN) {
+                        mma_bf16(c, m0, bl[nt][4 * h], bl[nt][4 * h + 1]);
+                        mma_bf16(c, m1, bl[nt][4 * h + 2], bl[nt][4 * h + 3]);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (own[nt][j & 1]) acc[mt][nt][j] = fmaf(c[j], j < 2 ? s0 : s1, acc[mt][nt][j]);
+                }
+            }
+        }
     }
 }
 
@@ -718,18 +738,18 @@ __device__ __forceinline__ void fetch_scales(const FewArgs& a, const Item& it, b
 template <int DT, int NT>
 __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant__ FewArgs a) {
     using F = Fmt<DT>;
-    constexpr int R = F::kRows, MT = R / 16, KW = kWarps / MT, NF = R / 2;
-    extern __shared__ __align__(128) uint8_t smem[];
+    constexpr int R = F::kRows, MT = R / 16, NF = R / 2;
+    extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ uint64_t full[kMaxStages], empty[kMaxStages], plan_ready;
-    __shared__ float4 red[2][kWarps][NT][32];
     __shared__ int n_active_sh, abort_sh, last_sh;
+    float4(*red)[MT][NT][32] = reinterpret_cast<float4(*)[MT][NT][32]>(smem + a.off_red);   // [warp]
     volatile int* abort_flag = &abort_sh;
     Plan P{reinterpret_cast<Active*>(smem + a.off_active), reinterpret_cast<float*>(smem + a.off_pairw),
            &n_active_sh};
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < a.n_stages; ++i) {
-            moe::mbar_init(&full[i], 1);        // the producer's arrive with the stage's bytes
+            moe::mbar_init(&full[i], 33);       // the weights' bytes, and the producer lanes' copies
             moe::mbar_init(&empty[i], kWarps);  // one arrive per consumer warp
         }
         moe::mbar_init(&plan_ready, 1);
@@ -743,16 +763,16 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
     const Active shared{-1, (1u << a.T) - 1u, 0, a.T};
     const int first_routed = a.Is ? 1 : 0;
 
-    if (warp >= kWarps && warp < 2 * kWarps) {
+    if (warp >= kWarps && warp < kWarps + kRouters) {
         // ---------------------------------------------------------- router
         const int tid = threadIdx.x - kGroup, rw = warp - kWarps;
         Scratch S;
         S.keys = reinterpret_cast<double*>(smem + a.off_scratch);
-        S.sel = reinterpret_cast<int*>(S.keys + (size_t)min(a.T, kWarps) * a.E);
+        S.sel = reinterpret_cast<int*>(S.keys + (size_t)min(a.T, kRouters) * a.E);
         S.selw = reinterpret_cast<float*>(S.sel + a.T * a.k);
         S.emask = reinterpret_cast<uint32_t*>(S.selw + a.T * a.k);
         S.apos = reinterpret_cast<int*>(S.emask + a.E);
-        for (int i = cta * kGroup + tid; i < a.H / R; i += gridDim.x * kGroup) a.joined[i] = 0;
+        for (int i = cta * kRouterGroup + tid; i < a.H / R; i += gridDim.x * kRouterGroup) a.joined[i] = 0;
         router_phase(a, rw);
         __threadfence();
         group_any(2, false);
@@ -771,13 +791,13 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
             __threadfence();
         }
         if (!group_any(2, !ok)) {
-            for (int t = rw; t < a.T; t += kWarps) choose(a, t, S.keys + (size_t)rw * a.E, S);
+            for (int t = rw; t < a.T; t += kRouters) choose(a, t, S.keys + (size_t)rw * a.E, S);
             group_any(2, false);
             build_plan(a, P, S, tid);
             group_any(2, false);
             if (tid == 0) moe::mbar_arrive(&plan_ready);
         }
-    } else if (warp == 2 * kWarps) {
+    } else if (warp == kWarps + kRouters) {
         // ---------------------------------------------------------- producer
         const uint64_t policy = moe::l2_policy_evict_first();
         bool ok = true;
@@ -797,7 +817,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
                 it.kn = min(kChunk, a.H - it.k0);
                 if (!claim()) return;
                 issue_weights<DT>(a, it, false, ring, policy);
-                issue_acts(a, false, it.mask, 0, it.count, it.k0, it.kn, ring, ring.slot);
+                issue_acts<DT>(a, false, it.mask, 0, it.count, it.k0, it.kn, ring, ring.slot);
                 mark();
                 ring.next();
             }
@@ -815,10 +835,9 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
             bool open = false;                 // barrier 1 has been passed
             int lack = 0, l_base = 0, l_count = 0, l_k0 = 0, l_kn = 0;
             auto supply = [&]() {
-                fence_proxy_async();           // the heads and tails are other blocks' plain stores
                 for (uint32_t m = __ballot_sync(0xffffffffu, lack); m; m &= m - 1) {
                     const int sl = __ffs(m) - 1;
-                    issue_acts(a, true, 0, __shfl_sync(0xffffffffu, l_base, sl),
+                    issue_acts<DT>(a, true, 0, __shfl_sync(0xffffffffu, l_base, sl),
                                __shfl_sync(0xffffffffu, l_count, sl), __shfl_sync(0xffffffffu, l_k0, sl),
                                __shfl_sync(0xffffffffu, l_kn, sl), ring, sl);
                 }
@@ -828,9 +847,10 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
                 int n = 0;
                 if (lane == 0) {
                     n = *reinterpret_cast<volatile int*>(bars + 1);
-                    __threadfence();
                 }
-                return __shfl_sync(0xffffffffu, n, 0) >= (int)gridDim.x;
+                n = __shfl_sync(0xffffffffu, n, 0);
+                __threadfence();               // heads and tails are read after the count
+                return n >= (int)gridDim.x;
             };
             long long pos = sh.b_at(cta);
             const long long end = sh.b_at(cta + 1);
@@ -874,7 +894,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
                 issue_weights<DT>(a, it, true, ring, policy);
                 mark();
                 if (open) {
-                    issue_acts(a, true, 0, it.base, it.count, it.k0, it.kn, ring, ring.slot);
+                    issue_acts<DT>(a, true, 0, it.base, it.count, it.k0, it.kn, ring, ring.slot);
                 } else if (lane == ring.slot) {
                     lack = 1;
                     l_base = it.base;
@@ -906,28 +926,26 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
                 if (issued >> i & 1u) moe::wait_bar(&full[i], last_phase >> i & 1u, abort_flag, a.status, true);
     } else {
         // ---------------------------------------------------------- consumers
-        const int mt = warp / KW, kw = warp % KW, tid = threadIdx.x;
+        const int tid = threadIdx.x;
         const int g = lane >> 2, t = lane & 3;
-        int buf = 0;
         bool ok = true;
-        float acc[NT][4];
+        float acc[MT][NT][4];
         auto clear = [&]() {
 #pragma unroll
-            for (int i = 0; i < NT; ++i)
+            for (int m = 0; m < MT; ++m)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
+                for (int i = 0; i < NT; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) acc[m][i][j] = 0.0f;
         };
         // one stage; false when the wait was given up
         auto stage_gate_up = [&](const Item& it) {
             int xrow[NT];
 #pragma unroll
             for (int i = 0; i < NT; ++i) xrow[i] = 8 * i + g < it.count ? 8 * i + g : 0;
-            float fsc[2][2] = {};
-            fetch_scales<DT>(a, it, false, mt, kw, fsc);
             ok = __all_sync(0xffffffffu, moe::wait_bar(&full[ring.slot], ring.phase, abort_flag, a.status));
             if (!ok) return;
-            mma_stage<DT, NT, false>(a, it, ring.base + ring.slot * a.stage_bytes, mt, kw, xrow, it.count > 8, fsc,
-                                     acc);
+            mma_stage<DT, NT, false>(it, ring.base + ring.slot * a.stage_bytes, warp, xrow, it.count > 8, acc);
             __syncwarp();
             if (lane == 0) moe::mbar_arrive(&empty[ring.slot]);
             ring.next();
@@ -939,32 +957,32 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
                 const int tok = 8 * i + g;
                 xrow[i] = it.mask >> tok & 1u ? __popc(it.mask & ((1u << tok) - 1u)) : -1;
             }
-            float fsc[2][2] = {};
-            fetch_scales<DT>(a, it, true, mt, kw, fsc);
             ok = __all_sync(0xffffffffu, moe::wait_bar(&full[ring.slot], ring.phase, abort_flag, a.status));
             if (!ok) return;
-            mma_stage<DT, NT, true>(a, it, ring.base + ring.slot * a.stage_bytes, mt, kw, xrow, it.mask >> 8, fsc,
-                                    acc);
+            mma_stage<DT, NT, true>(it, ring.base + ring.slot * a.stage_bytes, warp, xrow, it.mask >> 8, acc);
             __syncwarp();
             if (lane == 0) moe::mbar_arrive(&empty[ring.slot]);
             ring.next();
         };
-        // Leaves the warps' sums in red[buf] and waits for all of them; true
-        // when any warp has given up.
+        // Leaves the warps' sums in red (once the last ones have been read)
+        // and waits for all of them; true when any warp has given up.
         auto gather = [&]() {
+            group_any(1, false);
 #pragma unroll
-            for (int i = 0; i < NT; ++i)
-                red[buf][warp][i][lane] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int i = 0; i < NT; ++i)
+                    red[warp][m][i][lane] = make_float4(acc[m][i][0], acc[m][i][1], acc[m][i][2], acc[m][i][3]);
             return group_any(1, !ok);
         };
-        // Sum over the K slices: thread tid takes row group tid / (32 NT),
-        // column tile (tid / 32) % NT.
+        // Sum over the K slices, in their order: thread tid takes row tile
+        // tid / (32 NT), column tile (tid / 32) % NT.
         auto reduced = [&]() {
             const int m = tid / (32 * NT), i = tid / 32 % NT;
-            float4 s = red[buf][m * KW][i][lane];
+            float4 s = red[0][m][i][lane];
 #pragma unroll
-            for (int q = 1; q < KW; ++q) {
-                const float4 v = red[buf][m * KW + q][i][lane];
+            for (int q = 1; q < kWarps; ++q) {
+                const float4 v = red[q][m][i][lane];
                 s.x += v.x;
                 s.y += v.y;
                 s.z += v.z;
@@ -990,7 +1008,6 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
                     const int pair = act.base + c0 + j;
                     float v = gate[j] / (1.0f + expf(-gate[j])) * up[j];
                     if (act.expert >= 0) v *= P.pairw[pair];
-                    if (DT != MOE_DTYPE_BF16) v *= kLift;
                     // head and tail: together 16 significand bits
                     const __nv_bfloat16 hi = __float2bfloat16_rn(v);
                     const __nv_bfloat16 lo = __float2bfloat16_rn(v - __bfloat162float(hi));
@@ -999,7 +1016,6 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
                     a.act_lo[at] = *reinterpret_cast<const uint16_t*>(&lo);
                 }
             }
-            buf ^= 1;
             return true;
         };
 
@@ -1019,7 +1035,6 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
         if (good) {
             // barrier 1: this block's heads and tails are written
             __threadfence();
-            fence_proxy_async();
             group_any(1, false);
             if (tid == 0) atomicAdd(bars + 1, 1);
             long long pos = sh.b_at(cta);
@@ -1065,7 +1080,6 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
                         }
                     }
                 }
-                buf ^= 1;
                 if (whole) continue;
                 // a row block of several blocks: the last to leave its part
                 // adds them up in block order
@@ -1121,7 +1135,7 @@ struct FewLayout {
 FewLayout few_layout(const moe_config_t* c) {
     FewLayout L{};
     const int nch = c->H / 256 > 0 ? c->H / 256 : 1;
-    int split = 148 * kWarps / c->E;
+    int split = 148 * kRouters / c->E;
     split = split < 1 ? 1 : split > nch ? nch : split;
     L.n_split = split;
     const int Is = c->n_shared * c->I;
@@ -1170,8 +1184,43 @@ moe_status_t few_check(const moe_config_t* c) {
     return MOE_OK;
 }
 
-// Shared memory: plan, router scratch, then as many stages as fit.
+// Tensor maps of a matrix stored in bytes, rows of `rb` bytes.  The inner
+// dimension is a 64-byte piece of a row, then 8 rows, then the pieces along K
+// (zero beyond the row's end), so that a box lands as 512-byte groups of 8
+// rows in the 64-byte swizzle.
+//   down:    {64, 8, rb / 64, rows / 8},            box {64, 8, PB, R / 8}
+//   gate/up: {64, 8, rb / 64, 2, row groups},       box {64, 8, PB, 2, R / 16}
+// where the fourth dimension steps from a gate row to its up row.
 template <int DT>
+moe_status_t few_maps(FewArgs& a, const void* w13, const void* w2, const void* w13s, const void* w2s) {
+    using F = Fmt<DT>;
+    const uint32_t pb = kBox * F::kBits / 512;
+    auto gate_up = [&](CUtensorMap* m, const void* p, uint64_t experts, uint64_t n, const char* what) {
+        const uint64_t rb = (uint64_t)a.H * F::kBits / 8;
+        const uint64_t dims[5] = {64, 8, rb / 64, 2, (experts * 2 - 1) * n / 8};
+        const uint64_t strides[4] = {rb, 64, n * rb, 8 * rb};
+        const uint32_t box[5] = {64, 8, pb, 2, F::kRows / 16};
+        return moe::api_make_map_u8_sw64(m, p, 5, dims, strides, box, what);
+    };
+    auto down = [&](CUtensorMap* m, const void* p, uint64_t experts, uint64_t n, const char* what) {
+        const uint64_t rb = n * F::kBits / 8;
+        const uint64_t dims[4] = {64, 8, rb / 64, experts * a.H / 8};
+        const uint64_t strides[3] = {rb, 64, 8 * rb};
+        const uint32_t box[4] = {64, 8, pb, F::kRows / 8};
+        return moe::api_make_map_u8_sw64(m, p, 4, dims, strides, box, what);
+    };
+    FEW_TRY(gate_up(&a.m13, w13, a.E, a.I, "w13"));
+    FEW_TRY(down(&a.m2, w2, a.E, a.I, "w2"));
+    if (a.Is) {
+        FEW_TRY(gate_up(&a.m13s, w13s, 1, a.Is, "w13s"));
+        FEW_TRY(down(&a.m2s, w2s, 1, a.Is, "w2s"));
+    }
+    return MOE_OK;
+}
+
+// Shared memory: plan, router scratch, the consumers' sums, then as many
+// stages as fit.
+template <int DT, int NT>
 moe_status_t few_smem(FewArgs& a, int limit, size_t* bytes) {
     using F = Fmt<DT>;
     auto up = [](int v, int to) { return (v + to - 1) / to * to; };
@@ -1182,11 +1231,13 @@ moe_status_t few_smem(FewArgs& a, int limit, size_t* bytes) {
     a.off_pairw = off;
     off = up(off + (n + a.T) * 4, 16);
     a.off_scratch = off;
-    off += (a.T < kWarps ? a.T : kWarps) * a.E * 8 + n * 8 + a.E * 8;
-    a.off_ring = up(off, 128);
-    a.off_x = F::kRows * (F::kStride + F::kScaleStride);
-    const int x = a.T <= 8 ? 2 * a.T * kXStride : 2 * kT * kXStrideHalf;
-    a.stage_bytes = up(a.off_x + x, 128);
+    off = up(off + (a.T < kRouters ? a.T : kRouters) * a.E * 8 + n * 8 + a.E * 8, 16);
+    a.off_red = off;
+    off += kWarps * (F::kRows / 16) * NT * 512;
+    a.off_ring = up(off, 1024);
+    const int full = kChunk * 2 + F::kPad, half = kBox * 2 + F::kPad;
+    const int x = NT == 1 ? 2 * a.T * full : (16 * full > 2 * kT * half ? 16 * full : 2 * kT * half);
+    a.stage_bytes = up(off_x<DT>() + x, 512);
     const int stages = (limit - a.off_ring) / a.stage_bytes;
     a.n_stages = stages < kMaxStages ? stages : kMaxStages;
     if (a.n_stages < 2)
@@ -1206,7 +1257,7 @@ moe_status_t launch_few(FewArgs& a, cudaStream_t s) {
     if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, few_kernel<DT, NT>);
     if (e == cudaSuccess) {
         size_t smem = 0;
-        FEW_TRY(few_smem<DT>(a, optin - (int)fa.sharedSizeBytes, &smem));
+        FEW_TRY((few_smem<DT, NT>(a, optin - (int)fa.sharedSizeBytes, &smem)));
         e = cudaFuncSetAttribute(few_kernel<DT, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e == cudaSuccess) {
             void* args[] = {&a};
@@ -1219,7 +1270,9 @@ moe_status_t launch_few(FewArgs& a, cudaStream_t s) {
 }
 
 template <int DT>
-moe_status_t launch_tiles(FewArgs& a, cudaStream_t s) {
+moe_status_t launch_tiles(FewArgs& a, const void* w13, const void* w2, const void* w13s, const void* w2s,
+                          cudaStream_t s) {
+    FEW_TRY(few_maps<DT>(a, w13, w2, w13s, w2s));
     return a.T <= 8 ? launch_few<DT, 1>(a, s) : launch_few<DT, 2>(a, s);
 }
 
@@ -1271,14 +1324,11 @@ moe_status_t moe_forward_few(const moe_config_t* cfg, const void* x, const void*
     const FewLayout L = few_layout(cfg);
     if (ws_bytes < L.total)
         return ffail(MOE_ERR_WORKSPACE, "workspace has too few bytes, %s %lld", "needs", (long long)L.total);
-    FewArgs a = {};
+    FewArgs a;
+    memset(&a, 0, sizeof(a));
     a.x = static_cast<const uint16_t*>(x);
     a.w_router = static_cast<const uint16_t*>(w_router);
     a.bias = bias;
-    a.w13 = static_cast<const uint8_t*>(w13);
-    a.w2 = static_cast<const uint8_t*>(w2);
-    a.w13s = static_cast<const uint8_t*>(w13s);
-    a.w2s = static_cast<const uint8_t*>(w2s);
     a.s13 = w13_scale;
     a.s2 = w2_scale;
     a.s13s = w13s_scale;
@@ -1309,9 +1359,9 @@ moe_status_t moe_forward_few(const moe_config_t* cfg, const void* x, const void*
     a.stall = cfg->flags & MOE_FLAG_TEST_STALL ? 1 : 0;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     switch (cfg->dtype) {
-        case MOE_DTYPE_BF16: return launch_tiles<MOE_DTYPE_BF16>(a, s);
-        case MOE_DTYPE_FP8_E4M3_BLOCK128: return launch_tiles<MOE_DTYPE_FP8_E4M3_BLOCK128>(a, s);
-        default: return launch_tiles<MOE_DTYPE_MXFP4_BLOCK32>(a, s);
+        case MOE_DTYPE_BF16: return launch_tiles<MOE_DTYPE_BF16>(a, w13, w2, w13s, w2s, s);
+        case MOE_DTYPE_FP8_E4M3_BLOCK128: return launch_tiles<MOE_DTYPE_FP8_E4M3_BLOCK128>(a, w13, w2, w13s, w2s, s);
+        default: return launch_tiles<MOE_DTYPE_MXFP4_BLOCK32>(a, w13, w2, w13s, w2s, s);
     }
 }
 
