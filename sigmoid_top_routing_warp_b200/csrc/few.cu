@@ -7,9 +7,10 @@
 // one block per SM, each block walking its share of the weight rows through a
 // shared-memory ring while the multiplications keep up behind it.
 //
-// Roles in a block (13 warps):
-//   warp 12     producer: bulk copies of weight rows and of the activations
-//               they meet, stage by stage, as far ahead as the ring is deep
+// Roles in a block (16 warps):
+//   warp 12     weight producer: tensor copies of the weights (and scales),
+//               stage by stage, as far ahead as the ring is deep
+//   warps 13-15 activation producers: the rows that the weights meet
 //   warps 0-7   consumers: m16n8k16 matrix instructions, 16 weight rows by 8
 //               tokens; the tokens are the short side, so the 128-row tiles
 //               of tcgen05 would be coarse units to share out over 148 SMs
@@ -29,8 +30,7 @@
 //   2   the output rows' sum over all (expert, k) as one long K axis, shared
 //       out evenly to 128 columns; a row block that two or more blocks share
 //       is joined by the last of them, in block order
-// The producer issues phase 2's weight copies without waiting for barrier 1;
-// only the copies of the activations wait for it.
+// The weight producer does not wait for barrier 1; only the activations do.
 //
 // 8- and 4-bit weights become bf16 by moving their bits into a bf16's sign,
 // exponent and mantissa fields (e4m3 as value * 2^-120, e2m1 as value *
@@ -62,8 +62,11 @@ namespace {
 constexpr int kT = MOE_FEW_MAX_T;
 constexpr int kWarps = 8;                        // consumers
 constexpr int kRouters = 4;
+constexpr int kFeeders = 3;                      // warps that copy activations
 constexpr int kGroup = kWarps * 32, kRouterGroup = kRouters * 32;
-constexpr int kThreads = kGroup + kRouterGroup + 32;
+constexpr int kThreads = kGroup + kRouterGroup + 32 + kFeeders * 32;
+constexpr int kRouterVecs = 4;                   // 16-byte vectors of a router lane
+constexpr int kMaxBlocks = 256;                  // blocks the join buffer has room for
 constexpr int kChunk = 512;                      // K columns of a full stage
 constexpr int kBox = 256;                        // K columns of one tensor copy
 constexpr int kBoxBytes = 8192;                  // its bytes, for every weight type
@@ -108,7 +111,7 @@ struct FewArgs {
     int T, H, E, k, I, Is, n_group, topk_group, group_topn, norm, n_split, stall, ld_act;
     float rsf;
     // shared-memory layout (bytes)
-    int off_active, off_pairw, off_scratch, off_red, off_ring, stage_bytes, n_stages;
+    int off_active, off_pairw, off_cuts, off_scratch, off_red, off_ring, stage_bytes, n_stages;
 };
 
 // One touched expert: its tokens (bit mask), their number and its first
@@ -123,12 +126,14 @@ struct Active {
 struct Plan {
     Active* active;
     float* pairw;      // routing weight of a pair
+    int *cut1, *cut2;  // [blocks + 1] shares of the routed units and of phase 2
     int* n_active;
 };
 
 // Scratch of the router warps; the consumers' reduction buffer is apart.
 struct Scratch {
-    double* keys;      // [min(T, kRouters)][E]
+    unsigned long long* keys;   // [min(T, kRouters)][E]
+    double* scores;    // the same
     int* sel;          // [T, k]
     float* selw;       // [T, k]
     uint32_t* emask;   // [E] tokens of each expert
@@ -188,8 +193,7 @@ __device__ __forceinline__ void arrive_copied(uint64_t* bar) {
 }
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9},"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9},"
         " {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -200,124 +204,151 @@ __device__ __forceinline__ float e8m0(uint32_t s) {
     return __uint_as_float(s == 0u ? 0x00400000u : s == 255u ? 0x7fc00000u : s << 23);
 }
 
-// (key, index) order of the choice: larger key first, then lower index.
-__device__ __forceinline__ bool better(double a, int ia, double b, int ib) {
-    return a > b || (a == b && ia < ib);
-}
-__device__ __forceinline__ void warp_best(double& v, int& i) {
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-        const double ov = __shfl_xor_sync(0xffffffffu, v, off);
-        const int oi = __shfl_xor_sync(0xffffffffu, i, off);
-        if (better(ov, oi, v, i)) {
-            v = ov;
-            i = oi;
-        }
-    }
-}
-
-// Phase R: logits of expert e over one K slice, one warp each.  Eight exact
-// products are summed in binary32, those sums in binary64: the logit's error
-// stays near 2^-25 of a partial sum, far below the gap of two keys.
+// ------------------------------------------------------------------ router
+// Logits of expert e over one K slice, one warp each (router and consumer
+// warps).  Eight exact products are summed in binary32, those sums in
+// binary64: the logit's error stays near 2^-25 of a partial sum, far below the
+// gap of two keys.  A lane keeps its weights of the slice in registers and
+// walks the tokens.
 __device__ void router_phase(const FewArgs& a, int warp) {
     const int lane = threadIdx.x & 31;
     const int nch = a.H / 8;
-    const int per = (nch + a.n_split - 1) / a.n_split;
+    const int per = (nch + a.n_split - 1) / a.n_split;    // at most 32 * kRouterVecs
     const int units = a.E * a.n_split;
-    for (int u = blockIdx.x * kRouters + warp; u < units; u += gridDim.x * kRouters) {
+    for (int u = blockIdx.x * (kWarps + kRouters) + warp; u < units; u += gridDim.x * (kWarps + kRouters)) {
         const int e = u / a.n_split, sp = u % a.n_split;
-        const int c1 = min(nch, (sp + 1) * per);
+        const int c0 = sp * per + lane, c1 = min(nch, (sp + 1) * per);
         const uint4* wr = reinterpret_cast<const uint4*>(a.w_router + (size_t)e * a.H);
-        for (int t = 0; t < a.T; ++t) {
-            const uint4* xr = reinterpret_cast<const uint4*>(a.x + (size_t)t * a.H);
-            double acc = 0.0;
-#pragma unroll 4
-            for (int c = sp * per + lane; c < c1; c += 32) {
-                float w[8], x[8], s = 0.0f;
-                unpack8(__ldg(wr + c), w);
-                unpack8(__ldg(xr + c), x);
+        const uint4* xr = reinterpret_cast<const uint4*>(a.x);
+        uint4 w[kRouterVecs];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) s = fmaf(w[j], x[j], s);
+        for (int i = 0; i < kRouterVecs; ++i)
+            w[i] = c0 + 32 * i < c1 ? __ldg(wr + c0 + 32 * i) : make_uint4(0, 0, 0, 0);
+        double* out = a.part + (size_t)sp * a.T * a.E + e;
+#pragma unroll 2
+        for (int t = 0; t < a.T; ++t) {
+            uint4 x[kRouterVecs];
+#pragma unroll
+            for (int i = 0; i < kRouterVecs; ++i)
+                x[i] = c0 + 32 * i < c1 ? __ldg(xr + c0 + 32 * i) : make_uint4(0, 0, 0, 0);
+            double acc = 0.0;
+#pragma unroll
+            for (int i = 0; i < kRouterVecs; ++i) {
+                float wf[8], xf[8], s = 0.0f;
+                unpack8(w[i], wf);
+                unpack8(x[i], xf);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) s = fmaf(wf[j], xf[j], s);
                 acc += (double)s;
             }
 #pragma unroll
             for (int off = 16; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
-            if (lane == 0) a.part[((size_t)sp * a.T + t) * a.E + e] = acc;
+            if (lane == 0) *out = acc;
+            out += a.E;
+            xr += nch;
         }
     }
 }
 
-// The choice of token t by one warp; `key` holds E values.
-__device__ void choose(const FewArgs& a, int t, double* key, const Scratch& S) {
+// Keys are compared as integers in the order of their values; a NaN ranks
+// below every number, as -infinity (keys are never -0: a score is not
+// negative).
+__device__ __forceinline__ unsigned long long sortable(double v) {
+    if (isnan(v)) v = -INFINITY;
+    const long long b = __double_as_longlong(v);
+    return (unsigned long long)(b < 0 ? ~b : b | (1ll << 63));
+}
+__device__ __forceinline__ double from_sortable(unsigned long long k) {
+    return __longlong_as_double((long long)(k >> 63 ? k & ~(1ull << 63) : ~k));
+}
+
+// Warp-wide best of (key, index): larger key first, then lower index; an index
+// of 0x7fffffff with key 0 is nobody.  Every lane gets the winner.
+__device__ __forceinline__ int warp_best(unsigned long long key, int idx) {
+    const uint32_t hi = (uint32_t)(key >> 32), lo = (uint32_t)key;
+    const uint32_t mh = __reduce_max_sync(0xffffffffu, hi);
+    const uint32_t ml = __reduce_max_sync(0xffffffffu, hi == mh ? lo : 0u);
+    return (int)__reduce_min_sync(0xffffffffu, hi == mh && lo == ml ? (uint32_t)idx : 0x7fffffffu);
+}
+
+// The choice of token t by one warp, from its E keys and scores.
+__device__ void choose(const FewArgs& a, int t, const unsigned long long* key, const double* score,
+                       const Scratch& S) {
     const int lane = threadIdx.x & 31;
-    for (int e = lane; e < a.E; e += 32) {
-        double l = 0.0;
-        for (int sp = 0; sp < a.n_split; ++sp) l += __ldcg(a.part + ((size_t)sp * a.T + t) * a.E + e);
-        const double c = 1.0 / (1.0 + exp(-l)) + (double)__ldg(a.bias + e);
-        key[e] = isnan(c) ? -INFINITY : c;   // NaN ranks below numbers
-    }
-    __syncwarp();
     uint32_t keep = 0xffffffffu;
     const int gsz = a.E / a.n_group;
     if (a.n_group > 1) {
         // lane g: the sum of group g's group_topn largest keys, largest first
-        double gs = -INFINITY;
+        unsigned long long gs = 0;
+        int gi = 0x7fffffff;
         if (lane < a.n_group) {
-            double lv = INFINITY;
+            double sum = 0.0;
+            unsigned long long lk = ~0ull;
             int li = -1;
             for (int j = 0; j < a.group_topn; ++j) {
-                double bv = -INFINITY;
+                unsigned long long bk = 0;
                 int bi = 0x7fffffff;
-                for (int e = lane * gsz; e < (lane + 1) * gsz; ++e)
-                    if (better(lv, li, key[e], e) && better(key[e], e, bv, bi)) {
-                        bv = key[e];
+                for (int e = lane * gsz; e < (lane + 1) * gsz; ++e) {
+                    const unsigned long long v = key[e];
+                    if ((v < lk || (v == lk && e > li)) && v > bk) {
+                        bk = v;
                         bi = e;
                     }
-                gs = j == 0 ? bv : gs + bv;
-                lv = bv;
+                }
+                sum = j == 0 ? from_sortable(bk) : sum + from_sortable(bk);
+                lk = bk;
                 li = bi;
             }
-            if (isnan(gs)) gs = -INFINITY;
+            gs = sortable(sum);
+            gi = lane;
         }
         keep = 0;
-        bool taken = lane >= a.n_group;
         for (int j = 0; j < a.topk_group; ++j) {
-            double bv = taken ? -INFINITY : gs;
-            int bi = taken ? 0x7fffffff : lane;
-            warp_best(bv, bi);
-            keep |= 1u << (bi & 31);
-            if (lane == bi) taken = true;
+            const int b = warp_best(gs, gi);
+            keep |= 1u << b;
+            if (lane == b) {
+                gs = 0;
+                gi = 0x7fffffff;
+            }
         }
     }
-    double my_s = 0.0;
-    int my_e = 0;
-    double lv = INFINITY;
-    int li = -1;
-    for (int j = 0; j < a.k; ++j) {
-        double bv = -INFINITY;
-        int bi = 0x7fffffff;
-        for (int e = lane; e < a.E; e += 32)
-            if ((keep >> (a.n_group > 1 ? e / gsz : 0) & 1u) && better(lv, li, key[e], e) &&
-                better(key[e], e, bv, bi)) {
-                bv = key[e];
+    // lane l owns experts l, l + 32, ...; it rescans them when one is taken
+    uint32_t taken = 0;
+    unsigned long long bk = 0;
+    int bi = 0x7fffffff;
+    auto scan = [&]() {
+        bk = 0;
+        bi = 0x7fffffff;
+#pragma unroll 4
+        for (int i = 0; i < a.E / 32; ++i) {
+            const int e = lane + 32 * i;
+            const unsigned long long v = key[e];
+            const bool ok = !(taken >> i & 1u) && (a.n_group == 1 || (keep >> (e / gsz) & 1u));
+            if (ok && v > bk) {
+                bk = v;
                 bi = e;
             }
-        warp_best(bv, bi);
-        lv = bv;
-        li = bi;
-        if (lane == j) my_e = bi;
+        }
+    };
+    scan();
+    int my_e = 0;
+    for (int j = 0; j < a.k; ++j) {
+        const int e = warp_best(bk, bi);
+        if (lane == j) my_e = e;
+        if (lane == (e & 31)) {
+            taken |= 1u << (e >> 5);
+            scan();
+        }
+        __syncwarp();
     }
-    if (lane < a.k) {
-        double l = 0.0;
-        for (int sp = 0; sp < a.n_split; ++sp) l += __ldcg(a.part + ((size_t)sp * a.T + t) * a.E + my_e);
-        my_s = 1.0 / (1.0 + exp(-l));
-    }
+    const double my_s = lane < a.k ? score[my_e] : 0.0;
     double sum = 0.0;
     for (int j = 0; j < a.k; ++j) sum += __shfl_sync(0xffffffffu, my_s, j);
     if (lane < a.k) {
         const float w = (float)((a.norm ? my_s / sum : my_s) * (double)a.rsf);
         S.sel[t * a.k + lane] = my_e;
         S.selw[t * a.k + lane] = w;
+        atomicOr(&S.emask[my_e], 1u << t);
         if (blockIdx.x == 0) {
             if (a.idx) a.idx[(size_t)t * a.k + lane] = my_e;
             if (a.w) a.w[(size_t)t * a.k + lane] = w;
@@ -325,42 +356,79 @@ __device__ void choose(const FewArgs& a, int t, double* key, const Scratch& S) {
     }
 }
 
+// ------------------------------------------------------------------ shares
+// What block c of G works on.  Phase 1: units of the shared expert (known
+// before the choice) and of the routed ones, each cut into G contiguous runs.
+// Phase 2: the (row block, expert, K) axis in steps of 128 columns, cut at
+// even steps of an expert.  Every step moves the same bytes as H / 128 of a
+// unit, so phase 2's cuts make up for what phase 1's whole units leave uneven.
+__device__ __forceinline__ int cut(int c, int n, int G) { return (int)((unsigned)c * (unsigned)n / (unsigned)G); }
+
+// Cuts of the routed units and of phase 2, by threads tid of n.
+template <int DT>
+__device__ void make_cuts(const FewArgs& a, const Plan& P, int n_active, int tid, int n) {
+    constexpr int R = Fmt<DT>::kRows;
+    const int G = gridDim.x, routed = n_active - (a.Is ? 1 : 0);
+    const int us = a.Is / (R / 2), ur = routed * (a.I / (R / 2)), ublk = a.H / 128;
+    const int ws = a.Is / 128, wi = a.I / 128, wsum = ws + routed * wi;
+    const int tot2 = a.H / R * wsum, tot = (us + ur) * ublk + tot2;
+    // Taking earlier shares into account needs each to fit under the even
+    // share of the whole, or the cuts would run backwards.
+    const bool joint1 = (us + ur) / G >= (us + G - 1) / G;
+    const int most = joint1 ? (us + ur + G - 1) / G : (us + G - 1) / G + (ur + G - 1) / G;
+    const bool joint2 = tot / G >= most * ublk;
+    for (int c = tid; c <= G; c += n) {
+        const int s = cut(c, us, G);
+        const int r = joint1 ? cut(c, us + ur, G) - s : cut(c, ur, G);
+        int b = tot2;
+        if (c < G) {
+            b = joint2 ? (int)((double)c * ((double)tot / G)) - (s + r) * ublk : (int)((double)c * ((double)tot2 / G));
+            const int off = b % wsum;
+            b -= (off < ws ? off : (off - ws) % wi) & 1;
+        }
+        P.cut1[c] = r;
+        P.cut2[c] = b;
+    }
+}
+
 // Touched experts in ascending order after the shared one, with their tokens
-// and pairs, from the choice.  All router threads; `tid` within them.
+// and pairs, and the blocks' shares.  All router threads; `tid` within them.
+template <int DT>
 __device__ void build_plan(const FewArgs& a, const Plan& P, const Scratch& S, int tid) {
     const int lane = tid & 31;
-    for (int e = tid; e < a.E; e += kRouterGroup) S.emask[e] = 0;
-    group_any(2, false);
-    for (int i = tid; i < a.T * a.k; i += kRouterGroup) atomicOr(&S.emask[S.sel[i]], 1u << (i / a.k));
-    group_any(2, false);
     if (tid < 32) {
+        // lane l takes experts l * E / 32 and on
+        const int per = a.E / 32;
         int n = 0, pairs = 0;
-        if (a.Is) {
-            if (lane == 0) P.active[0] = Active{-1, (1u << a.T) - 1u, 0, a.T};
-            n = 1;
-            pairs = a.T;
+        for (int i = 0; i < per; ++i) {
+            const uint32_t m = S.emask[lane * per + i];
+            n += m != 0;
+            pairs += __popc(m);
         }
-        for (int e0 = 0; e0 < a.E; e0 += 32) {
-            const uint32_t m = S.emask[e0 + lane];
-            const int cnt = __popc(m);
-            const uint32_t hit = __ballot_sync(0xffffffffu, cnt > 0);
-            int incl = cnt;
+        const int n0 = n, p0 = pairs;
 #pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, incl, off);
-                if (lane >= off) incl += v;
+        for (int off = 1; off < 32; off <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, n, off), w = __shfl_up_sync(0xffffffffu, pairs, off);
+            if (lane >= off) {
+                n += v;
+                pairs += w;
             }
-            if (cnt) {
-                const int p = n + __popc(hit & ((1u << lane) - 1u));
-                P.active[p] = Active{e0 + lane, m, pairs + incl - cnt, cnt};
-                S.apos[e0 + lane] = p;
-            }
-            n += __popc(hit);
-            pairs += __shfl_sync(0xffffffffu, incl, 31);
         }
-        if (lane == 0) *P.n_active = n;
+        const int first = a.Is ? 1 : 0;
+        if (lane == 31) *P.n_active = first + n;
+        int at = first + n - n0, base = (a.Is ? a.T : 0) + pairs - p0;
+        for (int i = 0; i < per; ++i) {
+            const int e = lane * per + i;
+            const uint32_t m = S.emask[e];
+            if (!m) continue;
+            P.active[at] = Active{e, m, base, __popc(m)};
+            S.apos[e] = at++;
+            base += __popc(m);
+        }
+        if (a.Is && lane == 0) P.active[0] = Active{-1, (1u << a.T) - 1u, 0, a.T};
     }
     group_any(2, false);
+    make_cuts<DT>(a, P, *P.n_active, tid, kRouterGroup);
     if (a.Is)
         for (int t = tid; t < a.T; t += kRouterGroup) P.pairw[t] = 1.0f;
     for (int i = tid; i < a.T * a.k; i += kRouterGroup) {
@@ -370,83 +438,21 @@ __device__ void build_plan(const FewArgs& a, const Plan& P, const Scratch& S, in
     }
 }
 
-// ------------------------------------------------------------------ shares
-// What block c of G works on.  Phase 1 units: the shared expert's (known
-// before the choice) and the routed experts', each cut into G contiguous
-// runs; phase 2: the (row block, expert, K) axis in steps of 128 columns.
-// Every step and every H / 128 of a unit move the same bytes, so phase 2's
-// cuts make up for what phase 1's whole units leave uneven.
-struct Shares {
-    int G, us, ur, ublk;        // blocks; phase-1 units, shared and routed; steps of a unit
-    int ws, wi, wsum, nrb;      // steps of the shared and of a routed expert, of a row block; row blocks
-    bool joint1, joint2;        // cuts of the routed units / of phase 2 take earlier ones into account
-    long long tot2;
-
-    __device__ int s_at(int c) const { return (int)((long long)c * us / G); }
-    __device__ int r_at(int c) const {
-        return joint1 ? (int)((long long)c * (us + ur) / G) - s_at(c) : (int)((long long)c * ur / G);
-    }
-    // a cut moves back to the start of its tensor copy (two steps)
-    __device__ long long b_at(int c) const {
-        long long b;
-        if (joint2) {
-            const long long tot = (long long)(us + ur) * ublk + tot2;
-            b = c * tot / G - (long long)(s_at(c) + r_at(c)) * ublk;
-        } else {
-            b = c * tot2 / G;
-        }
-        if (b >= tot2) return tot2;
-        const int off = (int)(b % wsum);
-        return b - ((off < ws ? off : (off - ws) % wi) & 1);
-    }
-};
-
-template <int DT>
-__device__ Shares make_shares(const FewArgs& a, int n_active) {
-    constexpr int R = Fmt<DT>::kRows;
-    Shares s;
-    const int routed = n_active - (a.Is ? 1 : 0);
-    s.G = gridDim.x;
-    s.us = a.Is / (R / 2);
-    s.ur = routed * (a.I / (R / 2));
-    s.ublk = a.H / 128;
-    s.ws = a.Is / 128;
-    s.wi = a.I / 128;
-    s.wsum = s.ws + routed * s.wi;
-    s.nrb = a.H / R;
-    s.tot2 = (long long)s.nrb * s.wsum;
-    // both need every block's earlier part to fit under its even share of the
-    // whole, or the cuts would run backwards
-    s.joint1 = (s.us + s.ur) / s.G >= (s.us + s.G - 1) / s.G;
-    const int most = s.joint1 ? (s.us + s.ur + s.G - 1) / s.G
-                              : (s.us + s.G - 1) / s.G + (s.ur + s.G - 1) / s.G;
-    s.joint2 = ((long long)(s.us + s.ur) * s.ublk + s.tot2) / s.G >= (long long)most * s.ublk;
-    return s;
-}
-
 // ------------------------------------------------------------------ the ring
+// Slots of a stage, in the order every role walks them.  `w` and `x`: the
+// weights (and scales) and the activations have landed.
 struct Ring {
-    uint64_t *full, *empty;
+    uint64_t *w, *x, *empty;
     uint8_t* base;
-    int n, slot;
+    int n, bytes, slot;
     uint32_t phase;
-    __device__ void next() {
+    __device__ __forceinline__ void next() {
         if (++slot == n) {
             slot = 0;
             phase ^= 1;
         }
     }
-};
-
-// What a stage multiplies: `rows` weight rows of one matrix, columns k0 ..
-// k0 + kn - 1, with the activations of `count` pairs.
-struct Item {
-    int expert;        // -1: shared
-    int first;         // first feature (phase 1) or output row (phase 2)
-    int n, K;          // features of the expert; K of the matrix
-    uint32_t mask;
-    int base, count;
-    int k0, kn;
+    __device__ __forceinline__ uint8_t* stage() const { return base + slot * bytes; }
 };
 
 // Columns of a stage: phase 2 keeps head and tail rows of every pair, and
@@ -463,84 +469,130 @@ __host__ __device__ constexpr int off_x() {
     return 2 * kBoxBytes + Fmt<DT>::kScaleBytes;
 }
 
-// Row of its matrix that row r of the unit is: phase 1 alternates 8 gate rows
-// and the 8 up rows of the same features.
-__device__ __forceinline__ size_t weight_row(const Item& it, bool down, int H, int I, int r) {
-    if (down) return (it.expert < 0 ? 0 : (size_t)it.expert * H) + it.first + r;
-    const int f = it.first + (r >> 4) * 8 + (r & 7) + (r & 8 ? it.n : 0);
-    return (it.expert < 0 ? 0 : (size_t)it.expert * 2 * I) + f;
+// The stages of phase 1's unit with `count` tokens: stage(k0, kn).
+template <class Stage>
+__device__ __forceinline__ bool walk_unit(const FewArgs& a, Stage stage) {
+    for (int k0 = 0; k0 < a.H; k0 += kChunk)
+        if (!stage(k0, min(kChunk, a.H - k0))) return false;
+    return true;
 }
 
-// Producer, all lanes: the stage's weights (one tensor copy for each 256
-// columns) and scales.
+// The stages of phase 2's steps begin .. end - 1: item(rb, expert) before the
+// stages of an expert, stage(k0, kn), and row_end(rb) behind the last stage of
+// a row block (or of the share).  Each returns false to give up.
+template <class Item, class Stage, class RowEnd>
+__device__ __forceinline__ bool walk_down(const FewArgs& a, const Plan& P, int n_active, int begin, int end,
+                                          Item item, Stage stage, RowEnd row_end) {
+    if (begin >= end) return true;
+    const int first = a.Is ? 1 : 0, ws = a.Is / 128, wi = a.I / 128;
+    const int wsum = ws + (n_active - first) * wi;
+    int rb = begin / wsum, off = begin - rb * wsum, p = 0;
+    if (off >= ws) {
+        p = first + (off - ws) / wi;
+        off = (off - ws) % wi;
+    }
+    int pos = begin;
+    while (true) {
+        const Active act = P.active[p];
+        const int steps = act.expert < 0 ? ws : wi, most = chunk_cols(true, act.count) / 128;
+        if (!item(rb, act)) return false;
+        while (off < steps && pos < end) {
+            const int n = min(most, min(steps - off, end - pos));
+            if (!stage(off * 128, n * 128)) return false;
+            off += n;
+            pos += n;
+        }
+        off = 0;
+        if (++p == n_active || pos == end) {
+            if (!row_end(rb)) return false;
+            if (pos == end) return true;
+            p = 0;
+            ++rb;
+        }
+    }
+}
+
+// Row of its matrix that row r of the unit at feature (or output row) `first`
+// is: phase 1 alternates 8 gate rows and the 8 up rows of the same features.
+__device__ __forceinline__ size_t gate_up_row(const FewArgs& a, int expert, int first, int r) {
+    const int n = expert < 0 ? a.Is : a.I;
+    return (expert < 0 ? 0 : (size_t)expert * 2 * n) + first + (r >> 4) * 8 + (r & 7) + (r & 8 ? n : 0);
+}
+__device__ __forceinline__ size_t down_row(const FewArgs& a, int expert, int first, int r) {
+    return (expert < 0 ? 0 : (size_t)expert * a.H) + first + r;
+}
+
+// Weight producer: what one unit's (or expert's) stages share.
 template <int DT>
-__device__ void issue_weights(const FewArgs& a, const Item& it, bool down, const Ring& ring, uint64_t policy) {
+struct Source {
     using F = Fmt<DT>;
-    const int lane = threadIdx.x & 31;
-    const uint32_t dst = moe::smem_addr(ring.base + ring.slot * a.stage_bytes);
-    if (lane == 0) {
-        uint64_t* full = &ring.full[ring.slot];
-        const uint32_t bar = moe::smem_addr(full);
-        moe::mbar_arrive_expect_tx(full, it.kn > kBox ? 2 * kBoxBytes : kBoxBytes);
-        const int group = (int)(weight_row(it, down, a.H, a.I, 0) / 8);
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            if (b * kBox >= it.kn) break;
-            const int panel = (it.k0 + b * kBox) * F::kBits / 512;
-            if (down)
-                box_load_4d(dst + b * kBoxBytes, it.expert < 0 ? &a.m2s : &a.m2, bar, panel, group, policy);
-            else
-                box_load_5d(dst + b * kBoxBytes, it.expert < 0 ? &a.m13s : &a.m13, bar, panel, group, policy);
-        }
-    }
-    __syncwarp();
-    const void* sc = down ? (it.expert < 0 ? a.s2s : a.s2) : (it.expert < 0 ? a.s13s : a.s13);
-    if (DT == MOE_DTYPE_FP8_E4M3_BLOCK128) {
-        // [gate, up][4 blocks of 128 columns]; phase 2 has one row block
-        if (lane < (down ? 4 : 8) && (lane & 3) * 128 < it.kn) {
-            const size_t row = weight_row(it, down, a.H, a.I, lane < 4 ? 0 : 8) / 128;
-            copy4(dst + 2 * kBoxBytes + lane * 4,
-                  static_cast<const float*>(sc) + row * (it.K / 128) + it.k0 / 128 + (lane & 3));
-        }
-    } else if (DT == MOE_DTYPE_MXFP4_BLOCK32) {
-        // 16 bytes a row; they start at a multiple of 16 when K / 32 is one
-        const uint8_t* s8 = static_cast<const uint8_t*>(sc);
-        if (it.K % 512 == 0 && it.kn == kChunk && it.k0 % 512 == 0) {
-#pragma unroll
-            for (int r = lane; r < F::kRows; r += 32)
-                copy16(dst + 2 * kBoxBytes + r * 16,
-                       s8 + (weight_row(it, down, a.H, a.I, r) * it.K + it.k0) / 32);
-        } else {
-#pragma unroll 4
-            for (int i = lane; i < F::kRows * 4; i += 32)
-                if ((i & 3) * 128 < it.kn)
-                    copy4(dst + 2 * kBoxBytes + i * 4,
-                          s8 + (weight_row(it, down, a.H, a.I, i >> 2) * it.K + it.k0) / 32 + (i & 3) * 4);
-        }
-    }
-}
+    const CUtensorMap* map;
+    const uint8_t *s0, *s1;     // scales of this lane's rows, at column 0
+    int group, K;
+    bool down;
 
-// Producer, all lanes: the activation rows of the stage in `slot`, and the
-// lanes' arrival for it.
-template <int DT>
-__device__ void issue_acts(const FewArgs& a, bool down, uint32_t mask, int base, int count, int k0, int kn,
-                           const Ring& ring, int slot) {
-    const int lane = threadIdx.x & 31;
-    const int xs = x_stride<DT>(chunk_cols(down, count));
-    uint32_t dst = moe::smem_addr(ring.base + slot * a.stage_bytes + off_x<DT>());
-    if (down) {
-        for (int i = 0; i < 2 * count; ++i, dst += xs) {
-            const uint16_t* src = (i < count ? a.act_hi + (size_t)(base + i) * a.ld_act
-                                             : a.act_lo + (size_t)(base + i - count) * a.ld_act) + k0;
-            for (int c = lane * 8; c < kn; c += 256) copy16(dst + c * 2, src + c);
-        }
-    } else {
-        for (uint32_t m = mask; m; m &= m - 1, dst += xs) {
-            const uint16_t* src = a.x + (size_t)(__ffs(m) - 1) * a.H + k0;
-            for (int c = lane * 8; c < kn; c += 256) copy16(dst + c * 2, src + c);
+    __device__ __forceinline__ void unit(const FewArgs& a, bool dn, int expert, int first) {
+        const int lane = threadIdx.x & 31;
+        down = dn;
+        K = dn ? (expert < 0 ? a.Is : a.I) : a.H;
+        map = dn ? (expert < 0 ? &a.m2s : &a.m2) : (expert < 0 ? &a.m13s : &a.m13);
+        const uint8_t* sc = static_cast<const uint8_t*>(dn ? (expert < 0 ? a.s2s : a.s2)
+                                                           : (expert < 0 ? a.s13s : a.s13));
+        auto row = [&](int r) { return dn ? down_row(a, expert, first, r) : gate_up_row(a, expert, first, r); };
+        group = (int)(row(0) / 8);
+        if (DT == MOE_DTYPE_FP8_E4M3_BLOCK128) {
+            // lanes 0-3: the blocks of the gate (or output) rows, 4-7: of the up rows
+            s0 = sc + (row(lane & 4 ? 8 : 0) / 128 * (K / 128) + (lane & 3)) * 4;
+        } else if (DT == MOE_DTYPE_MXFP4_BLOCK32) {
+            s0 = sc + row(lane) * (K / 32);
+            s1 = sc + row(lane + 32) * (K / 32);
         }
     }
-    arrive_copied(&ring.full[slot]);
+
+    // All lanes: one tensor copy for each 256 columns, and the scales.
+    __device__ __forceinline__ void stage(const Ring& ring, int k0, int kn, uint64_t policy) const {
+        const int lane = threadIdx.x & 31;
+        const uint32_t dst = moe::smem_addr(ring.stage());
+        uint64_t* full = &ring.w[ring.slot];
+        if (lane == 0) {
+            const uint32_t bar = moe::smem_addr(full);
+            moe::mbar_arrive_expect_tx(full, kn > kBox ? 2 * kBoxBytes : kBoxBytes);
+            const int piece = k0 * F::kBits / 512;
+            if (down) {
+                box_load_4d(dst, map, bar, piece, group, policy);
+                if (kn > kBox) box_load_4d(dst + kBoxBytes, map, bar, piece + kBox * F::kBits / 512, group, policy);
+            } else {
+                box_load_5d(dst, map, bar, piece, group, policy);
+                if (kn > kBox) box_load_5d(dst + kBoxBytes, map, bar, piece + kBox * F::kBits / 512, group, policy);
+            }
+        }
+        const uint32_t sdst = dst + 2 * kBoxBytes;
+        if (DT == MOE_DTYPE_FP8_E4M3_BLOCK128) {
+            if (lane < (down ? 4 : 8) && (lane & 3) * 128 < kn) copy4(sdst + lane * 4, s0 + k0 / 128 * 4);
+            arrive_copied(full);
+        } else if (DT == MOE_DTYPE_MXFP4_BLOCK32) {
+            // a row's 16 bytes start at a multiple of 16 when K / 32 and k0 / 32 are
+            const uint8_t *p0 = s0 + k0 / 32, *p1 = s1 + k0 / 32;
+            if (kn == kChunk && ((K | k0) & 511) == 0) {
+                copy16(sdst + lane * 16, p0);
+                copy16(sdst + (lane + 32) * 16, p1);
+            } else {
+                for (int j = 0; j < kn / 32; j += 4) {
+                    copy4(sdst + lane * 16 + j, p0 + j);
+                    copy4(sdst + (lane + 32) * 16 + j, p1 + j);
+                }
+            }
+            arrive_copied(full);
+        }
+    }
+};
+
+// Activation producer, all lanes of one warp: `rows` rows of kn columns, the
+// i-th at the i-th set bit of `mask` (or the i-th at all), `ld` apart.
+__device__ __forceinline__ void copy_row(uint32_t dst, const uint16_t* src, int kn) {
+    const int c = (threadIdx.x & 31) * 8;
+    if (c < kn) copy16(dst + c * 2, src + c);
+    if (c + 256 < kn) copy16(dst + c * 2 + 512, src + c + 256);
 }
 
 // ------------------------------------------------------------------ multiplication
@@ -571,10 +623,10 @@ __device__ __forceinline__ void widen_e2m1(uint32_t v, uint32_t (&p)[4]) {
     p[3] = merge_sign<126>(v, (v >> 6) & 0x01c001c0u);
 }
 
-// The lane's activations of its column for the warp's 64 columns of K, in
-// the weights' order.
+// The lane's activations of its column for the warp's 64 columns of K, in the
+// weights' order.
 template <int DT>
-__device__ __forceinline__ void load_acts(const uint8_t* row, int t, uint32_t (&b)[8]) {
+__device__ __forceinline__ void load_acts(const uint8_t* row, int t, bool zero, uint32_t (&b)[8]) {
     uint4 v[2];
     if (DT == MOE_DTYPE_FP8_E4M3_BLOCK128) {
         // lane t: columns 16 t .. 16 t + 15
@@ -585,6 +637,7 @@ __device__ __forceinline__ void load_acts(const uint8_t* row, int t, uint32_t (&
         v[0] = *reinterpret_cast<const uint4*>(row + t * 16);
         v[1] = *reinterpret_cast<const uint4*>(row + 64 + t * 16);
     }
+    if (zero) v[0] = v[1] = make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const uint4 w = v[i];
@@ -608,31 +661,38 @@ __device__ __forceinline__ void load_acts(const uint8_t* row, int t, uint32_t (&
     }
 }
 
-// One warp's part of a stage: all rows of the unit by its 64 columns of K, for
-// NT tiles of 8 tokens.  xrow: the stage's activation row of this lane's
-// column, or -1.  In phase 2 a column is a token, and only the expert's own
-// tokens add the stage's products: an infinity or a NaN among its weights
-// reaches no other.
-template <int DT, int NT, bool DOWN>
-__device__ __forceinline__ void mma_stage(const Item& it, const uint8_t* stage, int kw, const int (&xrow)[NT],
-                                          bool tile1, float (&acc)[Fmt<DT>::kRows / 16][NT][4]) {
+// Which activation rows a lane multiplies in phase 1 (`row`: its column's
+// token's place in the unit's list) or in phase 2 (a column is a token).
+// Tiles are 8 columns.  With at most four tokens (FOLD) phase 2's tile holds
+// the heads in columns 0-3 and the tails in 4-7, which are added at the end;
+// otherwise heads and tails are two products.
+template <int NT>
+struct Columns {
+    int row[NT];        // row of the stage's activations
+    bool zero[NT];      // not the expert's token: the column adds nothing
+    bool own[NT][2];    // the same for the lane's two result columns
+    bool tile1;         // the second tile has any
+};
+
+// One warp's part of a stage: all rows of the unit by its 64 columns of K.
+// In phase 2 only the expert's own tokens add the stage's products: an
+// infinity or a NaN among its weights reaches no other.
+template <int DT, int NT, bool DOWN, bool FOLD>
+__device__ __forceinline__ void mma_stage(const uint8_t* stage, int kw, int count, const Columns<NT>& col,
+                                          float (&acc)[Fmt<DT>::kRows / 16][NT][4]) {
     using F = Fmt<DT>;
     constexpr int MT = F::kRows / 16;
     constexpr int PB = kBox * F::kBits / 512;        // 64-byte pieces of a row in a box
-    if (kw * kSlice >= it.kn) return;
+    constexpr bool TAIL = DOWN && !FOLD;             // a second product for the tails
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int xs = x_stride<DT>(chunk_cols(DOWN, it.count));
+    const int xs = x_stride<DT>(chunk_cols(DOWN, count));
     const uint8_t* x = stage + off_x<DT>() + kw * kSlice * 2;
     uint32_t b[NT][8], bl[NT][8];
-    bool own[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-        own[nt][0] = !DOWN || (it.mask >> (8 * nt + 2 * t) & 1u);
-        own[nt][1] = !DOWN || (it.mask >> (8 * nt + 2 * t + 1) & 1u);
-        if (nt == 1 && !tile1) continue;
-        const uint8_t* xr = x + max(xrow[nt], 0) * xs;
-        load_acts<DT>(xr, t, b[nt]);
-        if (DOWN) load_acts<DT>(xr + it.count * xs, t, bl[nt]);
+        if (nt == 1 && !col.tile1) continue;
+        load_acts<DT>(x + col.row[nt] * xs, t, DOWN && col.zero[nt], b[nt]);
+        if (TAIL) load_acts<DT>(x + (col.row[nt] + count) * xs, t, col.zero[nt], bl[nt]);
     }
     // this warp's columns in the boxes: first piece of 64 bytes
     const int c0 = kw * kSlice;
@@ -643,54 +703,75 @@ __device__ __forceinline__ void mma_stage(const Item& it, const uint8_t* stage, 
     for (int mt = 0; mt < MT; ++mt) {
         const uint8_t* w0 = w + (2 * mt) * PB * 512;
         const uint8_t* w1 = w0 + PB * 512;
-        if (DT == MOE_DTYPE_BF16) {
-            float c[NT][4] = {};
+        // products in independent chains: two halves of the slice, heads and tails
+        float c[2][NT][4] = {}, cl[2][NT][4] = {};
+        uint32_t top0 = 0, top1 = 0;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < 2; ++h) {
+            uint32_t m[2][4];
+            if (DT == MOE_DTYPE_BF16) {
                 const uint4 p = *reinterpret_cast<const uint4*>(w0 + h * 512 + ((t ^ sw) << 4));
                 const uint4 q = *reinterpret_cast<const uint4*>(w1 + h * 512 + ((t ^ sw) << 4));
-                const uint32_t m0[4] = {p.x, q.x, p.y, q.y}, m1[4] = {p.z, q.z, p.w, q.w};
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    if (nt == 1 && !tile1) continue;
-                    mma_bf16(c[nt], m0, b[nt][4 * h], b[nt][4 * h + 1]);
-                    mma_bf16(c[nt], m1, b[nt][4 * h + 2], b[nt][4 * h + 3]);
-                    if (DOWN) {
-                        mma_bf16(c[nt], m0, bl[nt][4 * h], bl[nt][4 * h + 1]);
-                        mma_bf16(c[nt], m1, bl[nt][4 * h + 2], bl[nt][4 * h + 3]);
-                    }
-                }
+                m[0][0] = p.x, m[0][1] = q.x, m[0][2] = p.y, m[0][3] = q.y;
+                m[1][0] = p.z, m[1][1] = q.z, m[1][2] = p.w, m[1][3] = q.w;
+            } else if (DT == MOE_DTYPE_FP8_E4M3_BLOCK128) {
+                const uint2 p = *reinterpret_cast<const uint2*>(w0 + ((t ^ sw) << 4) + 8 * h);
+                const uint2 q = *reinterpret_cast<const uint2*>(w1 + ((t ^ sw) << 4) + 8 * h);
+                widen_e4m3(p.x, m[0][0], m[0][2], top0);
+                widen_e4m3(q.x, m[0][1], m[0][3], top1);
+                widen_e4m3(p.y, m[1][0], m[1][2], top0);
+                widen_e4m3(q.y, m[1][1], m[1][3], top1);
+            } else {
+                // 16-byte piece of the 32-column block, a word a lane
+                const int off = ((((c0 >> 5) + h & 3) ^ sw) << 4) + t * 4;
+                uint32_t p[4], q[4];
+                widen_e2m1(*reinterpret_cast<const uint32_t*>(w0 + off), p);
+                widen_e2m1(*reinterpret_cast<const uint32_t*>(w1 + off), q);
+                m[0][0] = p[0], m[0][1] = q[0], m[0][2] = p[1], m[0][3] = q[1];
+                m[1][0] = p[2], m[1][1] = q[2], m[1][2] = p[3], m[1][3] = q[3];
             }
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (own[nt][j & 1]) acc[mt][nt][j] += c[nt][j];
-        } else if (DT == MOE_DTYPE_FP8_E4M3_BLOCK128) {
-            const uint4 p = *reinterpret_cast<const uint4*>(w0 + ((t ^ sw) << 4));
-            const uint4 q = *reinterpret_cast<const uint4*>(w1 + ((t ^ sw) << 4));
-            const uint32_t pc[4] = {p.x, p.y, p.z, p.w}, qc[4] = {q.x, q.y, q.z, q.w};
+                for (int nt = 0; nt < NT; ++nt) {
+                    if (nt == 1 && !col.tile1) continue;
+                    mma_bf16(c[h][nt], m[i], b[nt][4 * h + 2 * i], b[nt][4 * h + 2 * i + 1]);
+                    if (TAIL) mma_bf16(cl[h][nt], m[i], bl[nt][4 * h + 2 * i], bl[nt][4 * h + 2 * i + 1]);
+                }
+        }
+        float s[2][2];          // [half][rows g, rows g + 8]
+        if (DT == MOE_DTYPE_FP8_E4M3_BLOCK128) {
             const float* fs = reinterpret_cast<const float*>(sc) + c0 / 128;
-            const float s0 = fs[0], s1 = DOWN ? s0 : fs[4];
-            uint32_t top0 = 0, top1 = 0;
-            float c[NT][4] = {};
+            s[0][0] = s[1][0] = fs[0];
+            s[0][1] = s[1][1] = DOWN ? fs[0] : fs[4];
+        } else if (DT == MOE_DTYPE_MXFP4_BLOCK32) {
+            const uint8_t* sr = sc + (mt * 16 + g) * 16 + kw * 2;
+            const uint32_t e0 = *reinterpret_cast<const uint16_t*>(sr);
+            const uint32_t e1 = *reinterpret_cast<const uint16_t*>(sr + 128);
+            s[0][0] = e8m0(e0 & 255u), s[0][1] = e8m0(e1 & 255u);
+            s[1][0] = e8m0(e0 >> 8), s[1][1] = e8m0(e1 >> 8);
+        }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t m[4];
-                widen_e4m3(pc[i], m[0], m[2], top0);
-                widen_e4m3(qc[i], m[1], m[3], top1);
+        for (int nt = 0; nt < NT; ++nt) {
+            if (nt == 1 && !col.tile1) continue;
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    if (nt == 1 && !tile1) continue;
-                    mma_bf16(c[nt], m, b[nt][2 * i], b[nt][2 * i + 1]);
-                    if (DOWN) mma_bf16(c[nt], m, bl[nt][2 * i], bl[nt][2 * i + 1]);
+            for (int j = 0; j < 4; ++j) {
+                float v0 = c[0][nt][j], v1 = c[1][nt][j];
+                if (TAIL) {
+                    v0 += cl[0][nt][j];
+                    v1 += cl[1][nt][j];
                 }
+                float v;
+                if (DT == MOE_DTYPE_BF16)
+                    v = v0 + v1;
+                else if (DT == MOE_DTYPE_FP8_E4M3_BLOCK128)
+                    v = (v0 + v1) * s[0][j >> 1];
+                else
+                    v = fmaf(v0, s[0][j >> 1], v1 * s[1][j >> 1]);
+                if (!DOWN || col.own[nt][j & 1]) acc[mt][nt][j] += v;
             }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (own[nt][j & 1]) acc[mt][nt][j] = fmaf(c[nt][j], j < 2 ? s0 : s1, acc[mt][nt][j]);
+        }
+        if (DT == MOE_DTYPE_FP8_E4M3_BLOCK128) {
             // a NaN code anywhere in a row makes its sums NaN
             const uint32_t n0 = __vcmpeq2(top0, 0x07f007f0u), n1 = __vcmpeq2(top1, 0x07f007f0u);
             if (__any_sync(0xffffffffu, n0 | n1)) {
@@ -700,87 +781,70 @@ __device__ __forceinline__ void mma_stage(const Item& it, const uint8_t* stage, 
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        if (own[nt][j & 1] && (j < 2 ? r0 : r1)) acc[mt][nt][j] = __int_as_float(0x7fc00000);
-            }
-        } else {
-            const uint8_t* sr = sc + (mt * 16 + g) * 16 + kw * 2;
-            const uint32_t e0 = *reinterpret_cast<const uint16_t*>(sr);
-            const uint32_t e1 = *reinterpret_cast<const uint16_t*>(sr + 128);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                // 16-byte piece of the 32-column block, a word a lane
-                const int off = ((((c0 >> 5) + h & 3) ^ sw) << 4) + t * 4;
-                uint32_t p[4], q[4];
-                widen_e2m1(*reinterpret_cast<const uint32_t*>(w0 + off), p);
-                widen_e2m1(*reinterpret_cast<const uint32_t*>(w1 + off), q);
-                const uint32_t m0[4] = {p[0], q[0], p[1], q[1]}, m1[4] = {p[2], q[2], p[3], q[3]};
-                const float s0 = e8m0(e0 >> (8 * h) & 255u), s1 = e8m0(e1 >> (8 * h) & 255u);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    if (nt == 1 && !tile1) continue;
-                    float c[4] = {};
-                    mma_bf16(c, m0, b[nt][4 * h], b[nt][4 * h + 1]);
-                    mma_bf16(c, m1, b[nt][4 * h + 2], b[nt][4 * h + 3]);
-                    if (DOWN) {
-                        mma_bf16(c, m0, bl[nt][4 * h], bl[nt][4 * h + 1]);
-                        mma_bf16(c, m1, bl[nt][4 * h + 2], bl[nt][4 * h + 3]);
-                    }
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (own[nt][j & 1]) acc[mt][nt][j] = fmaf(c[j], j < 2 ? s0 : s1, acc[mt][nt][j]);
-                }
+                        if ((!DOWN || col.own[nt][j & 1]) && (j < 2 ? r0 : r1))
+                            acc[mt][nt][j] = __int_as_float(0x7fc00000);
             }
         }
     }
 }
 
 // ------------------------------------------------------------------ the kernel
-template <int DT, int NT>
+// NT: tiles of 8 tokens.  FOLD: at most four tokens.
+template <int DT, int NT, bool FOLD>
 __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant__ FewArgs a) {
     using F = Fmt<DT>;
     constexpr int R = F::kRows, MT = R / 16, NF = R / 2;
     extern __shared__ __align__(1024) uint8_t smem[];
-    __shared__ uint64_t full[kMaxStages], empty[kMaxStages], plan_ready;
+    __shared__ uint64_t bar_w[kMaxStages], bar_x[kMaxStages], bar_empty[kMaxStages], plan_ready;
     __shared__ int n_active_sh, abort_sh, last_sh;
     float4(*red)[MT][NT][32] = reinterpret_cast<float4(*)[MT][NT][32]>(smem + a.off_red);   // [warp]
     volatile int* abort_flag = &abort_sh;
-    Plan P{reinterpret_cast<Active*>(smem + a.off_active), reinterpret_cast<float*>(smem + a.off_pairw),
-           &n_active_sh};
+    const Plan P{reinterpret_cast<Active*>(smem + a.off_active), reinterpret_cast<float*>(smem + a.off_pairw),
+                 reinterpret_cast<int*>(smem + a.off_cuts), reinterpret_cast<int*>(smem + a.off_cuts) + kMaxBlocks + 1,
+                 &n_active_sh};
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < a.n_stages; ++i) {
-            moe::mbar_init(&full[i], 33);       // the weights' bytes, and the producer lanes' copies
-            moe::mbar_init(&empty[i], kWarps);  // one arrive per consumer warp
+            moe::mbar_init(&bar_w[i], F::kScaleBytes ? 33 : 1);  // the boxes' bytes, the lanes' scale copies
+            moe::mbar_init(&bar_x[i], 32);                       // the lanes' copies
+            moe::mbar_init(&bar_empty[i], kWarps);
         }
         moe::mbar_init(&plan_ready, 1);
         abort_sh = 0;
         moe::fence_barrier_init();
     }
     __syncthreads();
-    Ring ring{full, empty, smem + a.off_ring, a.n_stages, 0, 0};
+    Ring ring{bar_w, bar_x, bar_empty, smem + a.off_ring, a.n_stages, a.stage_bytes, 0, 0};
     int* bars = a.status + kBarWord;
-    const int cta = blockIdx.x;
+    const int cta = blockIdx.x, G = gridDim.x;
     const Active shared{-1, (1u << a.T) - 1u, 0, a.T};
-    const int first_routed = a.Is ? 1 : 0;
+    const int first_routed = a.Is ? 1 : 0, upe = a.I / NF;
+    const int s0 = cut(cta, a.Is / NF, G), s1 = cut(cta + 1, a.Is / NF, G);
+    // a wait that every lane of the warp takes and leaves together
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, moe::wait_bar(bar, parity, abort_flag, a.status)) != 0;
+    };
 
     if (warp >= kWarps && warp < kWarps + kRouters) {
         // ---------------------------------------------------------- router
         const int tid = threadIdx.x - kGroup, rw = warp - kWarps;
         Scratch S;
-        S.keys = reinterpret_cast<double*>(smem + a.off_scratch);
-        S.sel = reinterpret_cast<int*>(S.keys + (size_t)min(a.T, kRouters) * a.E);
+        S.keys = reinterpret_cast<unsigned long long*>(smem + a.off_scratch);
+        S.scores = reinterpret_cast<double*>(S.keys + (size_t)min(a.T, kRouters) * a.E);
+        S.sel = reinterpret_cast<int*>(S.scores + (size_t)min(a.T, kRouters) * a.E);
         S.selw = reinterpret_cast<float*>(S.sel + a.T * a.k);
         S.emask = reinterpret_cast<uint32_t*>(S.selw + a.T * a.k);
         S.apos = reinterpret_cast<int*>(S.emask + a.E);
-        for (int i = cta * kRouterGroup + tid; i < a.H / R; i += gridDim.x * kRouterGroup) a.joined[i] = 0;
-        router_phase(a, rw);
+        for (int i = cta * kRouterGroup + tid; i < a.H / R; i += G * kRouterGroup) a.joined[i] = 0;
+        for (int e = tid; e < a.E; e += kRouterGroup) S.emask[e] = 0;
+        router_phase(a, warp);
         __threadfence();
-        group_any(2, false);
+        asm volatile("barrier.cta.sync 3, %0;" ::"r"(kGroup + kRouterGroup) : "memory");
         bool ok = true;
         if (tid == 0) {
             if (!(a.stall && cta == 0)) atomicAdd(bars, 1);
             const long long t0 = clock64();
-            while (*reinterpret_cast<volatile int*>(bars) < (int)gridDim.x) {
+            while (*reinterpret_cast<volatile int*>(bars) < G) {
                 if (clock64() - t0 > moe::kWaitLimit) {
                     atomicOr(a.status, moe::DEV_STATUS_TIMEOUT);
                     *abort_flag = 1;
@@ -791,145 +855,149 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
             __threadfence();
         }
         if (!group_any(2, !ok)) {
-            for (int t = rw; t < a.T; t += kRouters) choose(a, t, S.keys + (size_t)rw * a.E, S);
-            group_any(2, false);
-            build_plan(a, P, S, tid);
+            for (int t0 = 0; t0 < a.T; t0 += kRouters) {
+                const int nt = min(kRouters, a.T - t0);
+#pragma unroll 2
+                for (int i = tid; i < nt * a.E; i += kRouterGroup) {
+                    const double* part = a.part + (size_t)t0 * a.E + i;
+                    double l = 0.0;
+#pragma unroll 4
+                    for (int sp = 0; sp < a.n_split; ++sp) l += __ldcg(part + (size_t)sp * a.T * a.E);
+                    const double s = 1.0 / (1.0 + exp(-l));
+                    S.scores[i] = s;
+                    S.keys[i] = sortable(s + (double)__ldg(a.bias + i % a.E));
+                }
+                group_any(2, false);
+                if (rw < nt) choose(a, t0 + rw, S.keys + (size_t)rw * a.E, S.scores + (size_t)rw * a.E, S);
+                group_any(2, false);
+            }
+            build_plan<DT>(a, P, S, tid);
             group_any(2, false);
             if (tid == 0) moe::mbar_arrive(&plan_ready);
         }
     } else if (warp == kWarps + kRouters) {
-        // ---------------------------------------------------------- producer
+        // ---------------------------------------------------------- weight producer
         const uint64_t policy = moe::l2_policy_evict_first();
-        bool ok = true;
         uint32_t issued = 0, last_phase = 0;   // slots in use, and their newest phase
-        auto claim = [&]() {
-            ok = __all_sync(0xffffffffu,
-                            moe::wait_bar(&ring.empty[ring.slot], ring.phase ^ 1, abort_flag, a.status));
-            return ok;
-        };
-        auto mark = [&]() {
+        Source<DT> src;
+        auto stage = [&](int k0, int kn) {
+            if (!wait(&ring.empty[ring.slot], ring.phase ^ 1)) return false;
+            src.stage(ring, k0, kn, policy);
             issued |= 1u << ring.slot;
             last_phase = (last_phase & ~(1u << ring.slot)) | (ring.phase << ring.slot);
+            ring.next();
+            return true;
         };
-        auto gate_up = [&](const Active& act, int n, int f0) {
-            Item it{act.expert, f0, n, a.H, act.mask, act.base, act.count, 0, 0};
-            for (; it.k0 < a.H; it.k0 += kChunk) {
-                it.kn = min(kChunk, a.H - it.k0);
-                if (!claim()) return;
-                issue_weights<DT>(a, it, false, ring, policy);
-                issue_acts<DT>(a, false, it.mask, 0, it.count, it.k0, it.kn, ring, ring.slot);
-                mark();
-                ring.next();
-            }
-        };
-        Shares sh = make_shares<DT>(a, first_routed);
-        for (int u = sh.s_at(cta); ok && u < sh.s_at(cta + 1); ++u) gate_up(shared, a.Is, u * NF);
-        if (ok) ok = __all_sync(0xffffffffu, moe::wait_bar(&plan_ready, 0, abort_flag, a.status));
+        bool ok = true;
+        for (int u = s0; ok && u < s1; ++u) {
+            src.unit(a, false, -1, u * NF);
+            ok = walk_unit(a, stage);
+        }
+        ok = ok && wait(&plan_ready, 0);
         if (ok) {
-            sh = make_shares<DT>(a, n_active_sh);
-            const int upe = a.I / NF;
-            for (int u = sh.r_at(cta); ok && u < sh.r_at(cta + 1); ++u)
-                gate_up(P.active[first_routed + u / upe], a.I, (u % upe) * NF);
-
-            // phase 2: lane i remembers what slot i still lacks
-            bool open = false;                 // barrier 1 has been passed
-            int lack = 0, l_base = 0, l_count = 0, l_k0 = 0, l_kn = 0;
-            auto supply = [&]() {
-                for (uint32_t m = __ballot_sync(0xffffffffu, lack); m; m &= m - 1) {
-                    const int sl = __ffs(m) - 1;
-                    issue_acts<DT>(a, true, 0, __shfl_sync(0xffffffffu, l_base, sl),
-                               __shfl_sync(0xffffffffu, l_count, sl), __shfl_sync(0xffffffffu, l_k0, sl),
-                               __shfl_sync(0xffffffffu, l_kn, sl), ring, sl);
-                }
-                lack = 0;
-            };
-            auto poll = [&]() {
-                int n = 0;
-                if (lane == 0) {
-                    n = *reinterpret_cast<volatile int*>(bars + 1);
-                }
-                n = __shfl_sync(0xffffffffu, n, 0);
-                __threadfence();               // heads and tails are read after the count
-                return n >= (int)gridDim.x;
-            };
-            long long pos = sh.b_at(cta);
-            const long long end = sh.b_at(cta + 1);
-            long long t0 = clock64();
-            while (ok && pos < end) {
-                const int rb = (int)(pos / sh.wsum);
-                int off = (int)(pos % sh.wsum);
-                int p, K;
-                if (off < sh.ws) {
-                    p = 0;
-                    K = a.Is;
-                } else {
-                    p = first_routed + (off - sh.ws) / sh.wi;
-                    off = (off - sh.ws) % sh.wi;
-                    K = a.I;
-                }
-                const Active act = P.active[p];
-                const int cols = chunk_cols(true, act.count);
-                const int left = (int)min((long long)(K / 128 - off), end - pos) * 128;
-                Item it{act.expert, rb * R, 0, K, act.mask, act.base, act.count, off * 128, min(cols, left)};
-                // a free slot, or barrier 1 so that the consumers can make one
-                while (true) {
-                    if (__all_sync(0xffffffffu, moe::mbar_try_wait(&ring.empty[ring.slot], ring.phase ^ 1))) break;
-                    if (!open && poll()) {
-                        open = true;
-                        supply();
-                    }
-                    bool late = false;
-                    if (lane == 0 && (*abort_flag || clock64() - t0 > moe::kWaitLimit)) {
-                        if (!*abort_flag) atomicOr(a.status, moe::DEV_STATUS_TIMEOUT);
-                        *abort_flag = 1;
-                        late = true;
-                    }
-                    if (__any_sync(0xffffffffu, late)) {
-                        ok = false;
-                        break;
-                    }
-                }
-                if (!ok) break;
-                t0 = clock64();
-                issue_weights<DT>(a, it, true, ring, policy);
-                mark();
-                if (open) {
-                    issue_acts<DT>(a, true, 0, it.base, it.count, it.k0, it.kn, ring, ring.slot);
-                } else if (lane == ring.slot) {
-                    lack = 1;
-                    l_base = it.base;
-                    l_count = it.count;
-                    l_k0 = it.k0;
-                    l_kn = it.kn;
-                }
-                ring.next();
-                pos += it.kn / 128;
+            for (int u = P.cut1[cta]; ok && u < P.cut1[cta + 1]; ++u) {
+                src.unit(a, false, P.active[first_routed + u / upe].expert, (u % upe) * NF);
+                ok = walk_unit(a, stage);
             }
-            while (ok && !open) {
-                if (poll()) {
-                    open = true;
-                    break;
-                }
-                bool late = false;
-                if (lane == 0 && (*abort_flag || clock64() - t0 > moe::kWaitLimit)) {
-                    if (!*abort_flag) atomicOr(a.status, moe::DEV_STATUS_TIMEOUT);
-                    *abort_flag = 1;
-                    late = true;
-                }
-                if (__any_sync(0xffffffffu, late)) ok = false;
-            }
-            supply();   // also when giving up: every stage's bytes then arrive
+            ok = ok && walk_down(a, P, n_active_sh, P.cut2[cta], P.cut2[cta + 1],
+                                 [&](int rb, const Active& act) {
+                                     src.unit(a, true, act.expert, rb * R);
+                                     return true;
+                                 },
+                                 stage, [](int) { return true; });
         }
         // no copy may still be in flight when the block leaves
         if (!ok)
             for (int i = 0; i < a.n_stages; ++i)
-                if (issued >> i & 1u) moe::wait_bar(&full[i], last_phase >> i & 1u, abort_flag, a.status, true);
+                if (issued >> i & 1u) moe::wait_bar(&bar_w[i], last_phase >> i & 1u, abort_flag, a.status, true);
+    } else if (warp > kWarps + kRouters) {
+        // ---------------------------------------------------------- activation producers
+        // warp j of kFeeders takes every kFeeders-th stage
+        int turn = kWarps + kRouters + 1 - warp;
+        auto mine = [&]() {
+            const bool m = turn == 0;
+            turn = turn == kFeeders - 1 ? 0 : turn + 1;
+            return m;
+        };
+        turn = turn < 0 ? turn + kFeeders : turn;
+        auto fed = [&]() {
+            arrive_copied(&ring.x[ring.slot]);
+        };
+        uint32_t mask = 0;
+        auto stage_x = [&](int k0, int kn) {
+            if (mine()) {
+                if (!wait(&ring.empty[ring.slot], ring.phase ^ 1)) return false;
+                uint32_t dst = moe::smem_addr(ring.stage() + off_x<DT>());
+                for (uint32_t m = mask; m; m &= m - 1, dst += x_stride<DT>(kChunk))
+                    copy_row(dst, a.x + (size_t)(__ffs(m) - 1) * a.H + k0, kn);
+                fed();
+            }
+            ring.next();
+            return true;
+        };
+        bool ok = true;
+        mask = shared.mask;
+        for (int u = s0; ok && u < s1; ++u) ok = walk_unit(a, stage_x);
+        ok = ok && wait(&plan_ready, 0);
+        if (ok) {
+            for (int u = P.cut1[cta]; ok && u < P.cut1[cta + 1]; ++u) {
+                mask = P.active[first_routed + u / upe].mask;
+                ok = walk_unit(a, stage_x);
+            }
+            // barrier 1: every block's heads and tails are written
+            bool late = false;
+            if (ok && lane == 0) {
+                const long long t0 = clock64();
+                while (*reinterpret_cast<volatile int*>(bars + 1) < G) {
+                    if (*abort_flag || clock64() - t0 > moe::kWaitLimit) {
+                        if (!*abort_flag) atomicOr(a.status, moe::DEV_STATUS_TIMEOUT);
+                        *abort_flag = 1;
+                        late = true;
+                        break;
+                    }
+                }
+            }
+            ok = ok && !__any_sync(0xffffffffu, late);
+            __threadfence();
+            const uint16_t *hi = nullptr, *lo = nullptr;
+            int count = 0, xs = 0;
+            if (ok)
+                walk_down(a, P, n_active_sh, P.cut2[cta], P.cut2[cta + 1],
+                          [&](int, const Active& act) {
+                              hi = a.act_hi + (size_t)act.base * a.ld_act;
+                              lo = a.act_lo + (size_t)act.base * a.ld_act;
+                              count = act.count;
+                              xs = x_stride<DT>(chunk_cols(true, count));
+                              return true;
+                          },
+                          [&](int k0, int kn) {
+                              if (mine()) {
+                                  if (!wait(&ring.empty[ring.slot], ring.phase ^ 1)) return false;
+                                  uint32_t dst = moe::smem_addr(ring.stage() + off_x<DT>());
+                                  const uint16_t *h = hi + k0, *l = lo + k0;
+                                  const uint32_t tail = (uint32_t)(count * xs);
+                                  for (int i = 0; i < count; ++i, dst += xs, h += a.ld_act, l += a.ld_act) {
+                                      copy_row(dst, h, kn);
+                                      copy_row(dst + tail, l, kn);
+                                  }
+                                  fed();
+                              }
+                              ring.next();
+                              return true;
+                          },
+                          [](int) { return true; });
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
     } else {
         // ---------------------------------------------------------- consumers
-        const int tid = threadIdx.x;
-        const int g = lane >> 2, t = lane & 3;
+        const int tid = threadIdx.x, g = lane >> 2, t = lane & 3;
+        router_phase(a, warp);
+        __threadfence();
+        asm volatile("barrier.cta.arrive 3, %0;" ::"r"(kGroup + kRouterGroup) : "memory");
         bool ok = true;
         float acc[MT][NT][4];
+        Columns<NT> col;
+        int count = 0;
         auto clear = [&]() {
 #pragma unroll
             for (int m = 0; m < MT; ++m)
@@ -938,30 +1006,13 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
 #pragma unroll
                     for (int j = 0; j < 4; ++j) acc[m][i][j] = 0.0f;
         };
-        // one stage; false when the wait was given up
-        auto stage_gate_up = [&](const Item& it) {
-            int xrow[NT];
-#pragma unroll
-            for (int i = 0; i < NT; ++i) xrow[i] = 8 * i + g < it.count ? 8 * i + g : 0;
-            ok = __all_sync(0xffffffffu, moe::wait_bar(&full[ring.slot], ring.phase, abort_flag, a.status));
-            if (!ok) return;
-            mma_stage<DT, NT, false>(it, ring.base + ring.slot * a.stage_bytes, warp, xrow, it.count > 8, acc);
-            __syncwarp();
-            if (lane == 0) moe::mbar_arrive(&empty[ring.slot]);
-            ring.next();
+        auto ready = [&]() {
+            ok = wait(&ring.w[ring.slot], ring.phase) && wait(&ring.x[ring.slot], ring.phase);
+            return ok;
         };
-        auto stage_down = [&](const Item& it) {
-            int xrow[NT];
-#pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                const int tok = 8 * i + g;
-                xrow[i] = it.mask >> tok & 1u ? __popc(it.mask & ((1u << tok) - 1u)) : -1;
-            }
-            ok = __all_sync(0xffffffffu, moe::wait_bar(&full[ring.slot], ring.phase, abort_flag, a.status));
-            if (!ok) return;
-            mma_stage<DT, NT, true>(it, ring.base + ring.slot * a.stage_bytes, warp, xrow, it.mask >> 8, acc);
+        auto release = [&]() {
             __syncwarp();
-            if (lane == 0) moe::mbar_arrive(&empty[ring.slot]);
+            if (lane == 0) moe::mbar_arrive(&ring.empty[ring.slot]);
             ring.next();
         };
         // Leaves the warps' sums in red (once the last ones have been read)
@@ -990,13 +1041,18 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
             }
             return s;
         };
-        auto gate_up = [&](const Active& act, int n, int f0) {
+        auto gate_up = [&](const Active& act, int f0) {
             clear();
-            Item it{act.expert, f0, n, a.H, act.mask, act.base, act.count, 0, 0};
-            for (; ok && it.k0 < a.H; it.k0 += kChunk) {
-                it.kn = min(kChunk, a.H - it.k0);
-                stage_gate_up(it);
-            }
+            count = act.count;
+#pragma unroll
+            for (int i = 0; i < NT; ++i) col.row[i] = 8 * i + g < count ? 8 * i + g : 0;
+            col.tile1 = count > 8;
+            walk_unit(a, [&](int, int kn) {
+                if (!ready()) return false;
+                if (warp * kSlice < kn) mma_stage<DT, NT, false, FOLD>(ring.stage(), warp, count, col, acc);
+                release();
+                return true;
+            });
             if (gather()) return false;
             if (tid < MT * NT * 32) {
                 const float4 s = reduced();
@@ -1004,7 +1060,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
                 const float gate[2] = {s.x, s.y}, up[2] = {s.z, s.w};
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    if (c0 + j >= act.count) continue;
+                    if (c0 + j >= count) continue;
                     const int pair = act.base + c0 + j;
                     float v = gate[j] / (1.0f + expf(-gate[j])) * up[j];
                     if (act.expert >= 0) v *= P.pairw[pair];
@@ -1020,52 +1076,58 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
         };
 
         bool good = true;
-        Shares sh = make_shares<DT>(a, first_routed);
-        for (int u = sh.s_at(cta); good && u < sh.s_at(cta + 1); ++u) good = gate_up(shared, a.Is, u * NF);
+        for (int u = s0; good && u < s1; ++u) good = gate_up(shared, u * NF);
         if (good) {
-            ok = __all_sync(0xffffffffu, moe::wait_bar(&plan_ready, 0, abort_flag, a.status));
+            ok = wait(&plan_ready, 0);
             good = !group_any(1, !ok);
         }
-        if (good) {
-            sh = make_shares<DT>(a, n_active_sh);
-            const int upe = a.I / NF;
-            for (int u = sh.r_at(cta); good && u < sh.r_at(cta + 1); ++u)
-                good = gate_up(P.active[first_routed + u / upe], a.I, (u % upe) * NF);
-        }
+        if (good)
+            for (int u = P.cut1[cta]; good && u < P.cut1[cta + 1]; ++u)
+                good = gate_up(P.active[first_routed + u / upe], (u % upe) * NF);
         if (good) {
             // barrier 1: this block's heads and tails are written
             __threadfence();
             group_any(1, false);
             if (tid == 0) atomicAdd(bars + 1, 1);
-            long long pos = sh.b_at(cta);
-            const long long begin = pos, end = sh.b_at(cta + 1);
-            while (good && pos < end) {
-                const int rb = (int)(pos / sh.wsum);
-                const long long lo = (long long)rb * sh.wsum, hi = lo + sh.wsum;
-                const long long seg0 = pos, seg1 = min(hi, end);
-                clear();
-                while (ok && pos < seg1) {
-                    int off = (int)(pos - lo), p, K;
-                    if (off < sh.ws) {
-                        p = 0;
-                        K = a.Is;
-                    } else {
-                        p = first_routed + (off - sh.ws) / sh.wi;
-                        off = (off - sh.ws) % sh.wi;
-                        K = a.I;
-                    }
-                    const Active act = P.active[p];
-                    const int left = (int)min((long long)(K / 128 - off), end - pos) * 128;
-                    Item it{act.expert, rb * R, 0, K, act.mask, act.base, act.count, off * 128,
-                            min(chunk_cols(true, act.count), left)};
-                    stage_down(it);
-                    pos += it.kn / 128;
+            const int begin = P.cut2[cta], end = P.cut2[cta + 1];
+            const int wsum = a.Is / 128 + (n_active_sh - first_routed) * (a.I / 128);
+            clear();
+            auto item = [&](int, const Active& act) {
+                count = act.count;
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    const int tok = FOLD ? g & 3 : 8 * i + g;
+                    const bool has = act.mask >> tok & 1u;
+                    col.zero[i] = !has;
+                    col.row[i] = has ? __popc(act.mask & ((1u << tok) - 1u)) + (FOLD && g >= 4 ? count : 0) : 0;
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        col.own[i][j] = act.mask >> (FOLD ? (2 * t + j) & 3 : 8 * i + 2 * t + j) & 1u;
                 }
-                if (gather()) break;
-                const bool whole = seg0 == lo && seg1 == hi;
-                float* mine = a.join + ((size_t)cta * 2 + (seg0 == begin ? 0 : 1)) * a.T * R;
+                col.tile1 = act.mask >> 8;
+                return true;
+            };
+            auto stage = [&](int, int kn) {
+                // a given-up wait ends in row_end, which all warps reach
+                if (ok && ready()) {
+                    if (warp * kSlice < kn) mma_stage<DT, NT, true, FOLD>(ring.stage(), warp, count, col, acc);
+                    release();
+                }
+                return true;
+            };
+            auto row_end = [&](int rb) {
+                if (gather()) return false;
+                const int lo = rb * wsum, hi = lo + wsum;
+                const bool whole = begin <= lo && hi <= end;
+                float* mine = a.join + ((size_t)cta * 2 + (begin >= lo ? 0 : 1)) * a.T * R;
                 if (tid < MT * NT * 32) {
-                    const float4 s = reduced();
+                    float4 s = reduced();
+                    if (FOLD) {   // columns 4-7 hold the tails' sums of columns 0-3
+                        s.x += __shfl_down_sync(0xffffffffu, s.x, 2);
+                        s.y += __shfl_down_sync(0xffffffffu, s.y, 2);
+                        s.z += __shfl_down_sync(0xffffffffu, s.z, 2);
+                        s.w += __shfl_down_sync(0xffffffffu, s.w, 2);
+                    }
                     const int r = tid / (32 * NT) * 16 + g, c0 = tid / 32 % NT * 8 + 2 * t;
                     const float v[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
@@ -1080,15 +1142,15 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
                         }
                     }
                 }
-                if (whole) continue;
+                clear();
+                if (whole) return true;
                 // a row block of several blocks: the last to leave its part
                 // adds them up in block order
-                int c0 = cta, c1 = cta;
-                while (c0 > 0 && sh.b_at(c0) > lo) --c0;
-                while (c1 + 1 < sh.G && sh.b_at(c1 + 1) < hi) ++c1;
+                int c0 = cta, c1 = cta + 1;
+                while (P.cut2[c0] > lo) --c0;
+                while (P.cut2[c1] < hi) ++c1;
                 int parts = 0;
-                for (int c = c0; c <= c1; ++c)
-                    parts += min(sh.b_at(c + 1), hi) > max(sh.b_at(c), lo);
+                for (int c = c0; c < c1; ++c) parts += P.cut2[c] < P.cut2[c + 1];
                 __threadfence();
                 group_any(1, false);
                 if (tid == 0) {
@@ -1099,22 +1161,21 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
                 if (last_sh) {
                     for (int i = tid; i < a.T * R; i += kGroup) {
                         float s = 0.0f;
-                        for (int c = c0; c <= c1; ++c) {
-                            const long long b0 = sh.b_at(c);
-                            if (min(sh.b_at(c + 1), hi) <= max(b0, lo)) continue;
-                            s += __ldcg(a.join + ((size_t)c * 2 + (b0 >= lo ? 0 : 1)) * a.T * R + i);
-                        }
+                        for (int c = c0; c < c1; ++c)
+                            if (P.cut2[c] < P.cut2[c + 1])
+                                s += __ldcg(a.join + ((size_t)c * 2 + (P.cut2[c] >= lo ? 0 : 1)) * a.T * R + i);
                         const __nv_bfloat16 b = __float2bfloat16_rn(s);
                         a.out[(size_t)(i / R) * a.H + rb * R + i % R] = *reinterpret_cast<const uint16_t*>(&b);
                     }
                 }
-                group_any(1, false);   // last_sh is read before the next one is written
-            }
+                return true;   // gather's first barrier keeps last_sh until every thread has read it
+            };
+            walk_down(a, P, n_active_sh, begin, end, item, stage, row_end);
         }
     }
     __syncthreads();
     // the last block to leave clears the counters for the next launch
-    if (threadIdx.x == 0 && atomicAdd(bars + 2, 1) == (int)gridDim.x - 1) {
+    if (threadIdx.x == 0 && atomicAdd(bars + 2, 1) == G - 1) {
         bars[0] = 0;
         bars[1] = 0;
         bars[2] = 0;
@@ -1124,19 +1185,20 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
 // ------------------------------------------------------------------ host side
 size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
 
-constexpr int kMaxBlocks = 256;       // blocks the join buffer has room for
-
 struct FewLayout {
     size_t part, hi, lo, join, joined, total;
     int n_split, ld_act;
 };
 
-// K slices of the router: enough that every router warp of the grid has one.
+// K slices of the router: enough that every warp has one, and short enough for
+// a lane's registers.
 FewLayout few_layout(const moe_config_t* c) {
     FewLayout L{};
-    const int nch = c->H / 256 > 0 ? c->H / 256 : 1;
-    int split = 148 * kRouters / c->E;
-    split = split < 1 ? 1 : split > nch ? nch : split;
+    const int nch = c->H / 8;
+    int split = 148 * (kWarps + kRouters) / c->E;
+    const int lo = (nch + 32 * kRouterVecs - 1) / (32 * kRouterVecs), hi = nch / 32 > 0 ? nch / 32 : 1;
+    split = split > hi ? hi : split;
+    split = split < lo ? lo : split;
     L.n_split = split;
     const int Is = c->n_shared * c->I;
     L.ld_act = Is > c->I ? Is : c->I;
@@ -1181,6 +1243,10 @@ moe_status_t few_check(const moe_config_t* c) {
     FEW_TRY(moe::api_check_config(&b));
     if (c->T > kT)
         return ffail(MOE_ERR_UNSUPPORTED, "%s=%lld is above %lld: use moe_forward", "T", c->T, kT);
+    // the shares are counted in 32 bits: steps of 16 rows by 128 columns
+    const long long act = (long long)c->T * c->k + c->n_shared, blocks = (long long)(c->H / 16) * (c->I / 128);
+    if (act * blocks > (1ll << 28) || act * (c->I / 8) > (1ll << 22) || (long long)c->E * 2 * c->I > (1ll << 31))
+        return ffail(MOE_ERR_UNSUPPORTED, "%s H=%lld, I=%lld too large", "few-token layer:", c->H, c->I);
     return MOE_OK;
 }
 
@@ -1229,9 +1295,11 @@ moe_status_t few_smem(FewArgs& a, int limit, size_t* bytes) {
     a.off_active = off;
     off += active * (int)sizeof(Active);
     a.off_pairw = off;
-    off = up(off + (n + a.T) * 4, 16);
+    off += (n + a.T) * 4;
+    a.off_cuts = off;
+    off = up(off + 2 * (kMaxBlocks + 1) * 4, 16);
     a.off_scratch = off;
-    off = up(off + (a.T < kRouters ? a.T : kRouters) * a.E * 8 + n * 8 + a.E * 8, 16);
+    off = up(off + (a.T < kRouters ? a.T : kRouters) * a.E * 16 + n * 8 + a.E * 8, 16);
     a.off_red = off;
     off += kWarps * (F::kRows / 16) * NT * 512;
     a.off_ring = up(off, 1024);
@@ -1240,29 +1308,32 @@ moe_status_t few_smem(FewArgs& a, int limit, size_t* bytes) {
     a.stage_bytes = up(off_x<DT>() + x, 512);
     const int stages = (limit - a.off_ring) / a.stage_bytes;
     a.n_stages = stages < kMaxStages ? stages : kMaxStages;
-    if (a.n_stages < 2)
-        return ffail(MOE_ERR_UNSUPPORTED, "%s: %lld bytes of shared memory hold fewer than two stages", "few-token layer",
+    // a feeder that waits for a slot has last waited kFeeders stages before:
+    // with fewer slots than that it could take an old phase for the new one
+    if (a.n_stages < kFeeders)
+        return ffail(MOE_ERR_UNSUPPORTED, "%s: %lld bytes of shared memory hold too few stages", "few-token layer",
                      limit);
     *bytes = (size_t)a.off_ring + (size_t)a.n_stages * a.stage_bytes;
     return MOE_OK;
 }
 
-template <int DT, int NT>
+template <int DT, int NT, bool FOLD>
 moe_status_t launch_few(FewArgs& a, cudaStream_t s) {
+    void (*kernel)(FewArgs) = few_kernel<DT, NT, FOLD>;
     int sms = 0, dev = 0, optin = 0;
     FEW_TRY(moe::api_sm_count(&sms));
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
     cudaFuncAttributes fa;
-    if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, few_kernel<DT, NT>);
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, kernel);
     if (e == cudaSuccess) {
         size_t smem = 0;
         FEW_TRY((few_smem<DT, NT>(a, optin - (int)fa.sharedSizeBytes, &smem)));
-        e = cudaFuncSetAttribute(few_kernel<DT, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e == cudaSuccess) {
             void* args[] = {&a};
             const int grid = sms < kMaxBlocks ? sms : kMaxBlocks;
-            e = cudaLaunchCooperativeKernel(few_kernel<DT, NT>, dim3(grid), dim3(kThreads), args, smem, s);
+            e = cudaLaunchCooperativeKernel(kernel, dim3(grid), dim3(kThreads), args, smem, s);
         }
     }
     if (e != cudaSuccess) return ffail(MOE_ERR_CUDA, "few-token layer launch: %s", cudaGetErrorString(e));
@@ -1273,7 +1344,8 @@ template <int DT>
 moe_status_t launch_tiles(FewArgs& a, const void* w13, const void* w2, const void* w13s, const void* w2s,
                           cudaStream_t s) {
     FEW_TRY(few_maps<DT>(a, w13, w2, w13s, w2s));
-    return a.T <= 8 ? launch_few<DT, 1>(a, s) : launch_few<DT, 2>(a, s);
+    if (a.T <= 4) return launch_few<DT, 1, true>(a, s);
+    return a.T <= 8 ? launch_few<DT, 1, false>(a, s) : launch_few<DT, 2, false>(a, s);
 }
 
 }  // namespace
