@@ -7,23 +7,23 @@
 // one block per SM, each block walking its share of the weight rows through a
 // shared-memory ring while the multiplications keep up behind it.
 //
-// Roles in a block (16 warps):
-//   warp 12     weight producer: tensor copies of the weights (and scales),
+// Roles in a block (21 warps):
+//   warps 0-15  consumers, two teams of eight that take stages in turn:
+//               m16n8k16 matrix instructions, 16 weight rows by 8 tokens; the
+//               tokens are the short side, so the 128-row tiles of tcgen05
+//               would be coarse units to share out over 148 SMs (a decode
+//               token touches 1728 16-row units but 216 of 128 rows), and 4-
+//               and 8-bit weights have to be widened in registers anyway.
+//               The second team first makes the choice and the plan of touched
+//               experts, while the first works on the shared expert, which
+//               needs neither
+//   warp 16     weight producer: tensor copies of the weights (and scales),
 //               stage by stage, as far ahead as the ring is deep
-//   warps 13-15 activation producers: the rows that the weights meet
-//   warps 0-7   consumers: m16n8k16 matrix instructions, 16 weight rows by 8
-//               tokens; the tokens are the short side, so the 128-row tiles
-//               of tcgen05 would be coarse units to share out over 148 SMs
-//               (a decode token touches 1728 16-row units but 216 of 128
-//               rows), and 4- and 8-bit weights need their values widened in
-//               registers anyway
-//   warps 8-11  router: logits, choice and the plan of touched experts, while
-//               the consumers already work on the shared expert, which needs
-//               no choice
+//   warps 17-20 activation producers: the rows that the weights meet
 //
 // Phases:
-//   R   a warp per (expert, K slice) of the logits; grid barrier 0; then every
-//       block repeats the choice (T * E keys) and the plan
+//   R   a team per expert's logits; grid barrier 0; then every block repeats
+//       the choice (T * E keys) and the plan
 //   1   units of nf SwiGLU features of one expert (nf gate rows, nf up rows,
 //       all of K): SiLU(g) * u * w leaves as a bf16 head and a bf16 tail (16
 //       significand bits) in the workspace; grid barrier 1
@@ -32,11 +32,12 @@
 //       is joined by the last of them, in block order
 // The weight producer does not wait for barrier 1; only the activations do.
 //
-// 8- and 4-bit weights become bf16 by moving their bits into a bf16's sign,
-// exponent and mantissa fields (e4m3 as value * 2^-120, e2m1 as value *
-// 2^-126: subnormals stay subnormals, so no case is special) and one exact
-// bf16 product that brings them back; their block scales multiply the products
-// in fp32.  Nothing is rounded on the way.
+// 8- and 4-bit weights become binary16 by one conversion for two weights
+// (exact: both types lie inside it), and the activations meet them in binary16
+// too: a warp scales its 64 columns of a token by the power of two that takes
+// the largest to 2^14, which keeps every bit of a bf16 value down to 2^-28 of
+// the largest and is off by 2^-39 of it below; the sums are brought back in
+// fp32 together with the weights' block scales.
 #include "moe.h"
 #include "kernels.cuh"
 #include "ptx.cuh"
@@ -60,13 +61,16 @@ moe_status_t api_make_map_u8_sw64(CUtensorMap* m, const void* ptr, uint32_t rank
 namespace {
 
 constexpr int kT = MOE_FEW_MAX_T;
-constexpr int kWarps = 8;                        // consumers
-constexpr int kRouters = 4;
-constexpr int kFeeders = 3;                      // warps that copy activations
-constexpr int kGroup = kWarps * 32, kRouterGroup = kRouters * 32;
-constexpr int kThreads = kGroup + kRouterGroup + 32 + kFeeders * 32;
-constexpr int kRouterVecs = 4;                   // 16-byte vectors of a router lane
+constexpr int kWarps = 8;                        // of a team of consumers
+constexpr int kFeeders = 4;                      // warps that copy activations
+constexpr int kTeam = kWarps * 32, kConsumers = 2 * kTeam;
+constexpr int kThreads = kConsumers + 32 + kFeeders * 32;
+constexpr int kRouterVecs = 4;                   // 16-byte vectors of a router lane at a time
 constexpr int kMaxBlocks = 256;                  // blocks the join buffer has room for
+constexpr int kHeadStart = 3;                    // stages copied before the router's loads are in
+constexpr int kAhead = 64;                       // steps of 128 columns fetched into L2 across barrier 1
+// named barriers
+constexpr int kBarAll = 1, kBarB = 2, kBarRouted = 3, kBarA = 4, kBarLogits = 5;
 constexpr int kChunk = 512;                      // K columns of a full stage
 constexpr int kBox = 256;                        // K columns of one tensor copy
 constexpr int kBoxBytes = 8192;                  // its bytes, for every weight type
@@ -104,12 +108,13 @@ struct FewArgs {
     int32_t* idx;
     float* w;
     int* status;
-    double* part;               // [n_split][T][E] logits of the K slices
+    double* logits;             // [T][E]
     uint16_t *act_hi, *act_lo;  // [pairs][ld_act] weighted SwiGLU outputs, head and tail
     float* join;                // [blocks][2][T][rows] partial sums of shared row blocks
     int* joined;                // [row blocks] blocks that have left theirs
-    int T, H, E, k, I, Is, n_group, topk_group, group_topn, norm, n_split, stall, ld_act;
+    int T, H, E, k, I, Is, n_group, topk_group, group_topn, norm, stall, ld_act, batch;
     float rsf;
+    double inv_g;               // 1 / blocks
     // shared-memory layout (bytes)
     int off_active, off_pairw, off_cuts, off_scratch, off_red, off_ring, stage_bytes, n_stages;
 };
@@ -130,9 +135,9 @@ struct Plan {
     int* n_active;
 };
 
-// Scratch of the router warps; the consumers' reduction buffer is apart.
+// Scratch of the choice; the consumers' reduction buffer is apart.
 struct Scratch {
-    unsigned long long* keys;   // [min(T, kRouters)][E]
+    unsigned long long* keys;   // [batch][E]
     double* scores;    // the same
     int* sel;          // [T, k]
     float* selw;       // [T, k]
@@ -149,7 +154,7 @@ __device__ __forceinline__ void unpack8(const uint4& v, float* f) {
     }
 }
 
-// Barrier of the consumers (id 1) or the router warps (id 2); true when any of
+// Barrier of both teams (kBarAll) or of one (kBarA, kBarB); true when any of
 // their threads says `bad`.
 __device__ __forceinline__ bool group_any(int id, bool bad) {
     int r;
@@ -157,9 +162,15 @@ __device__ __forceinline__ bool group_any(int id, bool bad) {
         "{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %2, 0;\n\t"
         "barrier.cta.red.or.pred q, %1, %3, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
         : "=r"(r)
-        : "r"(id), "r"((int)bad), "r"(id == 1 ? kGroup : kRouterGroup)
+        : "r"(id), "r"((int)bad), "r"(id == kBarAll ? kConsumers : kTeam)
         : "memory");
     return r != 0;
+}
+__device__ __forceinline__ void bar_sync(int id, int n) {
+    asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(int id, int n) {
+    asm volatile("barrier.cta.arrive %0, %1;" ::"r"(id), "r"(n) : "memory");
 }
 
 // Tensor copies of one box, with an L2 policy.
@@ -180,6 +191,14 @@ __device__ __forceinline__ void box_load_5d(uint32_t dst, const CUtensorMap* m, 
         : "memory");
 }
 
+// The same boxes into L2 only.
+__device__ __forceinline__ void box_fetch_4d(const CUtensorMap* m, int c2, int c3) {
+    asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %1, %2, %3}];" ::"l"(
+                     reinterpret_cast<uint64_t>(m)),
+                 "r"(0), "r"(c2), "r"(c3)
+                 : "memory");
+}
+
 // Asynchronous copies of 16 or 4 bytes by this thread, and its arrival on
 // `bar` once all of them have landed.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
@@ -192,11 +211,19 @@ __device__ __forceinline__ void arrive_copied(uint64_t* bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(moe::smem_addr(bar)) : "memory");
 }
 
-__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9},"
-        " {%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+// D += A B: bf16 operands for bf16 weights, binary16 for the others.
+template <bool BF16>
+__device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if (BF16)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9},"
+            " {%0, %1, %2, %3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9},"
+            " {%0, %1, %2, %3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
 // e8m0 scale byte -> binary32 (0 is 2^-127, 255 NaN)
@@ -205,48 +232,52 @@ __device__ __forceinline__ float e8m0(uint32_t s) {
 }
 
 // ------------------------------------------------------------------ router
-// Logits of expert e over one K slice, one warp each (router and consumer
-// warps).  Eight exact products are summed in binary32, those sums in
-// binary64: the logit's error stays near 2^-25 of a partial sum, far below the
-// gap of two keys.  A lane keeps its weights of the slice in registers and
-// walks the tokens.
-__device__ void router_phase(const FewArgs& a, int warp) {
-    const int lane = threadIdx.x & 31;
-    const int nch = a.H / 8;
-    const int per = (nch + a.n_split - 1) / a.n_split;    // at most 32 * kRouterVecs
-    const int units = a.E * a.n_split;
-    for (int u = blockIdx.x * (kWarps + kRouters) + warp; u < units; u += gridDim.x * (kWarps + kRouters)) {
-        const int e = u / a.n_split, sp = u % a.n_split;
-        const int c0 = sp * per + lane, c1 = min(nch, (sp + 1) * per);
+// Logits of expert e by one team: a warp sums a slice of K for every token,
+// the slices are joined in order.  Eight exact products are summed in
+// binary32, those sums in binary64: the logit's error stays near 2^-25 of a
+// partial sum, far below the gap of two keys.  `part`: [kWarps][kT] of the team.
+__device__ void router_phase(const FewArgs& a, int team, int warp, double (*part)[kT]) {
+    const int lane = threadIdx.x & 31, tid = threadIdx.x - team * kTeam;
+    const int nch = a.H / 8, per = (nch + kWarps - 1) / kWarps;
+    const int c1 = min(nch, (warp + 1) * per);
+    for (int e = blockIdx.x + team * gridDim.x; e < a.E; e += 2 * gridDim.x) {
         const uint4* wr = reinterpret_cast<const uint4*>(a.w_router + (size_t)e * a.H);
-        const uint4* xr = reinterpret_cast<const uint4*>(a.x);
-        uint4 w[kRouterVecs];
-#pragma unroll
-        for (int i = 0; i < kRouterVecs; ++i)
-            w[i] = c0 + 32 * i < c1 ? __ldg(wr + c0 + 32 * i) : make_uint4(0, 0, 0, 0);
-        double* out = a.part + (size_t)sp * a.T * a.E + e;
-#pragma unroll 2
-        for (int t = 0; t < a.T; ++t) {
-            uint4 x[kRouterVecs];
+        bool first = true;
+        for (int c0 = warp * per + lane; first || c0 - lane < c1; c0 += 32 * kRouterVecs, first = false) {
+            uint4 w[kRouterVecs];
 #pragma unroll
             for (int i = 0; i < kRouterVecs; ++i)
-                x[i] = c0 + 32 * i < c1 ? __ldg(xr + c0 + 32 * i) : make_uint4(0, 0, 0, 0);
-            double acc = 0.0;
+                w[i] = c0 + 32 * i < c1 ? __ldg(wr + c0 + 32 * i) : make_uint4(0, 0, 0, 0);
+            const uint4* xr = reinterpret_cast<const uint4*>(a.x);
+#pragma unroll 2
+            for (int t = 0; t < a.T; ++t, xr += nch) {
+                uint4 x[kRouterVecs];
 #pragma unroll
-            for (int i = 0; i < kRouterVecs; ++i) {
-                float wf[8], xf[8], s = 0.0f;
-                unpack8(w[i], wf);
-                unpack8(x[i], xf);
+                for (int i = 0; i < kRouterVecs; ++i)
+                    x[i] = c0 + 32 * i < c1 ? __ldg(xr + c0 + 32 * i) : make_uint4(0, 0, 0, 0);
+                double acc = 0.0;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) s = fmaf(wf[j], xf[j], s);
-                acc += (double)s;
+                for (int i = 0; i < kRouterVecs; ++i) {
+                    float wf[8], xf[8], s = 0.0f;
+                    unpack8(w[i], wf);
+                    unpack8(x[i], xf);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) s = fmaf(wf[j], xf[j], s);
+                    acc += (double)s;
+                }
+#pragma unroll
+                for (int off = 16; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
+                if (lane == 0) part[warp][t] = first ? acc : part[warp][t] + acc;
             }
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
-            if (lane == 0) *out = acc;
-            out += a.E;
-            xr += nch;
         }
+        group_any(team ? kBarB : kBarA, false);
+        if (tid < a.T) {
+            double l = 0.0;
+#pragma unroll
+            for (int q = 0; q < kWarps; ++q) l += part[q][tid];
+            a.logits[(size_t)tid * a.E + e] = l;
+        }
+        group_any(team ? kBarB : kBarA, false);
     }
 }
 
@@ -359,10 +390,14 @@ __device__ void choose(const FewArgs& a, int t, const unsigned long long* key, c
 // ------------------------------------------------------------------ shares
 // What block c of G works on.  Phase 1: units of the shared expert (known
 // before the choice) and of the routed ones, each cut into G contiguous runs.
-// Phase 2: the (row block, expert, K) axis in steps of 128 columns, cut at
-// even steps of an expert.  Every step moves the same bytes as H / 128 of a
-// unit, so phase 2's cuts make up for what phase 1's whole units leave uneven.
-__device__ __forceinline__ int cut(int c, int n, int G) { return (int)((unsigned)c * (unsigned)n / (unsigned)G); }
+// Phase 2: the (row block, expert, K) axis in steps of 128 columns.  Every
+// step moves the same bytes as H / 128 of a unit, so phase 2's cuts make up
+// for what phase 1's whole units leave uneven.
+// c * n / G, rounded down: the product's fraction is a multiple of 1 / G, far
+// more than binary64 loses.
+__device__ __forceinline__ int cut(const FewArgs& a, int c, int n) {
+    return (int)((double)c * ((double)n * a.inv_g) + 1e-6);
+}
 
 // Cuts of the routed units and of phase 2, by threads tid of n.
 template <int DT>
@@ -370,41 +405,37 @@ __device__ void make_cuts(const FewArgs& a, const Plan& P, int n_active, int tid
     constexpr int R = Fmt<DT>::kRows;
     const int G = gridDim.x, routed = n_active - (a.Is ? 1 : 0);
     const int us = a.Is / (R / 2), ur = routed * (a.I / (R / 2)), ublk = a.H / 128;
-    const int ws = a.Is / 128, wi = a.I / 128, wsum = ws + routed * wi;
-    const int tot2 = a.H / R * wsum, tot = (us + ur) * ublk + tot2;
+    const int tot2 = a.H / R * (a.Is / 128 + routed * (a.I / 128)), tot = (us + ur) * ublk + tot2;
     // Taking earlier shares into account needs each to fit under the even
     // share of the whole, or the cuts would run backwards.
-    const bool joint1 = (us + ur) / G >= (us + G - 1) / G;
-    const int most = joint1 ? (us + ur + G - 1) / G : (us + G - 1) / G + (ur + G - 1) / G;
-    const bool joint2 = tot / G >= most * ublk;
+    const int lo = cut(a, 1, us + ur), s_most = cut(a, 1, us + G - 1);
+    const bool joint1 = lo >= s_most;
+    const int most = joint1 ? cut(a, 1, us + ur + G - 1) : s_most + cut(a, 1, ur + G - 1);
+    const bool joint2 = cut(a, 1, tot) >= most * ublk;
     for (int c = tid; c <= G; c += n) {
-        const int s = cut(c, us, G);
-        const int r = joint1 ? cut(c, us + ur, G) - s : cut(c, ur, G);
-        int b = tot2;
-        if (c < G) {
-            b = joint2 ? (int)((double)c * ((double)tot / G)) - (s + r) * ublk : (int)((double)c * ((double)tot2 / G));
-            const int off = b % wsum;
-            b -= (off < ws ? off : (off - ws) % wi) & 1;
-        }
+        const int s = cut(a, c, us);
+        const int r = joint1 ? cut(a, c, us + ur) - s : cut(a, c, ur);
         P.cut1[c] = r;
-        P.cut2[c] = b;
+        P.cut2[c] = joint2 ? cut(a, c, tot) - (s + r) * ublk : cut(a, c, tot2);
     }
 }
 
 // Touched experts in ascending order after the shared one, with their tokens
-// and pairs, and the blocks' shares.  All router threads; `tid` within them.
+// and pairs, and the blocks' shares.  Team B; `tid` within it.
 template <int DT>
 __device__ void build_plan(const FewArgs& a, const Plan& P, const Scratch& S, int tid) {
-    const int lane = tid & 31;
+    const int lane = tid & 31, first = a.Is ? 1 : 0;
+    // lane l takes experts l * E / 32 and on
+    const int per = a.E / 32;
+    int n = 0, pairs = 0;
+#pragma unroll 8
+    for (int i = 0; i < per; ++i) {
+        const uint32_t m = S.emask[lane * per + i];
+        n += m != 0;
+        pairs += __popc(m);
+    }
+    const int n_active = first + __reduce_add_sync(0xffffffffu, n);
     if (tid < 32) {
-        // lane l takes experts l * E / 32 and on
-        const int per = a.E / 32;
-        int n = 0, pairs = 0;
-        for (int i = 0; i < per; ++i) {
-            const uint32_t m = S.emask[lane * per + i];
-            n += m != 0;
-            pairs += __popc(m);
-        }
         const int n0 = n, p0 = pairs;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
@@ -414,8 +445,7 @@ __device__ void build_plan(const FewArgs& a, const Plan& P, const Scratch& S, in
                 pairs += w;
             }
         }
-        const int first = a.Is ? 1 : 0;
-        if (lane == 31) *P.n_active = first + n;
+        if (lane == 0) *P.n_active = n_active;
         int at = first + n - n0, base = (a.Is ? a.T : 0) + pairs - p0;
         for (int i = 0; i < per; ++i) {
             const int e = lane * per + i;
@@ -426,12 +456,13 @@ __device__ void build_plan(const FewArgs& a, const Plan& P, const Scratch& S, in
             base += __popc(m);
         }
         if (a.Is && lane == 0) P.active[0] = Active{-1, (1u << a.T) - 1u, 0, a.T};
+    } else {
+        make_cuts<DT>(a, P, n_active, tid - 32, kTeam - 32);
     }
-    group_any(2, false);
-    make_cuts<DT>(a, P, *P.n_active, tid, kRouterGroup);
+    group_any(kBarB, false);
     if (a.Is)
-        for (int t = tid; t < a.T; t += kRouterGroup) P.pairw[t] = 1.0f;
-    for (int i = tid; i < a.T * a.k; i += kRouterGroup) {
+        for (int t = tid; t < a.T; t += kTeam) P.pairw[t] = 1.0f;
+    for (int i = tid; i < a.T * a.k; i += kTeam) {
         const Active act = P.active[S.apos[S.sel[i]]];
         const int t = i / a.k;
         P.pairw[act.base + __popc(act.mask & ((1u << t) - 1u))] = S.selw[i];
@@ -455,10 +486,10 @@ struct Ring {
     __device__ __forceinline__ uint8_t* stage() const { return base + slot * bytes; }
 };
 
-// Columns of a stage: phase 2 keeps head and tail rows of every pair, and
-// above eight pairs they only fit with half the columns.
+// Columns of a stage: above eight activation rows (heads and tails of every
+// pair in phase 2) there is room for half of them only.
 __device__ __forceinline__ int chunk_cols(bool down, int count) {
-    return down && count > 8 ? kBox : kChunk;
+    return (down ? 2 * count : count) > 8 ? kBox : kChunk;
 }
 template <int DT>
 __device__ __forceinline__ int x_stride(int cols) {
@@ -471,10 +502,15 @@ __host__ __device__ constexpr int off_x() {
 
 // The stages of phase 1's unit with `count` tokens: stage(k0, kn).
 template <class Stage>
-__device__ __forceinline__ bool walk_unit(const FewArgs& a, Stage stage) {
-    for (int k0 = 0; k0 < a.H; k0 += kChunk)
-        if (!stage(k0, min(kChunk, a.H - k0))) return false;
+__device__ __forceinline__ bool walk_unit(const FewArgs& a, int count, Stage stage) {
+    const int cols = chunk_cols(false, count);
+    for (int k0 = 0; k0 < a.H; k0 += cols)
+        if (!stage(k0, min(cols, a.H - k0))) return false;
     return true;
+}
+__device__ __forceinline__ int unit_stages(const FewArgs& a, int count) {
+    const int cols = chunk_cols(false, count);
+    return (a.H + cols - 1) / cols;
 }
 
 // The stages of phase 2's steps begin .. end - 1: item(rb, expert) before the
@@ -549,6 +585,13 @@ struct Source {
         }
     }
 
+    // Lane 0: phase 2's boxes of kn columns into L2.
+    __device__ __forceinline__ void fetch(int k0, int kn) const {
+        const int piece = k0 * F::kBits / 512;
+        box_fetch_4d(map, piece, group);
+        if (kn > kBox) box_fetch_4d(map, piece + kBox * F::kBits / 512, group);
+    }
+
     // All lanes: one tensor copy for each 256 columns, and the scales.
     __device__ __forceinline__ void stage(const Ring& ring, int k0, int kn, uint64_t policy) const {
         const int lane = threadIdx.x & 31;
@@ -571,7 +614,7 @@ struct Source {
             if (lane < (down ? 4 : 8) && (lane & 3) * 128 < kn) copy4(sdst + lane * 4, s0 + k0 / 128 * 4);
             arrive_copied(full);
         } else if (DT == MOE_DTYPE_MXFP4_BLOCK32) {
-            // a row's 16 bytes start at a multiple of 16 when K / 32 and k0 / 32 are
+            // a row's 16 bytes start at a multiple of 16 when K / 32 and k0 / 32 do
             const uint8_t *p0 = s0 + k0 / 32, *p1 = s1 + k0 / 32;
             if (kn == kChunk && ((K | k0) & 511) == 0) {
                 copy16(sdst + lane * 16, p0);
@@ -587,8 +630,7 @@ struct Source {
     }
 };
 
-// Activation producer, all lanes of one warp: `rows` rows of kn columns, the
-// i-th at the i-th set bit of `mask` (or the i-th at all), `ld` apart.
+// Activation producer, all lanes of one warp: a row of kn columns.
 __device__ __forceinline__ void copy_row(uint32_t dst, const uint16_t* src, int kn) {
     const int c = (threadIdx.x & 31) * 8;
     if (c < kn) copy16(dst + c * 2, src + c);
@@ -596,68 +638,52 @@ __device__ __forceinline__ void copy_row(uint32_t dst, const uint16_t* src, int 
 }
 
 // ------------------------------------------------------------------ multiplication
-// Weights become bf16 pairs whose order the activations' words follow: a
-// fragment of two registers, a[0] and a[1], pairs with two activation words.
-// (sign | magnitude bits) * 2^E, exact
-template <int E>
-__device__ __forceinline__ uint32_t merge_sign(uint32_t sign, uint32_t mag) {
-    const uint32_t v = (sign & 0x80008000u) | mag;
-    constexpr uint32_t kFactor = (uint32_t)(E + 127) << 7 | (uint32_t)(E + 127) << 23;
-    const uint32_t f = kFactor;
-    const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&v),
-                                     *reinterpret_cast<const __nv_bfloat162*>(&f));
-    return *reinterpret_cast<const uint32_t*>(&r);
+// four e4m3 codes -> two binary16 pairs
+__device__ __forceinline__ void widen_e4m3(uint32_t v, uint32_t& p0, uint32_t& p1) {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(p0), "=r"(p1)
+        : "r"(v));
 }
-// four e4m3 codes: pairs (0, 2) and (1, 3)
-__device__ __forceinline__ void widen_e4m3(uint32_t c, uint32_t& p0, uint32_t& p1, uint32_t& top) {
-    const uint32_t m0 = (c << 4) & 0x07f007f0u, m1 = (c >> 4) & 0x07f007f0u;
-    p0 = merge_sign<120>(c << 8, m0);
-    p1 = merge_sign<120>(c, m1);
-    top = __vmaxu2(top, __vmaxu2(m0, m1));   // 0x7f0 is e4m3's NaN
-}
-// eight e2m1 codes: pairs (0, 4), (1, 5), (2, 6), (3, 7)
+// eight e2m1 codes -> four binary16 pairs
 __device__ __forceinline__ void widen_e2m1(uint32_t v, uint32_t (&p)[4]) {
-    p[0] = merge_sign<126>(v << 12, (v << 6) & 0x01c001c0u);
-    p[1] = merge_sign<126>(v << 8, (v << 2) & 0x01c001c0u);
-    p[2] = merge_sign<126>(v << 4, (v >> 2) & 0x01c001c0u);
-    p[3] = merge_sign<126>(v, (v >> 6) & 0x01c001c0u);
+    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+        : "=r"(p[0]), "=r"(p[1]), "=r"(p[2]), "=r"(p[3])
+        : "r"(v));
 }
 
-// The lane's activations of its column for the warp's 64 columns of K, in the
-// weights' order.
+// The lane's activations of its column for the warp's 64 columns of K: for
+// e4m3 weights columns 16 t .. 16 t + 15, otherwise 8 t .. 8 t + 7 of each 32.
 template <int DT>
 __device__ __forceinline__ void load_acts(const uint8_t* row, int t, bool zero, uint32_t (&b)[8]) {
-    uint4 v[2];
-    if (DT == MOE_DTYPE_FP8_E4M3_BLOCK128) {
-        // lane t: columns 16 t .. 16 t + 15
-        v[0] = *reinterpret_cast<const uint4*>(row + t * 32);
-        v[1] = *reinterpret_cast<const uint4*>(row + t * 32 + 16);
-    } else {
-        // lane t: columns 8 t .. 8 t + 7 of each 32
-        v[0] = *reinterpret_cast<const uint4*>(row + t * 16);
-        v[1] = *reinterpret_cast<const uint4*>(row + 64 + t * 16);
-    }
-    if (zero) v[0] = v[1] = make_uint4(0, 0, 0, 0);
+    constexpr bool kWide = DT == MOE_DTYPE_FP8_E4M3_BLOCK128;
+    uint4 v0 = *reinterpret_cast<const uint4*>(row + t * (kWide ? 32 : 16));
+    uint4 v1 = *reinterpret_cast<const uint4*>(row + (kWide ? t * 32 + 16 : 64 + t * 16));
+    if (zero) v0 = v1 = make_uint4(0, 0, 0, 0);
+    b[0] = v0.x, b[1] = v0.y, b[2] = v0.z, b[3] = v0.w;
+    b[4] = v1.x, b[5] = v1.y, b[6] = v1.z, b[7] = v1.w;
+}
+
+// Exponent field (biased) of the factor that takes the largest of the column's
+// 64 values to 2^14 .. 2^15: an infinity or NaN counts as 2^128, and tiny ones
+// are lifted by at most 2^126.
+__device__ __forceinline__ uint32_t block_lift(const uint32_t (&b)[8]) {
+    uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const uint4 w = v[i];
-        uint32_t* o = b + 4 * i;
-        if (DT == MOE_DTYPE_BF16) {
-            o[0] = w.x;
-            o[1] = w.y;
-            o[2] = w.z;
-            o[3] = w.w;
-        } else if (DT == MOE_DTYPE_FP8_E4M3_BLOCK128) {
-            o[0] = __byte_perm(w.x, w.y, 0x5410);
-            o[1] = __byte_perm(w.x, w.y, 0x7632);
-            o[2] = __byte_perm(w.z, w.w, 0x5410);
-            o[3] = __byte_perm(w.z, w.w, 0x7632);
-        } else {
-            o[0] = __byte_perm(w.x, w.z, 0x5410);
-            o[1] = __byte_perm(w.x, w.z, 0x7632);
-            o[2] = __byte_perm(w.y, w.w, 0x5410);
-            o[3] = __byte_perm(w.y, w.w, 0x7632);
-        }
+    for (int i = 0; i < 8; ++i) m = __vmaxu2(m, b[i] & 0x7fff7fffu);
+    m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    const uint32_t e = max(m & 0xffffu, m >> 16) >> 7;
+    return min(268u - e, 253u);
+}
+__device__ __forceinline__ void to_f16(uint32_t (&b)[8], uint32_t lift) {
+    const float f = __uint_as_float(lift << 23);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float lo = __uint_as_float(b[i] << 16) * f, hi = __uint_as_float(b[i] & 0xffff0000u) * f;
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(b[i]) : "f"(hi), "f"(lo));
     }
 }
 
@@ -670,8 +696,8 @@ template <int NT>
 struct Columns {
     int row[NT];        // row of the stage's activations
     bool zero[NT];      // not the expert's token: the column adds nothing
-    bool own[NT][2];    // the same for the lane's two result columns
-    bool tile1;         // the second tile has any
+    bool own[NT][2];    // the lane's two result columns are the expert's tokens
+    bool on[NT];        // the tile has any
 };
 
 // One warp's part of a stage: all rows of the unit by its 64 columns of K.
@@ -684,15 +710,26 @@ __device__ __forceinline__ void mma_stage(const uint8_t* stage, int kw, int coun
     constexpr int MT = F::kRows / 16;
     constexpr int PB = kBox * F::kBits / 512;        // 64-byte pieces of a row in a box
     constexpr bool TAIL = DOWN && !FOLD;             // a second product for the tails
+    constexpr bool kBf16 = DT == MOE_DTYPE_BF16;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int xs = x_stride<DT>(chunk_cols(DOWN, count));
     const uint8_t* x = stage + off_x<DT>() + kw * kSlice * 2;
     uint32_t b[NT][8], bl[NT][8];
+    float back[NT][2];      // undoes the lift of the lane's two result columns
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-        if (nt == 1 && !col.tile1) continue;
+        if (NT > 1 && !col.on[nt]) continue;
         load_acts<DT>(x + col.row[nt] * xs, t, DOWN && col.zero[nt], b[nt]);
         if (TAIL) load_acts<DT>(x + (col.row[nt] + count) * xs, t, col.zero[nt], bl[nt]);
+        if (!kBf16) {
+            // a tail is at most 2^-8 of its head and takes the head's lift
+            const uint32_t lift = block_lift(b[nt]);
+            to_f16(b[nt], lift);
+            if (TAIL) to_f16(bl[nt], lift);
+            const float inv = __uint_as_float((254u - lift) << 23);
+            back[nt][0] = __shfl_sync(0xffffffffu, inv, 8 * t);
+            back[nt][1] = __shfl_sync(0xffffffffu, inv, 8 * t + 4);
+        }
     }
     // this warp's columns in the boxes: first piece of 64 bytes
     const int c0 = kw * kSlice;
@@ -705,7 +742,6 @@ __device__ __forceinline__ void mma_stage(const uint8_t* stage, int kw, int coun
         const uint8_t* w1 = w0 + PB * 512;
         // products in independent chains: two halves of the slice, heads and tails
         float c[2][NT][4] = {}, cl[2][NT][4] = {};
-        uint32_t top0 = 0, top1 = 0;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             uint32_t m[2][4];
@@ -717,10 +753,10 @@ __device__ __forceinline__ void mma_stage(const uint8_t* stage, int kw, int coun
             } else if (DT == MOE_DTYPE_FP8_E4M3_BLOCK128) {
                 const uint2 p = *reinterpret_cast<const uint2*>(w0 + ((t ^ sw) << 4) + 8 * h);
                 const uint2 q = *reinterpret_cast<const uint2*>(w1 + ((t ^ sw) << 4) + 8 * h);
-                widen_e4m3(p.x, m[0][0], m[0][2], top0);
-                widen_e4m3(q.x, m[0][1], m[0][3], top1);
-                widen_e4m3(p.y, m[1][0], m[1][2], top0);
-                widen_e4m3(q.y, m[1][1], m[1][3], top1);
+                widen_e4m3(p.x, m[0][0], m[0][2]);
+                widen_e4m3(q.x, m[0][1], m[0][3]);
+                widen_e4m3(p.y, m[1][0], m[1][2]);
+                widen_e4m3(q.y, m[1][1], m[1][3]);
             } else {
                 // 16-byte piece of the 32-column block, a word a lane
                 const int off = ((((c0 >> 5) + h & 3) ^ sw) << 4) + t * 4;
@@ -734,9 +770,9 @@ __device__ __forceinline__ void mma_stage(const uint8_t* stage, int kw, int coun
             for (int i = 0; i < 2; ++i)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    if (nt == 1 && !col.tile1) continue;
-                    mma_bf16(c[h][nt], m[i], b[nt][4 * h + 2 * i], b[nt][4 * h + 2 * i + 1]);
-                    if (TAIL) mma_bf16(cl[h][nt], m[i], bl[nt][4 * h + 2 * i], bl[nt][4 * h + 2 * i + 1]);
+                    if (NT > 1 && !col.on[nt]) continue;
+                    mma16<kBf16>(c[h][nt], m[i], b[nt][4 * h + 2 * i], b[nt][4 * h + 2 * i + 1]);
+                    if (TAIL) mma16<kBf16>(cl[h][nt], m[i], bl[nt][4 * h + 2 * i], bl[nt][4 * h + 2 * i + 1]);
                 }
         }
         float s[2][2];          // [half][rows g, rows g + 8]
@@ -753,7 +789,7 @@ __device__ __forceinline__ void mma_stage(const uint8_t* stage, int kw, int coun
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            if (nt == 1 && !col.tile1) continue;
+            if (NT > 1 && !col.on[nt]) continue;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 float v0 = c[0][nt][j], v1 = c[1][nt][j];
@@ -765,24 +801,10 @@ __device__ __forceinline__ void mma_stage(const uint8_t* stage, int kw, int coun
                 if (DT == MOE_DTYPE_BF16)
                     v = v0 + v1;
                 else if (DT == MOE_DTYPE_FP8_E4M3_BLOCK128)
-                    v = (v0 + v1) * s[0][j >> 1];
+                    v = (v0 + v1) * s[0][j >> 1] * back[nt][j & 1];
                 else
-                    v = fmaf(v0, s[0][j >> 1], v1 * s[1][j >> 1]);
+                    v = fmaf(v0, s[0][j >> 1], v1 * s[1][j >> 1]) * back[nt][j & 1];
                 if (!DOWN || col.own[nt][j & 1]) acc[mt][nt][j] += v;
-            }
-        }
-        if (DT == MOE_DTYPE_FP8_E4M3_BLOCK128) {
-            // a NaN code anywhere in a row makes its sums NaN
-            const uint32_t n0 = __vcmpeq2(top0, 0x07f007f0u), n1 = __vcmpeq2(top1, 0x07f007f0u);
-            if (__any_sync(0xffffffffu, n0 | n1)) {
-                const bool r0 = __ballot_sync(0xffffffffu, n0 != 0) >> (lane & 28) & 15u;
-                const bool r1 = __ballot_sync(0xffffffffu, n1 != 0) >> (lane & 28) & 15u;
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if ((!DOWN || col.own[nt][j & 1]) && (j < 2 ? r0 : r1))
-                            acc[mt][nt][j] = __int_as_float(0x7fc00000);
             }
         }
     }
@@ -797,6 +819,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ uint64_t bar_w[kMaxStages], bar_x[kMaxStages], bar_empty[kMaxStages], plan_ready;
     __shared__ int n_active_sh, abort_sh, last_sh;
+    __shared__ double part[2][kWarps][kT];
     float4(*red)[MT][NT][32] = reinterpret_cast<float4(*)[MT][NT][32]>(smem + a.off_red);   // [warp]
     volatile int* abort_flag = &abort_sh;
     const Plan P{reinterpret_cast<Active*>(smem + a.off_active), reinterpret_cast<float*>(smem + a.off_pairw),
@@ -819,68 +842,21 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
     const int cta = blockIdx.x, G = gridDim.x;
     const Active shared{-1, (1u << a.T) - 1u, 0, a.T};
     const int first_routed = a.Is ? 1 : 0, upe = a.I / NF;
-    const int s0 = cut(cta, a.Is / NF, G), s1 = cut(cta + 1, a.Is / NF, G);
+    const int s0 = cut(a, cta, a.Is / NF), s1 = cut(a, cta + 1, a.Is / NF);
+    const int shared_stages = (s1 - s0) * unit_stages(a, a.T);
     // a wait that every lane of the warp takes and leaves together
     auto wait = [&](uint64_t* bar, uint32_t parity) {
         return __all_sync(0xffffffffu, moe::wait_bar(bar, parity, abort_flag, a.status)) != 0;
     };
 
-    if (warp >= kWarps && warp < kWarps + kRouters) {
-        // ---------------------------------------------------------- router
-        const int tid = threadIdx.x - kGroup, rw = warp - kWarps;
-        Scratch S;
-        S.keys = reinterpret_cast<unsigned long long*>(smem + a.off_scratch);
-        S.scores = reinterpret_cast<double*>(S.keys + (size_t)min(a.T, kRouters) * a.E);
-        S.sel = reinterpret_cast<int*>(S.scores + (size_t)min(a.T, kRouters) * a.E);
-        S.selw = reinterpret_cast<float*>(S.sel + a.T * a.k);
-        S.emask = reinterpret_cast<uint32_t*>(S.selw + a.T * a.k);
-        S.apos = reinterpret_cast<int*>(S.emask + a.E);
-        for (int i = cta * kRouterGroup + tid; i < a.H / R; i += G * kRouterGroup) a.joined[i] = 0;
-        for (int e = tid; e < a.E; e += kRouterGroup) S.emask[e] = 0;
-        router_phase(a, warp);
-        __threadfence();
-        asm volatile("barrier.cta.sync 3, %0;" ::"r"(kGroup + kRouterGroup) : "memory");
-        bool ok = true;
-        if (tid == 0) {
-            if (!(a.stall && cta == 0)) atomicAdd(bars, 1);
-            const long long t0 = clock64();
-            while (*reinterpret_cast<volatile int*>(bars) < G) {
-                if (clock64() - t0 > moe::kWaitLimit) {
-                    atomicOr(a.status, moe::DEV_STATUS_TIMEOUT);
-                    *abort_flag = 1;
-                    ok = false;
-                    break;
-                }
-            }
-            __threadfence();
-        }
-        if (!group_any(2, !ok)) {
-            for (int t0 = 0; t0 < a.T; t0 += kRouters) {
-                const int nt = min(kRouters, a.T - t0);
-#pragma unroll 2
-                for (int i = tid; i < nt * a.E; i += kRouterGroup) {
-                    const double* part = a.part + (size_t)t0 * a.E + i;
-                    double l = 0.0;
-#pragma unroll 4
-                    for (int sp = 0; sp < a.n_split; ++sp) l += __ldcg(part + (size_t)sp * a.T * a.E);
-                    const double s = 1.0 / (1.0 + exp(-l));
-                    S.scores[i] = s;
-                    S.keys[i] = sortable(s + (double)__ldg(a.bias + i % a.E));
-                }
-                group_any(2, false);
-                if (rw < nt) choose(a, t0 + rw, S.keys + (size_t)rw * a.E, S.scores + (size_t)rw * a.E, S);
-                group_any(2, false);
-            }
-            build_plan<DT>(a, P, S, tid);
-            group_any(2, false);
-            if (tid == 0) moe::mbar_arrive(&plan_ready);
-        }
-    } else if (warp == kWarps + kRouters) {
+    if (warp == 2 * kWarps) {
         // ---------------------------------------------------------- weight producer
         const uint64_t policy = moe::l2_policy_evict_first();
         uint32_t issued = 0, last_phase = 0;   // slots in use, and their newest phase
         Source<DT> src;
+        int nth = 0;
         auto stage = [&](int k0, int kn) {
+            if (nth++ == kHeadStart) bar_sync(kBarRouted, kConsumers + 32);
             if (!wait(&ring.empty[ring.slot], ring.phase ^ 1)) return false;
             src.stage(ring, k0, kn, policy);
             issued |= 1u << ring.slot;
@@ -891,29 +867,56 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
         bool ok = true;
         for (int u = s0; ok && u < s1; ++u) {
             src.unit(a, false, -1, u * NF);
-            ok = walk_unit(a, stage);
+            ok = walk_unit(a, a.T, stage);
+        }
+        if (ok && nth <= kHeadStart) {   // not met yet
+            bar_sync(kBarRouted, kConsumers + 32);
+            nth = kHeadStart + 1;
         }
         ok = ok && wait(&plan_ready, 0);
         if (ok) {
             for (int u = P.cut1[cta]; ok && u < P.cut1[cta + 1]; ++u) {
-                src.unit(a, false, P.active[first_routed + u / upe].expert, (u % upe) * NF);
-                ok = walk_unit(a, stage);
+                const Active& act = P.active[first_routed + u / upe];
+                src.unit(a, false, act.expert, (u % upe) * NF);
+                ok = walk_unit(a, act.count, stage);
             }
-            ok = ok && walk_down(a, P, n_active_sh, P.cut2[cta], P.cut2[cta + 1],
-                                 [&](int rb, const Active& act) {
-                                     src.unit(a, true, act.expert, rb * R);
-                                     return true;
-                                 },
-                                 stage, [](int) { return true; });
+            // Phase 2.  Until barrier 1 opens the ring fills and no further;
+            // meanwhile the next boxes go into L2.
+            auto item = [&](int rb, const Active& act) {
+                src.unit(a, true, act.expert, rb * R);
+                return true;
+            };
+            auto pass = [](int) { return true; };
+            const int begin = P.cut2[cta], end = P.cut2[cta + 1];
+            int left = a.n_stages, at = begin;
+            auto stage2 = [&](int k0, int kn) {
+                if (left-- == 0) {
+                    int open = 1;
+                    if (lane == 0) open = *reinterpret_cast<volatile int*>(bars + 1) >= G;
+                    if (!__shfl_sync(0xffffffffu, open, 0)) {
+                        const Source<DT> keep = src;
+                        walk_down(a, P, n_active_sh, at, min(end, at + kAhead), item,
+                                  [&](int f0, int fn) {
+                                      if (lane == 0) src.fetch(f0, fn);
+                                      return true;
+                                  },
+                                  pass);
+                        src = keep;
+                    }
+                }
+                at += kn / 128;
+                return stage(k0, kn);
+            };
+            ok = ok && walk_down(a, P, n_active_sh, begin, end, item, stage2, pass);
         }
         // no copy may still be in flight when the block leaves
         if (!ok)
             for (int i = 0; i < a.n_stages; ++i)
                 if (issued >> i & 1u) moe::wait_bar(&bar_w[i], last_phase >> i & 1u, abort_flag, a.status, true);
-    } else if (warp > kWarps + kRouters) {
+    } else if (warp > 2 * kWarps) {
         // ---------------------------------------------------------- activation producers
         // warp j of kFeeders takes every kFeeders-th stage
-        int turn = kWarps + kRouters + 1 - warp;
+        int turn = 2 * kWarps + 1 - warp;
         auto mine = [&]() {
             const bool m = turn == 0;
             turn = turn == kFeeders - 1 ? 0 : turn + 1;
@@ -924,11 +927,12 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
             arrive_copied(&ring.x[ring.slot]);
         };
         uint32_t mask = 0;
+        int xs = 0;
         auto stage_x = [&](int k0, int kn) {
             if (mine()) {
                 if (!wait(&ring.empty[ring.slot], ring.phase ^ 1)) return false;
                 uint32_t dst = moe::smem_addr(ring.stage() + off_x<DT>());
-                for (uint32_t m = mask; m; m &= m - 1, dst += x_stride<DT>(kChunk))
+                for (uint32_t m = mask; m; m &= m - 1, dst += xs)
                     copy_row(dst, a.x + (size_t)(__ffs(m) - 1) * a.H + k0, kn);
                 fed();
             }
@@ -937,12 +941,15 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
         };
         bool ok = true;
         mask = shared.mask;
-        for (int u = s0; ok && u < s1; ++u) ok = walk_unit(a, stage_x);
+        xs = x_stride<DT>(chunk_cols(false, a.T));
+        for (int u = s0; ok && u < s1; ++u) ok = walk_unit(a, a.T, stage_x);
         ok = ok && wait(&plan_ready, 0);
         if (ok) {
             for (int u = P.cut1[cta]; ok && u < P.cut1[cta + 1]; ++u) {
-                mask = P.active[first_routed + u / upe].mask;
-                ok = walk_unit(a, stage_x);
+                const Active& act = P.active[first_routed + u / upe];
+                mask = act.mask;
+                xs = x_stride<DT>(chunk_cols(false, act.count));
+                ok = walk_unit(a, act.count, stage_x);
             }
             // barrier 1: every block's heads and tails are written
             bool late = false;
@@ -960,7 +967,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
             ok = ok && !__any_sync(0xffffffffu, late);
             __threadfence();
             const uint16_t *hi = nullptr, *lo = nullptr;
-            int count = 0, xs = 0;
+            int count = 0;
             if (ok)
                 walk_down(a, P, n_active_sh, P.cut2[cta], P.cut2[cta + 1],
                           [&](int, const Active& act) {
@@ -991,10 +998,64 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
     } else {
         // ---------------------------------------------------------- consumers
         const int tid = threadIdx.x, g = lane >> 2, t = lane & 3;
-        router_phase(a, warp);
+        const int team = warp / kWarps, kw = warp % kWarps;
+        bool ok = true, good = true;
+        router_phase(a, team, kw, part[team]);
         __threadfence();
-        asm volatile("barrier.cta.arrive 3, %0;" ::"r"(kGroup + kRouterGroup) : "memory");
-        bool ok = true;
+        bar_arrive(kBarRouted, kConsumers + 32);
+        if (team == 0) {
+            bar_arrive(kBarLogits, kConsumers);
+        } else {
+            // ------------------------------------------------------ choice and plan
+            const int rid = tid - kTeam;
+            Scratch S;
+            S.keys = reinterpret_cast<unsigned long long*>(smem + a.off_scratch);
+            S.scores = reinterpret_cast<double*>(S.keys + (size_t)a.batch * a.E);
+            S.sel = reinterpret_cast<int*>(S.scores + (size_t)a.batch * a.E);
+            S.selw = reinterpret_cast<float*>(S.sel + a.T * a.k);
+            S.emask = reinterpret_cast<uint32_t*>(S.selw + a.T * a.k);
+            S.apos = reinterpret_cast<int*>(S.emask + a.E);
+            for (int i = cta * kTeam + rid; i < a.H / R; i += G * kTeam) a.joined[i] = 0;
+            for (int e = rid; e < a.E; e += kTeam) S.emask[e] = 0;
+            __threadfence();
+            bar_sync(kBarLogits, kConsumers);
+            // barrier 0: every block's logits are written
+            if (rid == 0) {
+                if (!(a.stall && cta == 0)) atomicAdd(bars, 1);
+                const long long t0 = clock64();
+                while (*reinterpret_cast<volatile int*>(bars) < G) {
+                    if (clock64() - t0 > moe::kWaitLimit) {
+                        atomicOr(a.status, moe::DEV_STATUS_TIMEOUT);
+                        *abort_flag = 1;
+                        ok = false;
+                        break;
+                    }
+                }
+                __threadfence();
+            }
+            good = !group_any(kBarB, !ok);
+            if (good) {
+                for (int t0 = 0; t0 < a.T; t0 += a.batch) {
+                    const int nt = min(a.batch, a.T - t0);
+                    const double* l = a.logits + (size_t)t0 * a.E;
+#pragma unroll 4
+                    for (int i = rid; i < nt * a.E; i += kTeam) {
+                        const double s = 1.0 / (1.0 + exp(-__ldcg(l + i)));
+                        S.scores[i] = s;
+                        S.keys[i] = sortable(s + (double)__ldg(a.bias + i % a.E));
+                    }
+                    group_any(kBarB, false);
+                    if (kw < nt) choose(a, t0 + kw, S.keys + (size_t)kw * a.E, S.scores + (size_t)kw * a.E, S);
+                    group_any(kBarB, false);
+                }
+                build_plan<DT>(a, P, S, rid);
+                group_any(kBarB, false);
+                if (rid == 0) moe::mbar_arrive(&plan_ready);
+            }
+            // the shared expert's stages are the first team's
+            ring.slot = shared_stages % a.n_stages;
+            ring.phase = (uint32_t)(shared_stages / a.n_stages) & 1u;
+        }
         float acc[MT][NT][4];
         Columns<NT> col;
         int count = 0;
@@ -1010,21 +1071,50 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
             ok = wait(&ring.w[ring.slot], ring.phase) && wait(&ring.x[ring.slot], ring.phase);
             return ok;
         };
+        int turn = 0;            // whose stage it is, once both teams work
+        bool both = false;
+        auto my_stage = [&]() {
+            const bool m = !both || turn == team;
+            turn ^= 1;
+            return m;
+        };
         auto release = [&]() {
             __syncwarp();
             if (lane == 0) moe::mbar_arrive(&ring.empty[ring.slot]);
-            ring.next();
         };
-        // Leaves the warps' sums in red (once the last ones have been read)
-        // and waits for all of them; true when any warp has given up.
+        // Leaves the warps' sums in red (once the last ones have been read),
+        // the second team's added to the first's, and waits for all of them;
+        // true when any warp has given up.
         auto gather = [&]() {
-            group_any(1, false);
+            const int bar = both ? kBarAll : kBarA;
+            group_any(bar, false);
+            auto put = [&]() {
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
+                for (int m = 0; m < MT; ++m)
 #pragma unroll
-                for (int i = 0; i < NT; ++i)
-                    red[warp][m][i][lane] = make_float4(acc[m][i][0], acc[m][i][1], acc[m][i][2], acc[m][i][3]);
-            return group_any(1, !ok);
+                    for (int i = 0; i < NT; ++i)
+                        red[kw][m][i][lane] = make_float4(acc[m][i][0], acc[m][i][1], acc[m][i][2], acc[m][i][3]);
+            };
+            if (both) {
+                if (team) put();
+                group_any(bar, false);
+            }
+            if (!team) {
+                if (both) {
+#pragma unroll
+                    for (int m = 0; m < MT; ++m)
+#pragma unroll
+                        for (int i = 0; i < NT; ++i) {
+                            const float4 v = red[kw][m][i][lane];
+                            acc[m][i][0] += v.x;
+                            acc[m][i][1] += v.y;
+                            acc[m][i][2] += v.z;
+                            acc[m][i][3] += v.w;
+                        }
+                }
+                put();
+            }
+            return group_any(bar, !ok);
         };
         // Sum over the K slices, in their order: thread tid takes row tile
         // tid / (32 NT), column tile (tid / 32) % NT.
@@ -1045,12 +1135,17 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
             clear();
             count = act.count;
 #pragma unroll
-            for (int i = 0; i < NT; ++i) col.row[i] = 8 * i + g < count ? 8 * i + g : 0;
-            col.tile1 = count > 8;
-            walk_unit(a, [&](int, int kn) {
-                if (!ready()) return false;
-                if (warp * kSlice < kn) mma_stage<DT, NT, false, FOLD>(ring.stage(), warp, count, col, acc);
-                release();
+            for (int i = 0; i < NT; ++i) {
+                col.row[i] = 8 * i + g < count ? 8 * i + g : 0;
+                col.on[i] = count > 8 * i;
+            }
+            walk_unit(a, count, [&](int, int kn) {
+                if (my_stage()) {
+                    if (!ready()) return false;
+                    if (kw * kSlice < kn) mma_stage<DT, NT, false, FOLD>(ring.stage(), kw, count, col, acc);
+                    release();
+                }
+                ring.next();
                 return true;
             });
             if (gather()) return false;
@@ -1075,19 +1170,19 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
             return true;
         };
 
-        bool good = true;
-        for (int u = s0; good && u < s1; ++u) good = gate_up(shared, u * NF);
-        if (good) {
-            ok = wait(&plan_ready, 0);
-            good = !group_any(1, !ok);
-        }
+        if (team == 0)
+            for (int u = s0; good && u < s1; ++u) good = gate_up(shared, u * NF);
+        if (good) ok = wait(&plan_ready, 0);
+        good = !group_any(kBarAll, !(good && ok));
+        both = true;
+        turn = 0;
         if (good)
             for (int u = P.cut1[cta]; good && u < P.cut1[cta + 1]; ++u)
                 good = gate_up(P.active[first_routed + u / upe], (u % upe) * NF);
         if (good) {
             // barrier 1: this block's heads and tails are written
             __threadfence();
-            group_any(1, false);
+            group_any(kBarAll, false);
             if (tid == 0) atomicAdd(bars + 1, 1);
             const int begin = P.cut2[cta], end = P.cut2[cta + 1];
             const int wsum = a.Is / 128 + (n_active_sh - first_routed) * (a.I / 128);
@@ -1104,15 +1199,17 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
                     for (int j = 0; j < 2; ++j)
                         col.own[i][j] = act.mask >> (FOLD ? (2 * t + j) & 3 : 8 * i + 2 * t + j) & 1u;
                 }
-                col.tile1 = act.mask >> 8;
+#pragma unroll
+                for (int i = 0; i < NT; ++i) col.on[i] = act.mask >> (8 * i) & 255u;
                 return true;
             };
             auto stage = [&](int, int kn) {
                 // a given-up wait ends in row_end, which all warps reach
-                if (ok && ready()) {
-                    if (warp * kSlice < kn) mma_stage<DT, NT, true, FOLD>(ring.stage(), warp, count, col, acc);
+                if (my_stage() && ok && ready()) {
+                    if (kw * kSlice < kn) mma_stage<DT, NT, true, FOLD>(ring.stage(), kw, count, col, acc);
                     release();
                 }
+                ring.next();
                 return true;
             };
             auto row_end = [&](int rb) {
@@ -1152,14 +1249,14 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
                 int parts = 0;
                 for (int c = c0; c < c1; ++c) parts += P.cut2[c] < P.cut2[c + 1];
                 __threadfence();
-                group_any(1, false);
+                group_any(kBarAll, false);
                 if (tid == 0) {
                     last_sh = atomicAdd(a.joined + rb, 1) == parts - 1;
                     __threadfence();
                 }
-                group_any(1, false);
+                group_any(kBarAll, false);
                 if (last_sh) {
-                    for (int i = tid; i < a.T * R; i += kGroup) {
+                    for (int i = tid; i < a.T * R; i += kConsumers) {
                         float s = 0.0f;
                         for (int c = c0; c < c1; ++c)
                             if (P.cut2[c] < P.cut2[c + 1])
@@ -1186,20 +1283,12 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
 size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
 
 struct FewLayout {
-    size_t part, hi, lo, join, joined, total;
-    int n_split, ld_act;
+    size_t logits, hi, lo, join, joined, total;
+    int ld_act;
 };
 
-// K slices of the router: enough that every warp has one, and short enough for
-// a lane's registers.
 FewLayout few_layout(const moe_config_t* c) {
     FewLayout L{};
-    const int nch = c->H / 8;
-    int split = 148 * (kWarps + kRouters) / c->E;
-    const int lo = (nch + 32 * kRouterVecs - 1) / (32 * kRouterVecs), hi = nch / 32 > 0 ? nch / 32 : 1;
-    split = split > hi ? hi : split;
-    split = split < lo ? lo : split;
-    L.n_split = split;
     const int Is = c->n_shared * c->I;
     L.ld_act = Is > c->I ? Is : c->I;
     size_t off = 256;
@@ -1208,7 +1297,7 @@ FewLayout few_layout(const moe_config_t* c) {
         off = up256(off + bytes);
         return at;
     };
-    L.part = take((size_t)split * c->T * c->E * 8);
+    L.logits = take((size_t)c->T * c->E * 8);
     L.hi = take((size_t)c->T * (c->k + 1) * L.ld_act * 2);
     L.lo = take((size_t)c->T * (c->k + 1) * L.ld_act * 2);
     L.join = take((size_t)kMaxBlocks * 2 * c->T * 64 * 4);
@@ -1299,18 +1388,26 @@ moe_status_t few_smem(FewArgs& a, int limit, size_t* bytes) {
     a.off_cuts = off;
     off = up(off + 2 * (kMaxBlocks + 1) * 4, 16);
     a.off_scratch = off;
-    off = up(off + (a.T < kRouters ? a.T : kRouters) * a.E * 16 + n * 8 + a.E * 8, 16);
+    // tokens chosen at a time, so that their keys and scores stay within 16 KB
+    const int most = a.E <= 256 ? 4 : a.E <= 512 ? 2 : 1;
+    a.batch = a.T < most ? a.T : most;
+    off = up(off + a.batch * a.E * 16 + n * 8 + a.E * 8, 16);
     a.off_red = off;
     off += kWarps * (F::kRows / 16) * NT * 512;
     a.off_ring = up(off, 1024);
     const int full = kChunk * 2 + F::kPad, half = kBox * 2 + F::kPad;
-    const int x = NT == 1 ? 2 * a.T * full : (16 * full > 2 * kT * half ? 16 * full : 2 * kT * half);
+    const int x = a.T <= 4 ? 2 * a.T * full : 8 * full > 2 * a.T * half ? 8 * full : 2 * a.T * half;
     a.stage_bytes = up(off_x<DT>() + x, 512);
     const int stages = (limit - a.off_ring) / a.stage_bytes;
-    a.n_stages = stages < kMaxStages ? stages : kMaxStages;
-    // a feeder that waits for a slot has last waited kFeeders stages before:
-    // with fewer slots than that it could take an old phase for the new one
-    if (a.n_stages < kFeeders)
+    a.n_stages = (stages < kMaxStages ? stages : kMaxStages) & ~1;
+    // Who waits on a slot's barrier must not miss a whole turn of it, or it
+    // takes an old phase for the new one.  A team sees every second stage: an
+    // even number of slots gives it the same ones each time.  A feeder that
+    // waits for stage i to be free has seen stage i - kFeeders - n released;
+    // kFeeders being even, that was the same team's, which releases in order,
+    // so stage i - 2 n is released too when n >= kFeeders.
+    static_assert(kFeeders == 4, "an even number, at most the least number of stages");
+    if (a.n_stages < 4)
         return ffail(MOE_ERR_UNSUPPORTED, "%s: %lld bytes of shared memory hold too few stages", "few-token layer",
                      limit);
     *bytes = (size_t)a.off_ring + (size_t)a.n_stages * a.stage_bytes;
@@ -1333,6 +1430,7 @@ moe_status_t launch_few(FewArgs& a, cudaStream_t s) {
         if (e == cudaSuccess) {
             void* args[] = {&a};
             const int grid = sms < kMaxBlocks ? sms : kMaxBlocks;
+            a.inv_g = 1.0 / grid;
             e = cudaLaunchCooperativeKernel(kernel, dim3(grid), dim3(kThreads), args, smem, s);
         }
     }
@@ -1410,7 +1508,7 @@ moe_status_t moe_forward_few(const moe_config_t* cfg, const void* x, const void*
     a.w = topk_w;
     char* base = static_cast<char*>(ws);
     a.status = reinterpret_cast<int*>(base);
-    a.part = reinterpret_cast<double*>(base + L.part);
+    a.logits = reinterpret_cast<double*>(base + L.logits);
     a.act_hi = reinterpret_cast<uint16_t*>(base + L.hi);
     a.act_lo = reinterpret_cast<uint16_t*>(base + L.lo);
     a.join = reinterpret_cast<float*>(base + L.join);
@@ -1426,7 +1524,6 @@ moe_status_t moe_forward_few(const moe_config_t* cfg, const void* x, const void*
     a.group_topn = cfg->group_topn;
     a.norm = cfg->norm_topk_prob != 0;
     a.rsf = cfg->routed_scaling_factor;
-    a.n_split = L.n_split;
     a.ld_act = L.ld_act;
     a.stall = cfg->flags & MOE_FLAG_TEST_STALL ? 1 : 0;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
