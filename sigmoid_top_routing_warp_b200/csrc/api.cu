@@ -1183,8 +1183,8 @@ moe_status_t api_make_map_3d_bf16(CUtensorMap* m, const void* ptr, uint64_t d0, 
 }
 
 // Bytes as a tensor of `rank` dimensions (strides of all but the first, in
-// bytes), 64-byte swizzle.
-moe_status_t api_make_map_u8_sw64(CUtensorMap* m, const void* ptr, uint32_t rank, const uint64_t* dims,
+// bytes), 128-byte swizzle.
+moe_status_t api_make_map_u8_sw128(CUtensorMap* m, const void* ptr, uint32_t rank, const uint64_t* dims,
                                   const uint64_t* strides, const uint32_t* box, const char* what) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
@@ -1198,7 +1198,7 @@ moe_status_t api_make_map_u8_sw64(CUtensorMap* m, const void* ptr, uint32_t rank
         if (i + 1 < rank) st[i] = strides[i];
     }
     CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void*>(ptr), d, st, b, estr,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return fail(MOE_ERR_CUDA, "tensor map for %s failed (%d)", what, (int)r);
     return MOE_OK;

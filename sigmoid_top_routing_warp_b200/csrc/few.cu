@@ -54,7 +54,7 @@ moe_status_t api_check_config(const moe_config_t* c);
 moe_status_t api_fail(moe_status_t st, const char* msg);
 void api_clear_error();
 moe_status_t api_sm_count(int* n);
-moe_status_t api_make_map_u8_sw64(CUtensorMap* m, const void* ptr, uint32_t rank, const uint64_t* dims,
+moe_status_t api_make_map_u8_sw128(CUtensorMap* m, const void* ptr, uint32_t rank, const uint64_t* dims,
                                   const uint64_t* strides, const uint32_t* box, const char* what);
 }  // namespace moe
 
@@ -80,19 +80,22 @@ constexpr int kBarWord = moe::kSchedFirstWord;   // grid barriers (2) and the ex
 
 // Per weight type: rows of a unit, bits of a weight, bytes of a stage's
 // scales, and the activation rows' padding in a stage.  A stage holds 16 KB of
-// weights, as 64-byte pieces of 8 rows (512 bytes, 64-byte swizzle): a
-// fragment load's lanes (8 rows by four 16-byte pieces) then fall on different
-// banks.  The padding does the same for the activations (16 bytes a lane; 32
-// for e4m3, whose lanes hold 16 weights).
+// weights, as 128-byte pieces of 8 rows (1024 bytes, 128-byte swizzle: 64-byte
+// pieces ran at 5 TB/s at most).  A lane's part of a piece, and the padding of
+// the activation rows, are chosen so that a load's lanes (8 rows by 4) fall on
+// different banks:
+//   bf16   the 16-byte parts 2 t and 2 t + 1: 16 columns in a row
+//   e4m3   word t of each 16-byte part: 4 columns of each 16
+//   MXFP4  word t of each 16-byte part: 8 columns of each 32
 template <int DT>
 struct Fmt;
 template <>
 struct Fmt<MOE_DTYPE_BF16> {
-    static constexpr int kRows = 16, kBits = 16, kScaleBytes = 0, kPad = 64;
+    static constexpr int kRows = 16, kBits = 16, kScaleBytes = 0, kPad = 16;
 };
 template <>
 struct Fmt<MOE_DTYPE_FP8_E4M3_BLOCK128> {
-    static constexpr int kRows = 32, kBits = 8, kScaleBytes = 128, kPad = 16;  // scales: [2][4] fp32
+    static constexpr int kRows = 32, kBits = 8, kScaleBytes = 128, kPad = 32;  // scales: [2][4] fp32
 };
 template <>
 struct Fmt<MOE_DTYPE_MXFP4_BLOCK32> {
@@ -173,29 +176,19 @@ __device__ __forceinline__ void bar_arrive(int id, int n) {
     asm volatile("barrier.cta.arrive %0, %1;" ::"r"(id), "r"(n) : "memory");
 }
 
-// Tensor copies of one box, with an L2 policy.
-__device__ __forceinline__ void box_load_4d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int c2, int c3,
-                                            uint64_t policy) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
-        " [%0], [%1, {%3, %3, %4, %5}], [%2], %6;" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(0), "r"(c2), "r"(c3), "l"(policy)
-        : "memory");
-}
-__device__ __forceinline__ void box_load_5d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int c2, int c4,
-                                            uint64_t policy) {
+// Tensor copies of one box, with an L2 policy, or into L2 only.
+__device__ __forceinline__ void box_load(uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1, int c2,
+                                         int c3, int c4, uint64_t policy) {
     asm volatile(
         "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
-        " [%0], [%1, {%3, %3, %4, %3, %5}], [%2], %6;" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(0), "r"(c2), "r"(c4), "l"(policy)
+        " [%0], [%1, {%3, %4, %5, %6, %7}], [%2], %8;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "l"(policy)
         : "memory");
 }
-
-// The same boxes into L2 only.
-__device__ __forceinline__ void box_fetch_4d(const CUtensorMap* m, int c2, int c3) {
-    asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %1, %2, %3}];" ::"l"(
+__device__ __forceinline__ void box_fetch(const CUtensorMap* m, int c0, int c1, int c2, int c3, int c4) {
+    asm volatile("cp.async.bulk.prefetch.tensor.5d.L2.global.tile [%0, {%1, %2, %3, %4, %5}];" ::"l"(
                      reinterpret_cast<uint64_t>(m)),
-                 "r"(0), "r"(c2), "r"(c3)
+                 "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
                  : "memory");
 }
 
@@ -226,9 +219,12 @@ __device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uin
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// e8m0 scale byte -> binary32 (0 is 2^-127, 255 NaN)
-__device__ __forceinline__ float e8m0(uint32_t s) {
-    return __uint_as_float(s == 0u ? 0x00400000u : s == 255u ? 0x7fc00000u : s << 23);
+// Two e8m0 scale bytes -> binary32 (0 is 2^-127, 255 NaN): both are bf16 values.
+__device__ __forceinline__ void e8m0x2(uint32_t v, float& lo, float& hi) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.bf16x2.ue8m0x2 %0, a;\n\t}" : "=r"(r) : "r"(v));
+    lo = __uint_as_float(r << 16);
+    hi = __uint_as_float(r & 0xffff0000u);
 }
 
 // ------------------------------------------------------------------ router
@@ -475,8 +471,12 @@ __device__ void build_plan(const FewArgs& a, const Plan& P, const Scratch& S, in
 struct Ring {
     uint64_t *w, *x, *empty;
     uint8_t* base;
-    int n, bytes, slot;
+    int n, bytes, scales, slot;   // scales: their offset in a stage
     uint32_t phase;
+    // Teams and feeders own slots, so that whoever waits on a slot's barriers
+    // has waited on every turn of it and cannot take an old phase for a new one.
+    __device__ __forceinline__ int team() const { return slot & 1; }
+    __device__ __forceinline__ int feeder() const { return slot % kFeeders; }
     __device__ __forceinline__ void next() {
         if (++slot == n) {
             slot = 0;
@@ -495,10 +495,9 @@ template <int DT>
 __device__ __forceinline__ int x_stride(int cols) {
     return cols * 2 + Fmt<DT>::kPad;
 }
-template <int DT>
-__host__ __device__ constexpr int off_x() {
-    return 2 * kBoxBytes + Fmt<DT>::kScaleBytes;
-}
+// The activations stand behind the stage's boxes: a stage of half the columns
+// has one box and room for more rows.
+__device__ __forceinline__ int off_x(int cols) { return cols > kBox ? 2 * kBoxBytes : kBoxBytes; }
 
 // The stages of phase 1's unit with `count` tokens: stage(k0, kn).
 template <class Stage>
@@ -585,11 +584,14 @@ struct Source {
         }
     }
 
-    // Lane 0: phase 2's boxes of kn columns into L2.
+    // Coordinates of the box at column k (see few_maps): 4-bit rows are one
+    // dimension in bytes, the others are cut into 128-byte pieces.
+    __device__ __forceinline__ int byte_of(int k) const { return F::kBits == 4 ? k / 2 : 0; }
+    __device__ __forceinline__ int piece_of(int k) const { return F::kBits == 4 ? 0 : k * F::kBits / 1024; }
+
+    // Lane 0: the boxes of kn columns into L2.
     __device__ __forceinline__ void fetch(int k0, int kn) const {
-        const int piece = k0 * F::kBits / 512;
-        box_fetch_4d(map, piece, group);
-        if (kn > kBox) box_fetch_4d(map, piece + kBox * F::kBits / 512, group);
+        for (int k = k0; k < k0 + kn; k += kBox) box_fetch(map, byte_of(k), 0, piece_of(k), 0, group);
     }
 
     // All lanes: one tensor copy for each 256 columns, and the scales.
@@ -600,16 +602,11 @@ struct Source {
         if (lane == 0) {
             const uint32_t bar = moe::smem_addr(full);
             moe::mbar_arrive_expect_tx(full, kn > kBox ? 2 * kBoxBytes : kBoxBytes);
-            const int piece = k0 * F::kBits / 512;
-            if (down) {
-                box_load_4d(dst, map, bar, piece, group, policy);
-                if (kn > kBox) box_load_4d(dst + kBoxBytes, map, bar, piece + kBox * F::kBits / 512, group, policy);
-            } else {
-                box_load_5d(dst, map, bar, piece, group, policy);
-                if (kn > kBox) box_load_5d(dst + kBoxBytes, map, bar, piece + kBox * F::kBits / 512, group, policy);
-            }
+            box_load(dst, map, bar, byte_of(k0), 0, piece_of(k0), 0, group, policy);
+            if (kn > kBox)
+                box_load(dst + kBoxBytes, map, bar, byte_of(k0 + kBox), 0, piece_of(k0 + kBox), 0, group, policy);
         }
-        const uint32_t sdst = dst + 2 * kBoxBytes;
+        const uint32_t sdst = dst + ring.scales;
         if (DT == MOE_DTYPE_FP8_E4M3_BLOCK128) {
             if (lane < (down ? 4 : 8) && (lane & 3) * 128 < kn) copy4(sdst + lane * 4, s0 + k0 / 128 * 4);
             arrive_copied(full);
@@ -654,16 +651,26 @@ __device__ __forceinline__ void widen_e2m1(uint32_t v, uint32_t (&p)[4]) {
         : "r"(v));
 }
 
-// The lane's activations of its column for the warp's 64 columns of K: for
-// e4m3 weights columns 16 t .. 16 t + 15, otherwise 8 t .. 8 t + 7 of each 32.
+// The lane's activations of its column for the warp's 64 columns of K, in the
+// order of the weights' columns.
 template <int DT>
 __device__ __forceinline__ void load_acts(const uint8_t* row, int t, bool zero, uint32_t (&b)[8]) {
-    constexpr bool kWide = DT == MOE_DTYPE_FP8_E4M3_BLOCK128;
-    uint4 v0 = *reinterpret_cast<const uint4*>(row + t * (kWide ? 32 : 16));
-    uint4 v1 = *reinterpret_cast<const uint4*>(row + (kWide ? t * 32 + 16 : 64 + t * 16));
-    if (zero) v0 = v1 = make_uint4(0, 0, 0, 0);
-    b[0] = v0.x, b[1] = v0.y, b[2] = v0.z, b[3] = v0.w;
-    b[4] = v1.x, b[5] = v1.y, b[6] = v1.z, b[7] = v1.w;
+    if (DT == MOE_DTYPE_FP8_E4M3_BLOCK128) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint2 v = *reinterpret_cast<const uint2*>(row + j * 32 + t * 8);
+            b[2 * j] = v.x, b[2 * j + 1] = v.y;
+        }
+    } else {
+        constexpr bool kWide = DT == MOE_DTYPE_BF16;
+        const uint4 v0 = *reinterpret_cast<const uint4*>(row + t * (kWide ? 32 : 16));
+        const uint4 v1 = *reinterpret_cast<const uint4*>(row + (kWide ? t * 32 + 16 : 64 + t * 16));
+        b[0] = v0.x, b[1] = v0.y, b[2] = v0.z, b[3] = v0.w;
+        b[4] = v1.x, b[5] = v1.y, b[6] = v1.z, b[7] = v1.w;
+    }
+    if (zero)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) b[i] = 0;
 }
 
 // Exponent field (biased) of the factor that takes the largest of the column's
@@ -700,66 +707,63 @@ struct Columns {
     bool on[NT];        // the tile has any
 };
 
-// One warp's part of a stage: all rows of the unit by its 64 columns of K.
-// In phase 2 only the expert's own tokens add the stage's products: an
-// infinity or a NaN among its weights reaches no other.
+// One warp's part of a stage for one tile of tokens: all rows of the unit by
+// its 64 columns of K.  In phase 2 only the expert's own tokens add the
+// stage's products: an infinity or a NaN among its weights reaches no other.
+// A stage with tokens in both tiles does this twice: with 16 tokens 1.4 of
+// them meet an expert on average, and a branch at every product cost more.
 template <int DT, int NT, bool DOWN, bool FOLD>
-__device__ __forceinline__ void mma_stage(const uint8_t* stage, int kw, int count, const Columns<NT>& col,
-                                          float (&acc)[Fmt<DT>::kRows / 16][NT][4]) {
+__device__ __forceinline__ void mma_tile(const uint8_t* stage, const uint8_t* sc, int kw, int count,
+                                         const Columns<NT>& col, int nt, float (&acc)[Fmt<DT>::kRows / 16][NT][4]) {
     using F = Fmt<DT>;
     constexpr int MT = F::kRows / 16;
-    constexpr int PB = kBox * F::kBits / 512;        // 64-byte pieces of a row in a box
+    constexpr int PB = kBox * F::kBits / 1024;       // 128-byte pieces of a row in a box
     constexpr bool TAIL = DOWN && !FOLD;             // a second product for the tails
     constexpr bool kBf16 = DT == MOE_DTYPE_BF16;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int xs = x_stride<DT>(chunk_cols(DOWN, count));
-    const uint8_t* x = stage + off_x<DT>() + kw * kSlice * 2;
-    uint32_t b[NT][8], bl[NT][8];
-    float back[NT][2];      // undoes the lift of the lane's two result columns
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        if (NT > 1 && !col.on[nt]) continue;
-        load_acts<DT>(x + col.row[nt] * xs, t, DOWN && col.zero[nt], b[nt]);
-        if (TAIL) load_acts<DT>(x + (col.row[nt] + count) * xs, t, col.zero[nt], bl[nt]);
-        if (!kBf16) {
-            // a tail is at most 2^-8 of its head and takes the head's lift
-            const uint32_t lift = block_lift(b[nt]);
-            to_f16(b[nt], lift);
-            if (TAIL) to_f16(bl[nt], lift);
-            const float inv = __uint_as_float((254u - lift) << 23);
-            back[nt][0] = __shfl_sync(0xffffffffu, inv, 8 * t);
-            back[nt][1] = __shfl_sync(0xffffffffu, inv, 8 * t + 4);
-        }
+    const int cols = chunk_cols(DOWN, count), xs = x_stride<DT>(cols);
+    const uint8_t* x = stage + off_x(cols) + kw * kSlice * 2 + col.row[nt] * xs;
+    uint32_t b[8], bl[8];
+    float back[2] = {1.0f, 1.0f};   // undoes the lift of the lane's two result columns
+    load_acts<DT>(x, t, DOWN && col.zero[nt], b);
+    if (TAIL) load_acts<DT>(x + count * xs, t, col.zero[nt], bl);
+    if (!kBf16) {
+        // a tail is at most 2^-8 of its head and takes the head's lift
+        const uint32_t lift = block_lift(b);
+        to_f16(b, lift);
+        if (TAIL) to_f16(bl, lift);
+        const float inv = __uint_as_float((254u - lift) << 23);
+        back[0] = __shfl_sync(0xffffffffu, inv, 8 * t);
+        back[1] = __shfl_sync(0xffffffffu, inv, 8 * t + 4);
     }
-    // this warp's columns in the boxes: first piece of 64 bytes
+    // this warp's columns in the boxes: row g of their piece, and the 16-byte
+    // parts' swizzle
     const int c0 = kw * kSlice;
-    const uint8_t* w = stage + (c0 / kBox) * kBoxBytes + (c0 % kBox) * F::kBits / 512 * 512 + g * 64;
-    const int sw = (g >> 1) & 3;                     // 64-byte swizzle of row g
-    const uint8_t* sc = stage + 2 * kBoxBytes;
+    const uint8_t* w = stage + (c0 / kBox) * kBoxBytes + (c0 % kBox) * F::kBits / 1024 * 1024 + g * 128;
+    auto part = [&](int i) { return (((c0 * F::kBits / 128 & 7) + i) ^ g) << 4; };
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-        const uint8_t* w0 = w + (2 * mt) * PB * 512;
-        const uint8_t* w1 = w0 + PB * 512;
+        const uint8_t* w0 = w + (2 * mt) * PB * 1024;
+        const uint8_t* w1 = w0 + PB * 1024;
         // products in independent chains: two halves of the slice, heads and tails
-        float c[2][NT][4] = {}, cl[2][NT][4] = {};
+        float c[2][4] = {}, cl[2][4] = {};
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             uint32_t m[2][4];
-            if (DT == MOE_DTYPE_BF16) {
-                const uint4 p = *reinterpret_cast<const uint4*>(w0 + h * 512 + ((t ^ sw) << 4));
-                const uint4 q = *reinterpret_cast<const uint4*>(w1 + h * 512 + ((t ^ sw) << 4));
+            if (kBf16) {
+                const uint4 p = *reinterpret_cast<const uint4*>(w0 + part(2 * t + h));
+                const uint4 q = *reinterpret_cast<const uint4*>(w1 + part(2 * t + h));
                 m[0][0] = p.x, m[0][1] = q.x, m[0][2] = p.y, m[0][3] = q.y;
                 m[1][0] = p.z, m[1][1] = q.z, m[1][2] = p.w, m[1][3] = q.w;
             } else if (DT == MOE_DTYPE_FP8_E4M3_BLOCK128) {
-                const uint2 p = *reinterpret_cast<const uint2*>(w0 + ((t ^ sw) << 4) + 8 * h);
-                const uint2 q = *reinterpret_cast<const uint2*>(w1 + ((t ^ sw) << 4) + 8 * h);
-                widen_e4m3(p.x, m[0][0], m[0][2]);
-                widen_e4m3(q.x, m[0][1], m[0][3]);
-                widen_e4m3(p.y, m[1][0], m[1][2]);
-                widen_e4m3(q.y, m[1][1], m[1][3]);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int off = part(2 * h + i) + t * 4;
+                    widen_e4m3(*reinterpret_cast<const uint32_t*>(w0 + off), m[i][0], m[i][2]);
+                    widen_e4m3(*reinterpret_cast<const uint32_t*>(w1 + off), m[i][1], m[i][3]);
+                }
             } else {
-                // 16-byte piece of the 32-column block, a word a lane
-                const int off = ((((c0 >> 5) + h & 3) ^ sw) << 4) + t * 4;
+                const int off = part(h) + t * 4;
                 uint32_t p[4], q[4];
                 widen_e2m1(*reinterpret_cast<const uint32_t*>(w0 + off), p);
                 widen_e2m1(*reinterpret_cast<const uint32_t*>(w1 + off), q);
@@ -767,47 +771,42 @@ __device__ __forceinline__ void mma_stage(const uint8_t* stage, int kw, int coun
                 m[1][0] = p[2], m[1][1] = q[2], m[1][2] = p[3], m[1][3] = q[3];
             }
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    if (NT > 1 && !col.on[nt]) continue;
-                    mma16<kBf16>(c[h][nt], m[i], b[nt][4 * h + 2 * i], b[nt][4 * h + 2 * i + 1]);
-                    if (TAIL) mma16<kBf16>(cl[h][nt], m[i], bl[nt][4 * h + 2 * i], bl[nt][4 * h + 2 * i + 1]);
-                }
+            for (int i = 0; i < 2; ++i) {
+                mma16<kBf16>(c[h], m[i], b[4 * h + 2 * i], b[4 * h + 2 * i + 1]);
+                if (TAIL) mma16<kBf16>(cl[h], m[i], bl[4 * h + 2 * i], bl[4 * h + 2 * i + 1]);
+            }
         }
         float s[2][2];          // [half][rows g, rows g + 8]
         if (DT == MOE_DTYPE_FP8_E4M3_BLOCK128) {
             const float* fs = reinterpret_cast<const float*>(sc) + c0 / 128;
-            s[0][0] = s[1][0] = fs[0];
-            s[0][1] = s[1][1] = DOWN ? fs[0] : fs[4];
+            s[0][0] = fs[0];
+            s[0][1] = DOWN ? fs[0] : fs[4];
         } else if (DT == MOE_DTYPE_MXFP4_BLOCK32) {
             const uint8_t* sr = sc + (mt * 16 + g) * 16 + kw * 2;
-            const uint32_t e0 = *reinterpret_cast<const uint16_t*>(sr);
-            const uint32_t e1 = *reinterpret_cast<const uint16_t*>(sr + 128);
-            s[0][0] = e8m0(e0 & 255u), s[0][1] = e8m0(e1 & 255u);
-            s[1][0] = e8m0(e0 >> 8), s[1][1] = e8m0(e1 >> 8);
+            e8m0x2(*reinterpret_cast<const uint16_t*>(sr), s[0][0], s[1][0]);
+            e8m0x2(*reinterpret_cast<const uint16_t*>(sr + 128), s[0][1], s[1][1]);
         }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            if (NT > 1 && !col.on[nt]) continue;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float v0 = c[0][nt][j], v1 = c[1][nt][j];
-                if (TAIL) {
-                    v0 += cl[0][nt][j];
-                    v1 += cl[1][nt][j];
-                }
-                float v;
-                if (DT == MOE_DTYPE_BF16)
-                    v = v0 + v1;
-                else if (DT == MOE_DTYPE_FP8_E4M3_BLOCK128)
-                    v = (v0 + v1) * s[0][j >> 1] * back[nt][j & 1];
-                else
-                    v = fmaf(v0, s[0][j >> 1], v1 * s[1][j >> 1]) * back[nt][j & 1];
-                if (!DOWN || col.own[nt][j & 1]) acc[mt][nt][j] += v;
-            }
+        for (int j = 0; j < 4; ++j) {
+            const float v0 = TAIL ? c[0][j] + cl[0][j] : c[0][j], v1 = TAIL ? c[1][j] + cl[1][j] : c[1][j];
+            float v;
+            if (kBf16)
+                v = v0 + v1;
+            else if (DT == MOE_DTYPE_FP8_E4M3_BLOCK128)
+                v = (v0 + v1) * s[0][j >> 1] * back[j & 1];
+            else
+                v = fmaf(v0, s[0][j >> 1], v1 * s[1][j >> 1]) * back[j & 1];
+            acc[mt][nt][j] += !DOWN || col.own[nt][j & 1] ? v : 0.0f;
         }
     }
+}
+
+template <int DT, int NT, bool DOWN, bool FOLD>
+__device__ __forceinline__ void mma_stage(const uint8_t* stage, const uint8_t* sc, int kw, int count,
+                                          const Columns<NT>& col, float (&acc)[Fmt<DT>::kRows / 16][NT][4]) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+        if (NT == 1 || col.on[nt]) mma_tile<DT, NT, DOWN, FOLD>(stage, sc, kw, count, col, nt, acc);
 }
 
 // ------------------------------------------------------------------ the kernel
@@ -816,7 +815,8 @@ template <int DT, int NT, bool FOLD>
 __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant__ FewArgs a) {
     using F = Fmt<DT>;
     constexpr int R = F::kRows, MT = R / 16, NF = R / 2;
-    extern __shared__ __align__(1024) uint8_t smem[];
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ uint64_t bar_w[kMaxStages], bar_x[kMaxStages], bar_empty[kMaxStages], plan_ready;
     __shared__ int n_active_sh, abort_sh, last_sh;
     __shared__ double part[2][kWarps][kT];
@@ -837,7 +837,8 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
         moe::fence_barrier_init();
     }
     __syncthreads();
-    Ring ring{bar_w, bar_x, bar_empty, smem + a.off_ring, a.n_stages, a.stage_bytes, 0, 0};
+    Ring ring{bar_w, bar_x, bar_empty, smem + a.off_ring, a.n_stages, a.stage_bytes, a.stage_bytes - F::kScaleBytes,
+              0, 0};
     int* bars = a.status + kBarWord;
     const int cta = blockIdx.x, G = gridDim.x;
     const Active shared{-1, (1u << a.T) - 1u, 0, a.T};
@@ -915,23 +916,21 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
                 if (issued >> i & 1u) moe::wait_bar(&bar_w[i], last_phase >> i & 1u, abort_flag, a.status, true);
     } else if (warp > 2 * kWarps) {
         // ---------------------------------------------------------- activation producers
-        // warp j of kFeeders takes every kFeeders-th stage
-        int turn = 2 * kWarps + 1 - warp;
-        auto mine = [&]() {
-            const bool m = turn == 0;
-            turn = turn == kFeeders - 1 ? 0 : turn + 1;
-            return m;
-        };
-        turn = turn < 0 ? turn + kFeeders : turn;
+        const int feeder = warp - 2 * kWarps - 1;
         auto fed = [&]() {
             arrive_copied(&ring.x[ring.slot]);
         };
         uint32_t mask = 0;
-        int xs = 0;
+        int xs = 0, off = 0;     // of the unit's stages
+        auto shape = [&](bool down, int count) {
+            const int cols = chunk_cols(down, count);
+            xs = x_stride<DT>(cols);
+            off = off_x(cols);
+        };
         auto stage_x = [&](int k0, int kn) {
-            if (mine()) {
+            if (ring.feeder() == feeder) {
                 if (!wait(&ring.empty[ring.slot], ring.phase ^ 1)) return false;
-                uint32_t dst = moe::smem_addr(ring.stage() + off_x<DT>());
+                uint32_t dst = moe::smem_addr(ring.stage()) + off;
                 for (uint32_t m = mask; m; m &= m - 1, dst += xs)
                     copy_row(dst, a.x + (size_t)(__ffs(m) - 1) * a.H + k0, kn);
                 fed();
@@ -941,14 +940,14 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
         };
         bool ok = true;
         mask = shared.mask;
-        xs = x_stride<DT>(chunk_cols(false, a.T));
+        shape(false, a.T);
         for (int u = s0; ok && u < s1; ++u) ok = walk_unit(a, a.T, stage_x);
         ok = ok && wait(&plan_ready, 0);
         if (ok) {
             for (int u = P.cut1[cta]; ok && u < P.cut1[cta + 1]; ++u) {
                 const Active& act = P.active[first_routed + u / upe];
                 mask = act.mask;
-                xs = x_stride<DT>(chunk_cols(false, act.count));
+                shape(false, act.count);
                 ok = walk_unit(a, act.count, stage_x);
             }
             // barrier 1: every block's heads and tails are written
@@ -974,13 +973,13 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
                               hi = a.act_hi + (size_t)act.base * a.ld_act;
                               lo = a.act_lo + (size_t)act.base * a.ld_act;
                               count = act.count;
-                              xs = x_stride<DT>(chunk_cols(true, count));
+                              shape(true, count);
                               return true;
                           },
                           [&](int k0, int kn) {
-                              if (mine()) {
+                              if (ring.feeder() == feeder) {
                                   if (!wait(&ring.empty[ring.slot], ring.phase ^ 1)) return false;
-                                  uint32_t dst = moe::smem_addr(ring.stage() + off_x<DT>());
+                                  uint32_t dst = moe::smem_addr(ring.stage()) + off;
                                   const uint16_t *h = hi + k0, *l = lo + k0;
                                   const uint32_t tail = (uint32_t)(count * xs);
                                   for (int i = 0; i < count; ++i, dst += xs, h += a.ld_act, l += a.ld_act) {
@@ -1035,16 +1034,28 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
             }
             good = !group_any(kBarB, !ok);
             if (good) {
+                // batch * E is at most 4 kTeam; the next batch's logits are
+                // fetched while this one's experts are chosen
+                double l[4];
+                auto fetch = [&](int t0) {
+                    const int n = min(a.batch, a.T - t0) * a.E;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (rid + j * kTeam < n) l[j] = __ldcg(a.logits + (size_t)t0 * a.E + rid + j * kTeam);
+                };
+                fetch(0);
                 for (int t0 = 0; t0 < a.T; t0 += a.batch) {
                     const int nt = min(a.batch, a.T - t0);
-                    const double* l = a.logits + (size_t)t0 * a.E;
-#pragma unroll 4
-                    for (int i = rid; i < nt * a.E; i += kTeam) {
-                        const double s = 1.0 / (1.0 + exp(-__ldcg(l + i)));
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int i = rid + j * kTeam;
+                        if (i >= nt * a.E) continue;
+                        const double s = 1.0 / (1.0 + exp(-l[j]));
                         S.scores[i] = s;
                         S.keys[i] = sortable(s + (double)__ldg(a.bias + i % a.E));
                     }
                     group_any(kBarB, false);
+                    if (t0 + a.batch < a.T) fetch(t0 + a.batch);
                     if (kw < nt) choose(a, t0 + kw, S.keys + (size_t)kw * a.E, S.scores + (size_t)kw * a.E, S);
                     group_any(kBarB, false);
                 }
@@ -1071,13 +1082,8 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
             ok = wait(&ring.w[ring.slot], ring.phase) && wait(&ring.x[ring.slot], ring.phase);
             return ok;
         };
-        int turn = 0;            // whose stage it is, once both teams work
-        bool both = false;
-        auto my_stage = [&]() {
-            const bool m = !both || turn == team;
-            turn ^= 1;
-            return m;
-        };
+        bool both = false;       // the second team has joined
+        auto my_stage = [&]() { return !both || ring.team() == team; };
         auto release = [&]() {
             __syncwarp();
             if (lane == 0) moe::mbar_arrive(&ring.empty[ring.slot]);
@@ -1142,7 +1148,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
             walk_unit(a, count, [&](int, int kn) {
                 if (my_stage()) {
                     if (!ready()) return false;
-                    if (kw * kSlice < kn) mma_stage<DT, NT, false, FOLD>(ring.stage(), kw, count, col, acc);
+                    if (kw * kSlice < kn) mma_stage<DT, NT, false, FOLD>(ring.stage(), ring.stage() + ring.scales, kw, count, col, acc);
                     release();
                 }
                 ring.next();
@@ -1175,7 +1181,6 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
         if (good) ok = wait(&plan_ready, 0);
         good = !group_any(kBarAll, !(good && ok));
         both = true;
-        turn = 0;
         if (good)
             for (int u = P.cut1[cta]; good && u < P.cut1[cta + 1]; ++u)
                 good = gate_up(P.active[first_routed + u / upe], (u % upe) * NF);
@@ -1206,7 +1211,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
             auto stage = [&](int, int kn) {
                 // a given-up wait ends in row_end, which all warps reach
                 if (my_stage() && ok && ready()) {
-                    if (kw * kSlice < kn) mma_stage<DT, NT, true, FOLD>(ring.stage(), kw, count, col, acc);
+                    if (kw * kSlice < kn) mma_stage<DT, NT, true, FOLD>(ring.stage(), ring.stage() + ring.scales, kw, count, col, acc);
                     release();
                 }
                 ring.next();
@@ -1339,30 +1344,32 @@ moe_status_t few_check(const moe_config_t* c) {
     return MOE_OK;
 }
 
-// Tensor maps of a matrix stored in bytes, rows of `rb` bytes.  The inner
-// dimension is a 64-byte piece of a row, then 8 rows, then the pieces along K
-// (zero beyond the row's end), so that a box lands as 512-byte groups of 8
-// rows in the 64-byte swizzle.
-//   down:    {64, 8, rb / 64, rows / 8},            box {64, 8, PB, R / 8}
-//   gate/up: {64, 8, rb / 64, 2, row groups},       box {64, 8, PB, 2, R / 16}
-// where the fourth dimension steps from a gate row to its up row.
+// Tensor maps of a matrix stored in bytes, rows of `rb` bytes, all of five
+// dimensions.  A box of 256 columns lands as 128-byte pieces of 8 rows (1024
+// bytes, 128-byte swizzle), the pieces along K inside 8-row groups:
+//   {128, 8, rb / 128, halves, row groups}, box {128, 8, PB, halves, groups of a unit}
+// `halves` steps from a gate row to its up row (1 for the down matrix).  A
+// 4-bit row may end inside a piece, so there the first dimension is the whole
+// row and a box one piece of it ({rb, 8, 1, halves, row groups}); beyond a
+// row's end a box is filled with zeros.
 template <int DT>
 moe_status_t few_maps(FewArgs& a, const void* w13, const void* w2, const void* w13s, const void* w2s) {
     using F = Fmt<DT>;
-    const uint32_t pb = kBox * F::kBits / 512;
+    const bool whole = F::kBits == 4;
+    auto map = [&](CUtensorMap* m, const void* p, uint64_t K, uint64_t groups, uint32_t halves, uint64_t n,
+                   const char* what) {
+        const uint64_t rb = K * F::kBits / 8;
+        const uint64_t dims[5] = {whole ? rb : 128, 8, whole ? 1 : rb / 128, halves, groups};
+        const uint64_t strides[4] = {rb, 128, n * rb, 8 * rb};
+        const uint32_t box[5] = {128, 8, whole ? 1u : (uint32_t)kBox * F::kBits / 1024, halves,
+                                 F::kRows / 8 / halves};
+        return moe::api_make_map_u8_sw128(m, p, 5, dims, strides, box, what);
+    };
     auto gate_up = [&](CUtensorMap* m, const void* p, uint64_t experts, uint64_t n, const char* what) {
-        const uint64_t rb = (uint64_t)a.H * F::kBits / 8;
-        const uint64_t dims[5] = {64, 8, rb / 64, 2, (experts * 2 - 1) * n / 8};
-        const uint64_t strides[4] = {rb, 64, n * rb, 8 * rb};
-        const uint32_t box[5] = {64, 8, pb, 2, F::kRows / 16};
-        return moe::api_make_map_u8_sw64(m, p, 5, dims, strides, box, what);
+        return map(m, p, a.H, (experts * 2 - 1) * n / 8, 2, n, what);
     };
     auto down = [&](CUtensorMap* m, const void* p, uint64_t experts, uint64_t n, const char* what) {
-        const uint64_t rb = n * F::kBits / 8;
-        const uint64_t dims[4] = {64, 8, rb / 64, experts * a.H / 8};
-        const uint64_t strides[3] = {rb, 64, 8 * rb};
-        const uint32_t box[4] = {64, 8, pb, F::kRows / 8};
-        return moe::api_make_map_u8_sw64(m, p, 4, dims, strides, box, what);
+        return map(m, p, n, experts * a.H / 8, 1, 8, what);
     };
     FEW_TRY(gate_up(&a.m13, w13, a.E, a.I, "w13"));
     FEW_TRY(down(&a.m2, w2, a.E, a.I, "w2"));
@@ -1395,22 +1402,18 @@ moe_status_t few_smem(FewArgs& a, int limit, size_t* bytes) {
     a.off_red = off;
     off += kWarps * (F::kRows / 16) * NT * 512;
     a.off_ring = up(off, 1024);
+    // activation rows: 8 of a full stage, or in half a stage, behind its one
+    // box, as many as phase 2 can need
     const int full = kChunk * 2 + F::kPad, half = kBox * 2 + F::kPad;
-    const int x = a.T <= 4 ? 2 * a.T * full : 8 * full > 2 * a.T * half ? 8 * full : 2 * a.T * half;
-    a.stage_bytes = up(off_x<DT>() + x, 512);
-    const int stages = (limit - a.off_ring) / a.stage_bytes;
-    a.n_stages = (stages < kMaxStages ? stages : kMaxStages) & ~1;
-    // Who waits on a slot's barrier must not miss a whole turn of it, or it
-    // takes an old phase for the new one.  A team sees every second stage: an
-    // even number of slots gives it the same ones each time.  A feeder that
-    // waits for stage i to be free has seen stage i - kFeeders - n released;
-    // kFeeders being even, that was the same team's, which releases in order,
-    // so stage i - 2 n is released too when n >= kFeeders.
-    static_assert(kFeeders == 4, "an even number, at most the least number of stages");
-    if (a.n_stages < 4)
+    int x = (a.T <= 4 ? 2 * a.T : 8) * full;
+    if (a.T > 4 && 2 * a.T * half - kBoxBytes > x) x = 2 * a.T * half - kBoxBytes;
+    a.stage_bytes = up(2 * kBoxBytes + x + F::kScaleBytes, 1024);
+    const int stages = (limit - 1024 - a.off_ring) / a.stage_bytes;   // 1024: the boxes' alignment
+    a.n_stages = stages < kMaxStages ? stages : kMaxStages;
+    if (a.n_stages < kFeeders)
         return ffail(MOE_ERR_UNSUPPORTED, "%s: %lld bytes of shared memory hold too few stages", "few-token layer",
                      limit);
-    *bytes = (size_t)a.off_ring + (size_t)a.n_stages * a.stage_bytes;
+    *bytes = 1024 + (size_t)a.off_ring + (size_t)a.n_stages * a.stage_bytes;
     return MOE_OK;
 }
 
