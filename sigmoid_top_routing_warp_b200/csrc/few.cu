@@ -68,7 +68,8 @@ constexpr int kThreads = kConsumers + 32 + kFeeders * 32;
 constexpr int kRouterVecs = 4;                   // 16-byte vectors of a router lane at a time
 constexpr int kMaxBlocks = 256;                  // blocks the join buffer has room for
 constexpr int kHeadStart = 3;                    // stages copied before the router's loads are in
-constexpr int kAhead = 64;                       // steps of 128 columns fetched into L2 across barrier 1
+constexpr int kWindow = 3;                       // stages under way while the choice is made
+constexpr int kAhead = 24;                       // steps of 128 columns fetched into L2 across barrier 1
 // named barriers
 constexpr int kBarAll = 1, kBarB = 2, kBarRouted = 3, kBarA = 4, kBarLogits = 5;
 constexpr int kChunk = 512;                      // K columns of a full stage
@@ -386,9 +387,8 @@ __device__ void choose(const FewArgs& a, int t, const unsigned long long* key, c
 // ------------------------------------------------------------------ shares
 // What block c of G works on.  Phase 1: units of the shared expert (known
 // before the choice) and of the routed ones, each cut into G contiguous runs.
-// Phase 2: the (row block, expert, K) axis in steps of 128 columns.  Every
-// step moves the same bytes as H / 128 of a unit, so phase 2's cuts make up
-// for what phase 1's whole units leave uneven.
+// Phase 2: the (row block, expert, K) axis in steps of 128 columns, cut evenly
+// (barrier 1 has brought the blocks together).
 // c * n / G, rounded down: the product's fraction is a multiple of 1 / G, far
 // more than binary64 loses.
 __device__ __forceinline__ int cut(const FewArgs& a, int c, int n) {
@@ -400,19 +400,14 @@ template <int DT>
 __device__ void make_cuts(const FewArgs& a, const Plan& P, int n_active, int tid, int n) {
     constexpr int R = Fmt<DT>::kRows;
     const int G = gridDim.x, routed = n_active - (a.Is ? 1 : 0);
-    const int us = a.Is / (R / 2), ur = routed * (a.I / (R / 2)), ublk = a.H / 128;
-    const int tot2 = a.H / R * (a.Is / 128 + routed * (a.I / 128)), tot = (us + ur) * ublk + tot2;
-    // Taking earlier shares into account needs each to fit under the even
-    // share of the whole, or the cuts would run backwards.
-    const int lo = cut(a, 1, us + ur), s_most = cut(a, 1, us + G - 1);
-    const bool joint1 = lo >= s_most;
-    const int most = joint1 ? cut(a, 1, us + ur + G - 1) : s_most + cut(a, 1, ur + G - 1);
-    const bool joint2 = cut(a, 1, tot) >= most * ublk;
+    const int us = a.Is / (R / 2), ur = routed * (a.I / (R / 2));
+    const int tot2 = a.H / R * (a.Is / 128 + routed * (a.I / 128));
+    // Blocks with one shared unit more get one routed unit less, where every
+    // block has enough of them for the cuts not to run backwards.
+    const bool joint = cut(a, 1, us + ur) >= cut(a, 1, us + G - 1);
     for (int c = tid; c <= G; c += n) {
-        const int s = cut(a, c, us);
-        const int r = joint1 ? cut(a, c, us + ur) - s : cut(a, c, ur);
-        P.cut1[c] = r;
-        P.cut2[c] = joint2 ? cut(a, c, tot) - (s + r) * ublk : cut(a, c, tot2);
+        P.cut1[c] = joint ? cut(a, c, us + ur) - cut(a, c, us) : cut(a, c, ur);
+        P.cut2[c] = cut(a, c, tot2);
     }
 }
 
@@ -856,9 +851,16 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
         uint32_t issued = 0, last_phase = 0;   // slots in use, and their newest phase
         Source<DT> src;
         int nth = 0;
+        bool window = true;
         auto stage = [&](int k0, int kn) {
             if (nth++ == kHeadStart) bar_sync(kBarRouted, kConsumers + 32);
             if (!wait(&ring.empty[ring.slot], ring.phase ^ 1)) return false;
+            if (window) {
+                // more copies under way than HBM's latency needs would only
+                // queue, and the router's barrier and loads behind them
+                const int back = ring.slot - kWindow;
+                if (!wait(&ring.w[back < 0 ? back + ring.n : back], back < 0 ? ring.phase ^ 1 : ring.phase)) return false;
+            }
             src.stage(ring, k0, kn, policy);
             issued |= 1u << ring.slot;
             last_phase = (last_phase & ~(1u << ring.slot)) | (ring.phase << ring.slot);
@@ -875,6 +877,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
             nth = kHeadStart + 1;
         }
         ok = ok && wait(&plan_ready, 0);
+        window = false;
         if (ok) {
             for (int u = P.cut1[cta]; ok && u < P.cut1[cta + 1]; ++u) {
                 const Active& act = P.active[first_routed + u / upe];
