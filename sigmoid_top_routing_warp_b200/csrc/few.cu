@@ -7,22 +7,21 @@
 // one block per SM, each block walking its share of the weight rows through a
 // shared-memory ring while the multiplications keep up behind it.
 //
-// Roles in a block (21 warps):
-//   warps 0-15  consumers, two teams of eight that take stages in turn:
-//               m16n8k16 matrix instructions, 16 weight rows by 8 tokens; the
-//               tokens are the short side, so the 128-row tiles of tcgen05
-//               would be coarse units to share out over 148 SMs (a decode
-//               token touches 1728 16-row units but 216 of 128 rows), and 4-
-//               and 8-bit weights have to be widened in registers anyway.
-//               The second team first makes the choice and the plan of touched
-//               experts, while the first works on the shared expert, which
-//               needs neither
+// Roles in a block (20 warps):
+//   warps 0-15  consumers, each with 64 columns of every stage: m16n8k16
+//               matrix instructions, 16 weight rows by 8 tokens; the tokens
+//               are the short side, so the 128-row tiles of tcgen05 would be
+//               coarse units to share out over 148 SMs (a decode token touches
+//               1728 16-row units but 216 of 128 rows), and 4- and 8-bit
+//               weights have to be widened in registers anyway.  Warps 8-15
+//               first make the choice and the plan of touched experts, while
+//               warps 0-7 work on the shared expert, which needs neither
 //   warp 16     weight producer: tensor copies of the weights (and scales),
 //               stage by stage, as far ahead as the ring is deep
-//   warps 17-20 activation producers: the rows that the weights meet
+//   warps 17-19 activation producers: the rows that the weights meet
 //
 // Phases:
-//   R   a team per expert's logits; grid barrier 0; then every block repeats
+//   R   half a block per expert's logits; grid barrier 0; then every block repeats
 //       the choice (T * E keys) and the plan
 //   1   units of nf SwiGLU features of one expert (nf gate rows, nf up rows,
 //       all of K): SiLU(g) * u * w leaves as a bf16 head and a bf16 tail (16
@@ -48,6 +47,7 @@
 
 #include <cstdio>
 #include <cstring>
+#include <type_traits>
 
 namespace moe {
 moe_status_t api_check_config(const moe_config_t* c);
@@ -61,26 +61,26 @@ moe_status_t api_make_map_u8_sw128(CUtensorMap* m, const void* ptr, uint32_t ran
 namespace {
 
 constexpr int kT = MOE_FEW_MAX_T;
-constexpr int kWarps = 8;                        // of a team of consumers
-constexpr int kFeeders = 4;                      // warps that copy activations
+constexpr int kWarps = 8;                        // of a team: warps 0-7 (A) and 8-15 (B)
+constexpr int kFeeders = 3;                      // warps that copy activations
 constexpr int kTeam = kWarps * 32, kConsumers = 2 * kTeam;
 constexpr int kThreads = kConsumers + 32 + kFeeders * 32;
 constexpr int kRouterVecs = 4;                   // 16-byte vectors of a router lane at a time
 constexpr int kMaxBlocks = 256;                  // blocks the join buffer has room for
-constexpr int kHeadStart = 3;                    // stages copied before the router's loads are in
-constexpr int kWindow = 3;                       // stages under way while the choice is made
+constexpr int kHeadStart = 2;                    // stages copied before the router's loads are in
+constexpr int kWindow = 2;                       // stages under way while the choice is made
 constexpr int kAhead = 24;                       // steps of 128 columns fetched into L2 across barrier 1
 // named barriers
 constexpr int kBarAll = 1, kBarB = 2, kBarRouted = 3, kBarA = 4, kBarLogits = 5;
-constexpr int kChunk = 512;                      // K columns of a full stage
+constexpr int kChunk = 1024;                     // K columns of a full stage
 constexpr int kBox = 256;                        // K columns of one tensor copy
 constexpr int kBoxBytes = 8192;                  // its bytes, for every weight type
-constexpr int kSlice = kChunk / kWarps;          // K columns of a warp in a stage
-constexpr int kMaxStages = 16;
+constexpr int kSlice = 64;                       // K columns of a warp in a stage
+constexpr int kMaxStages = 8;
 constexpr int kBarWord = moe::kSchedFirstWord;   // grid barriers (2) and the exit count, in the status block
 
 // Per weight type: rows of a unit, bits of a weight, bytes of a stage's
-// scales, and the activation rows' padding in a stage.  A stage holds 16 KB of
+// scales, and the activation rows' padding in a stage.  A stage holds 32 KB of
 // weights, as 128-byte pieces of 8 rows (1024 bytes, 128-byte swizzle: 64-byte
 // pieces ran at 5 TB/s at most).  A lane's part of a piece, and the padding of
 // the activation rows, are chosen so that a load's lanes (8 rows by 4) fall on
@@ -96,11 +96,11 @@ struct Fmt<MOE_DTYPE_BF16> {
 };
 template <>
 struct Fmt<MOE_DTYPE_FP8_E4M3_BLOCK128> {
-    static constexpr int kRows = 32, kBits = 8, kScaleBytes = 128, kPad = 32;  // scales: [2][4] fp32
+    static constexpr int kRows = 32, kBits = 8, kScaleBytes = 128, kPad = 32;  // scales: [2][8] fp32
 };
 template <>
 struct Fmt<MOE_DTYPE_MXFP4_BLOCK32> {
-    static constexpr int kRows = 64, kBits = 4, kScaleBytes = 1024, kPad = 64;  // [64][16] e8m0
+    static constexpr int kRows = 64, kBits = 4, kScaleBytes = 2048, kPad = 64;  // [64][32] e8m0
 };
 
 struct FewArgs {
@@ -144,7 +144,7 @@ struct Scratch {
     unsigned long long* keys;   // [batch][E]
     double* scores;    // the same
     int* sel;          // [T, k]
-    float* selw;       // [T, k]
+    double* sels;      // [T, k] their scores
     uint32_t* emask;   // [E] tokens of each expert
     int* apos;         // [E] its place in the list
 };
@@ -177,6 +177,58 @@ __device__ __forceinline__ void bar_arrive(int id, int n) {
     asm volatile("barrier.cta.arrive %0, %1;" ::"r"(id), "r"(n) : "memory");
 }
 
+// Shared memory by 32-bit address.
+__device__ __forceinline__ uint4 lds128(uint32_t p) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(p));
+    return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t p) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(p));
+    return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t p) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(p));
+    return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t p) {
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(p));
+    return v;
+}
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ void bar_done(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// A wait that has not been met at once: bounded, and every lane of the warp
+// leaves it with the same answer.  `drain`: see moe::wait_bar.
+__device__ __noinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status,
+                                           bool drain) {
+    const long long t0 = clock64();
+    while (true) {
+        if (__all_sync(0xffffffffu, bar_try(bar, parity))) return true;
+        bool stop = !drain && *abort_flag;
+        if (clock64() - t0 > moe::kWaitLimit) {
+            if (!*abort_flag) atomicOr(status, moe::DEV_STATUS_TIMEOUT);
+            *abort_flag = 1;
+            stop = true;
+        }
+        if (__any_sync(0xffffffffu, stop)) return false;
+    }
+}
+
 // Tensor copies of one box, with an L2 policy, or into L2 only.
 __device__ __forceinline__ void box_load(uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1, int c2,
                                          int c3, int c4, uint64_t policy) {
@@ -201,8 +253,11 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
 __device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void arrive_copied(uint64_t* bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(moe::smem_addr(bar)) : "memory");
+__device__ __forceinline__ void arrive_copied(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void expect_bytes(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 
 // D += A B: bf16 operands for bf16 weights, binary16 for the others.
@@ -369,18 +424,10 @@ __device__ void choose(const FewArgs& a, int t, const unsigned long long* key, c
         }
         __syncwarp();
     }
-    const double my_s = lane < a.k ? score[my_e] : 0.0;
-    double sum = 0.0;
-    for (int j = 0; j < a.k; ++j) sum += __shfl_sync(0xffffffffu, my_s, j);
     if (lane < a.k) {
-        const float w = (float)((a.norm ? my_s / sum : my_s) * (double)a.rsf);
         S.sel[t * a.k + lane] = my_e;
-        S.selw[t * a.k + lane] = w;
+        S.sels[t * a.k + lane] = score[my_e];
         atomicOr(&S.emask[my_e], 1u << t);
-        if (blockIdx.x == 0) {
-            if (a.idx) a.idx[(size_t)t * a.k + lane] = my_e;
-            if (a.w) a.w[(size_t)t * a.k + lane] = w;
-        }
     }
 }
 
@@ -450,27 +497,35 @@ __device__ void build_plan(const FewArgs& a, const Plan& P, const Scratch& S, in
     } else {
         make_cuts<DT>(a, P, n_active, tid - 32, kTeam - 32);
     }
-    group_any(kBarB, false);
-    if (a.Is)
-        for (int t = tid; t < a.T; t += kTeam) P.pairw[t] = 1.0f;
+}
+
+// Routing weights of the pairs (the producers need not wait for them).
+__device__ void pair_weights(const FewArgs& a, const Plan& P, const Scratch& S, int tid) {
     for (int i = tid; i < a.T * a.k; i += kTeam) {
-        const Active act = P.active[S.apos[S.sel[i]]];
         const int t = i / a.k;
-        P.pairw[act.base + __popc(act.mask & ((1u << t) - 1u))] = S.selw[i];
+        double sum = 0.0;
+        for (int j = 0; j < a.k; ++j) sum += S.sels[t * a.k + j];
+        const double v = a.norm ? S.sels[i] / sum : S.sels[i];
+        const float w = (float)(v * (double)a.rsf);
+        const Active act = P.active[S.apos[S.sel[i]]];
+        P.pairw[act.base + __popc(act.mask & ((1u << t) - 1u))] = w;
+        if (blockIdx.x == 0) {
+            if (a.idx) a.idx[i] = S.sel[i];
+            if (a.w) a.w[i] = w;
+        }
     }
 }
 
 // ------------------------------------------------------------------ the ring
-// Slots of a stage, in the order every role walks them.  `w` and `x`: the
-// weights (and scales) and the activations have landed.
+// Slots of a stage, in the order every role walks them; 32-bit addresses.
+// Barriers of a slot: `w` and `x`, the weights (and scales) and the activations
+// have landed; `empty`, every consumer warp is through.
 struct Ring {
-    uint64_t *w, *x, *empty;
-    uint8_t* base;
+    uint32_t w, x, empty, base;
     int n, bytes, scales, slot;   // scales: their offset in a stage
     uint32_t phase;
-    // Teams and feeders own slots, so that whoever waits on a slot's barriers
-    // has waited on every turn of it and cannot take an old phase for a new one.
-    __device__ __forceinline__ int team() const { return slot & 1; }
+    // Feeders own slots: whoever waits on a slot's barriers has waited on every
+    // turn of it and cannot take an old phase for a new one.
     __device__ __forceinline__ int feeder() const { return slot % kFeeders; }
     __device__ __forceinline__ void next() {
         if (++slot == n) {
@@ -478,21 +533,22 @@ struct Ring {
             phase ^= 1;
         }
     }
-    __device__ __forceinline__ uint8_t* stage() const { return base + slot * bytes; }
+    __device__ __forceinline__ uint32_t stage() const { return base + slot * bytes; }
 };
 
 // Columns of a stage: above eight activation rows (heads and tails of every
-// pair in phase 2) there is room for half of them only.
+// pair in phase 2) there is room for half of them, above 16 for a quarter.
 __device__ __forceinline__ int chunk_cols(bool down, int count) {
-    return (down ? 2 * count : count) > 8 ? kBox : kChunk;
+    const int rows = down ? 2 * count : count;
+    return rows <= 8 ? kChunk : rows <= 16 ? kChunk / 2 : kChunk / 4;
 }
 template <int DT>
 __device__ __forceinline__ int x_stride(int cols) {
     return cols * 2 + Fmt<DT>::kPad;
 }
-// The activations stand behind the stage's boxes: a stage of half the columns
-// has one box and room for more rows.
-__device__ __forceinline__ int off_x(int cols) { return cols > kBox ? 2 * kBoxBytes : kBoxBytes; }
+// The activations stand behind the stage's boxes: a stage of fewer columns
+// has fewer boxes and room for more rows.
+__device__ __forceinline__ int off_x(int cols) { return cols / kBox * kBoxBytes; }
 
 // The stages of phase 1's unit with `count` tokens: stage(k0, kn).
 template <class Stage>
@@ -571,8 +627,8 @@ struct Source {
         auto row = [&](int r) { return dn ? down_row(a, expert, first, r) : gate_up_row(a, expert, first, r); };
         group = (int)(row(0) / 8);
         if (DT == MOE_DTYPE_FP8_E4M3_BLOCK128) {
-            // lanes 0-3: the blocks of the gate (or output) rows, 4-7: of the up rows
-            s0 = sc + (row(lane & 4 ? 8 : 0) / 128 * (K / 128) + (lane & 3)) * 4;
+            // lanes 0-7: the blocks of the gate (or output) rows, 8-15: of the up rows
+            s0 = sc + (row(lane & 8 ? 8 : 0) / 128 * (K / 128) + (lane & 7)) * 4;
         } else if (DT == MOE_DTYPE_MXFP4_BLOCK32) {
             s0 = sc + row(lane) * (K / 32);
             s1 = sc + row(lane + 32) * (K / 32);
@@ -592,41 +648,44 @@ struct Source {
     // All lanes: one tensor copy for each 256 columns, and the scales.
     __device__ __forceinline__ void stage(const Ring& ring, int k0, int kn, uint64_t policy) const {
         const int lane = threadIdx.x & 31;
-        const uint32_t dst = moe::smem_addr(ring.stage());
-        uint64_t* full = &ring.w[ring.slot];
+        const uint32_t dst = ring.stage(), bar = ring.w + 8 * ring.slot;
         if (lane == 0) {
-            const uint32_t bar = moe::smem_addr(full);
-            moe::mbar_arrive_expect_tx(full, kn > kBox ? 2 * kBoxBytes : kBoxBytes);
-            box_load(dst, map, bar, byte_of(k0), 0, piece_of(k0), 0, group, policy);
-            if (kn > kBox)
-                box_load(dst + kBoxBytes, map, bar, byte_of(k0 + kBox), 0, piece_of(k0 + kBox), 0, group, policy);
+            expect_bytes(bar, (kn + kBox - 1) / kBox * kBoxBytes);
+            for (int k = 0; k < kn; k += kBox)
+                box_load(dst + k / kBox * kBoxBytes, map, bar, byte_of(k0 + k), 0, piece_of(k0 + k), 0, group, policy);
         }
         const uint32_t sdst = dst + ring.scales;
         if (DT == MOE_DTYPE_FP8_E4M3_BLOCK128) {
-            if (lane < (down ? 4 : 8) && (lane & 3) * 128 < kn) copy4(sdst + lane * 4, s0 + k0 / 128 * 4);
-            arrive_copied(full);
+            if (lane < (down ? 8 : 16) && (lane & 7) * 128 < kn) copy4(sdst + lane * 4, s0 + k0 / 128 * 4);
+            arrive_copied(bar);
         } else if (DT == MOE_DTYPE_MXFP4_BLOCK32) {
-            // a row's 16 bytes start at a multiple of 16 when K / 32 and k0 / 32 do
-            const uint8_t *p0 = s0 + k0 / 32, *p1 = s1 + k0 / 32;
-            if (kn == kChunk && ((K | k0) & 511) == 0) {
-                copy16(sdst + lane * 16, p0);
-                copy16(sdst + (lane + 32) * 16, p1);
-            } else {
-                for (int j = 0; j < kn / 32; j += 4) {
-                    copy4(sdst + lane * 16 + j, p0 + j);
-                    copy4(sdst + (lane + 32) * 16 + j, p1 + j);
+            // 16 bytes of a row for 512 columns; they start at a multiple of 16
+            // when K / 32 and k0 / 32 do
+            for (int k = 0; k < kn; k += 512) {
+                const uint8_t *p0 = s0 + (k0 + k) / 32, *p1 = s1 + (k0 + k) / 32;
+                const uint32_t d0 = sdst + lane * 32 + k / 32, d1 = d0 + 1024;
+                if (kn - k >= 512 && ((K | k0) & 511) == 0) {
+                    copy16(d0, p0);
+                    copy16(d1, p1);
+                } else {
+                    for (int j = 0; j < min(512, kn - k) / 32; j += 4) {
+                        copy4(d0 + j, p0 + j);
+                        copy4(d1 + j, p1 + j);
+                    }
                 }
             }
-            arrive_copied(full);
+            arrive_copied(bar);
         }
     }
 };
 
 // Activation producer, all lanes of one warp: a row of kn columns.
 __device__ __forceinline__ void copy_row(uint32_t dst, const uint16_t* src, int kn) {
-    const int c = (threadIdx.x & 31) * 8;
-    if (c < kn) copy16(dst + c * 2, src + c);
-    if (c + 256 < kn) copy16(dst + c * 2 + 512, src + c + 256);
+#pragma unroll
+    for (int j = 0; j < kChunk / 256; ++j) {
+        const int c = (threadIdx.x & 31) * 8 + j * 256;
+        if (c < kn) copy16(dst + c * 2, src + c);
+    }
 }
 
 // ------------------------------------------------------------------ multiplication
@@ -649,17 +708,17 @@ __device__ __forceinline__ void widen_e2m1(uint32_t v, uint32_t (&p)[4]) {
 // The lane's activations of its column for the warp's 64 columns of K, in the
 // order of the weights' columns.
 template <int DT>
-__device__ __forceinline__ void load_acts(const uint8_t* row, int t, bool zero, uint32_t (&b)[8]) {
+__device__ __forceinline__ void load_acts(uint32_t row, int t, bool zero, uint32_t (&b)[8]) {
     if (DT == MOE_DTYPE_FP8_E4M3_BLOCK128) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const uint2 v = *reinterpret_cast<const uint2*>(row + j * 32 + t * 8);
+            const uint2 v = lds64(row + j * 32 + t * 8);
             b[2 * j] = v.x, b[2 * j + 1] = v.y;
         }
     } else {
         constexpr bool kWide = DT == MOE_DTYPE_BF16;
-        const uint4 v0 = *reinterpret_cast<const uint4*>(row + t * (kWide ? 32 : 16));
-        const uint4 v1 = *reinterpret_cast<const uint4*>(row + (kWide ? t * 32 + 16 : 64 + t * 16));
+        const uint4 v0 = lds128(row + t * (kWide ? 32 : 16));
+        const uint4 v1 = lds128(row + (kWide ? t * 32 + 16 : 64 + t * 16));
         b[0] = v0.x, b[1] = v0.y, b[2] = v0.z, b[3] = v0.w;
         b[4] = v1.x, b[5] = v1.y, b[6] = v1.z, b[7] = v1.w;
     }
@@ -689,79 +748,101 @@ __device__ __forceinline__ void to_f16(uint32_t (&b)[8], uint32_t lift) {
     }
 }
 
-// Which activation rows a lane multiplies in phase 1 (`row`: its column's
-// token's place in the unit's list) or in phase 2 (a column is a token).
-// Tiles are 8 columns.  With at most four tokens (FOLD) phase 2's tile holds
-// the heads in columns 0-3 and the tails in 4-7, which are added at the end;
-// otherwise heads and tails are two products.
+// Two binary32 operations in one instruction.
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& x, float& y) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+// Which activation rows a lane multiplies in phase 1 (its column's token's
+// place in the unit's list) or in phase 2 (a column is a token).  Tiles are 8
+// columns.  With at most four tokens (FOLD) phase 2's tile holds the heads in
+// columns 0-3 and the tails in 4-7, which are added at the end; otherwise heads
+// and tails are two products.
 template <int NT>
 struct Columns {
-    int row[NT];        // row of the stage's activations
+    int x[NT];          // the lane's row in a stage
+    int tail;           // from a head to its tail
     bool zero[NT];      // not the expert's token: the column adds nothing
     bool own[NT][2];    // the lane's two result columns are the expert's tokens
     bool on[NT];        // the tile has any
 };
 
 // One warp's part of a stage for one tile of tokens: all rows of the unit by
-// its 64 columns of K.  In phase 2 only the expert's own tokens add the
-// stage's products: an infinity or a NaN among its weights reaches no other.
-// A stage with tokens in both tiles does this twice: with 16 tokens 1.4 of
-// them meet an expert on average, and a branch at every product cost more.
+// 64 columns of K.  In phase 2 only the expert's own tokens add the stage's
+// products: an infinity or a NaN among its weights reaches no other.  A stage
+// with tokens in both tiles does this twice: with 16 tokens 1.4 of them meet
+// an expert on average, and a branch at every product cost more.
 template <int DT, int NT, bool DOWN, bool FOLD>
-__device__ __forceinline__ void mma_tile(const uint8_t* stage, const uint8_t* sc, int kw, int count,
-                                         const Columns<NT>& col, int nt, float (&acc)[Fmt<DT>::kRows / 16][NT][4]) {
+__device__ __forceinline__ void mma_tile(uint32_t stage, uint32_t sc, int slice, const Columns<NT>& col, int nt,
+                                         float (&acc)[Fmt<DT>::kRows / 16][NT][4]) {
     using F = Fmt<DT>;
     constexpr int MT = F::kRows / 16;
     constexpr int PB = kBox * F::kBits / 1024;       // 128-byte pieces of a row in a box
     constexpr bool TAIL = DOWN && !FOLD;             // a second product for the tails
     constexpr bool kBf16 = DT == MOE_DTYPE_BF16;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int cols = chunk_cols(DOWN, count), xs = x_stride<DT>(cols);
-    const uint8_t* x = stage + off_x(cols) + kw * kSlice * 2 + col.row[nt] * xs;
+    const uint32_t x = stage + col.x[nt] + slice * (kSlice * 2);
     uint32_t b[8], bl[8];
-    float back[2] = {1.0f, 1.0f};   // undoes the lift of the lane's two result columns
     load_acts<DT>(x, t, DOWN && col.zero[nt], b);
-    if (TAIL) load_acts<DT>(x + count * xs, t, col.zero[nt], bl);
+    if (TAIL) load_acts<DT>(x + col.tail, t, col.zero[nt], bl);
+    uint64_t back = 0;              // undoes the lift of the lane's two result columns
     if (!kBf16) {
         // a tail is at most 2^-8 of its head and takes the head's lift
         const uint32_t lift = block_lift(b);
         to_f16(b, lift);
         if (TAIL) to_f16(bl, lift);
         const float inv = __uint_as_float((254u - lift) << 23);
-        back[0] = __shfl_sync(0xffffffffu, inv, 8 * t);
-        back[1] = __shfl_sync(0xffffffffu, inv, 8 * t + 4);
+        back = pack2(__shfl_sync(0xffffffffu, inv, 8 * t), __shfl_sync(0xffffffffu, inv, 8 * t + 4));
     }
-    // this warp's columns in the boxes: row g of their piece, and the 16-byte
-    // parts' swizzle
-    const int c0 = kw * kSlice;
-    const uint8_t* w = stage + (c0 / kBox) * kBoxBytes + (c0 % kBox) * F::kBits / 1024 * 1024 + g * 128;
-    auto part = [&](int i) { return (((c0 * F::kBits / 128 & 7) + i) ^ g) << 4; };
+    // row g of the slice's piece; its 16-byte parts are swizzled by the row,
+    // and the slice's first part is a multiple of a power of two of them
+    constexpr int kParts = kSlice * F::kBits / 128;  // 8, 4, 2
+    const int in_box = slice & (kBox / kSlice - 1);
+    const uint32_t w = stage + slice / (kBox / kSlice) * kBoxBytes + in_box * kParts / 8 * 1024 + g * 128 +
+                       (kBf16 ? 0 : t * 4);
+    const int sw = (g ^ (in_box * kParts & 7)) << 4;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-        const uint8_t* w0 = w + (2 * mt) * PB * 1024;
-        const uint8_t* w1 = w0 + PB * 1024;
+        const uint32_t w0 = w + (2 * mt) * PB * 1024, w1 = w0 + PB * 1024;
         // products in independent chains: two halves of the slice, heads and tails
         float c[2][4] = {}, cl[2][4] = {};
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             uint32_t m[2][4];
             if (kBf16) {
-                const uint4 p = *reinterpret_cast<const uint4*>(w0 + part(2 * t + h));
-                const uint4 q = *reinterpret_cast<const uint4*>(w1 + part(2 * t + h));
+                const uint4 p = lds128(w0 + ((2 * t + h) << 4 ^ sw)), q = lds128(w1 + ((2 * t + h) << 4 ^ sw));
                 m[0][0] = p.x, m[0][1] = q.x, m[0][2] = p.y, m[0][3] = q.y;
                 m[1][0] = p.z, m[1][1] = q.z, m[1][2] = p.w, m[1][3] = q.w;
             } else if (DT == MOE_DTYPE_FP8_E4M3_BLOCK128) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const int off = part(2 * h + i) + t * 4;
-                    widen_e4m3(*reinterpret_cast<const uint32_t*>(w0 + off), m[i][0], m[i][2]);
-                    widen_e4m3(*reinterpret_cast<const uint32_t*>(w1 + off), m[i][1], m[i][3]);
+                    widen_e4m3(lds32(w0 + ((2 * h + i) << 4 ^ sw)), m[i][0], m[i][2]);
+                    widen_e4m3(lds32(w1 + ((2 * h + i) << 4 ^ sw)), m[i][1], m[i][3]);
                 }
             } else {
-                const int off = part(h) + t * 4;
                 uint32_t p[4], q[4];
-                widen_e2m1(*reinterpret_cast<const uint32_t*>(w0 + off), p);
-                widen_e2m1(*reinterpret_cast<const uint32_t*>(w1 + off), q);
+                widen_e2m1(lds32(w0 + (h << 4 ^ sw)), p);
+                widen_e2m1(lds32(w1 + (h << 4 ^ sw)), q);
                 m[0][0] = p[0], m[0][1] = q[0], m[0][2] = p[1], m[0][3] = q[1];
                 m[1][0] = p[2], m[1][1] = q[2], m[1][2] = p[3], m[1][3] = q[3];
             }
@@ -771,37 +852,50 @@ __device__ __forceinline__ void mma_tile(const uint8_t* stage, const uint8_t* sc
                 if (TAIL) mma16<kBf16>(cl[h], m[i], bl[4 * h + 2 * i], bl[4 * h + 2 * i + 1]);
             }
         }
-        float s[2][2];          // [half][rows g, rows g + 8]
+        uint64_t s[2][2];          // [half][rows g, rows g + 8]
         if (DT == MOE_DTYPE_FP8_E4M3_BLOCK128) {
-            const float* fs = reinterpret_cast<const float*>(sc) + c0 / 128;
-            s[0][0] = fs[0];
-            s[0][1] = DOWN ? fs[0] : fs[4];
+            const float s0 = __uint_as_float(lds32(sc + slice / 2 * 4));
+            const float s1 = DOWN ? s0 : __uint_as_float(lds32(sc + slice / 2 * 4 + 32));
+            s[0][0] = pack2(s0, s0);
+            s[0][1] = pack2(s1, s1);
         } else if (DT == MOE_DTYPE_MXFP4_BLOCK32) {
-            const uint8_t* sr = sc + (mt * 16 + g) * 16 + kw * 2;
-            e8m0x2(*reinterpret_cast<const uint16_t*>(sr), s[0][0], s[1][0]);
-            e8m0x2(*reinterpret_cast<const uint16_t*>(sr + 128), s[0][1], s[1][1]);
+            const uint32_t sr = sc + (mt * 16 + g) * 32 + slice * 2;
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                float lo, hi;
+                e8m0x2(lds16(sr + r * 256), lo, hi);
+                s[0][r] = pack2(lo, lo);
+                s[1][r] = pack2(hi, hi);
+            }
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float v0 = TAIL ? c[0][j] + cl[0][j] : c[0][j], v1 = TAIL ? c[1][j] + cl[1][j] : c[1][j];
-            float v;
+        for (int r = 0; r < 2; ++r) {
+            uint64_t v0 = pack2(c[0][2 * r], c[0][2 * r + 1]), v1 = pack2(c[1][2 * r], c[1][2 * r + 1]);
+            if (TAIL) {
+                v0 = add2(v0, pack2(cl[0][2 * r], cl[0][2 * r + 1]));
+                v1 = add2(v1, pack2(cl[1][2 * r], cl[1][2 * r + 1]));
+            }
+            uint64_t v;
             if (kBf16)
-                v = v0 + v1;
+                v = add2(v0, v1);
             else if (DT == MOE_DTYPE_FP8_E4M3_BLOCK128)
-                v = (v0 + v1) * s[0][j >> 1] * back[j & 1];
+                v = mul2(mul2(add2(v0, v1), s[0][r]), back);
             else
-                v = fmaf(v0, s[0][j >> 1], v1 * s[1][j >> 1]) * back[j & 1];
-            acc[mt][nt][j] += !DOWN || col.own[nt][j & 1] ? v : 0.0f;
+                v = mul2(fma2(v0, s[0][r], mul2(v1, s[1][r])), back);
+            float x0, x1;
+            unpack2(v, x0, x1);
+            acc[mt][nt][2 * r] += !DOWN || col.own[nt][0] ? x0 : 0.0f;
+            acc[mt][nt][2 * r + 1] += !DOWN || col.own[nt][1] ? x1 : 0.0f;
         }
     }
 }
 
 template <int DT, int NT, bool DOWN, bool FOLD>
-__device__ __forceinline__ void mma_stage(const uint8_t* stage, const uint8_t* sc, int kw, int count,
-                                          const Columns<NT>& col, float (&acc)[Fmt<DT>::kRows / 16][NT][4]) {
+__device__ __forceinline__ void mma_stage(uint32_t stage, uint32_t sc, int slice, const Columns<NT>& col,
+                                          float (&acc)[Fmt<DT>::kRows / 16][NT][4]) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
-        if (NT == 1 || col.on[nt]) mma_tile<DT, NT, DOWN, FOLD>(stage, sc, kw, count, col, nt, acc);
+        if (NT == 1 || col.on[nt]) mma_tile<DT, NT, DOWN, FOLD>(stage, sc, slice, col, nt, acc);
 }
 
 // ------------------------------------------------------------------ the kernel
@@ -810,8 +904,7 @@ template <int DT, int NT, bool FOLD>
 __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant__ FewArgs a) {
     using F = Fmt<DT>;
     constexpr int R = F::kRows, MT = R / 16, NF = R / 2;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ uint64_t bar_w[kMaxStages], bar_x[kMaxStages], bar_empty[kMaxStages], plan_ready;
     __shared__ int n_active_sh, abort_sh, last_sh;
     __shared__ double part[2][kWarps][kT];
@@ -825,15 +918,17 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
         for (int i = 0; i < a.n_stages; ++i) {
             moe::mbar_init(&bar_w[i], F::kScaleBytes ? 33 : 1);  // the boxes' bytes, the lanes' scale copies
             moe::mbar_init(&bar_x[i], 32);                       // the lanes' copies
-            moe::mbar_init(&bar_empty[i], kWarps);
+            moe::mbar_init(&bar_empty[i], 2 * kWarps);           // consumer warps
         }
         moe::mbar_init(&plan_ready, 1);
         abort_sh = 0;
         moe::fence_barrier_init();
     }
     __syncthreads();
-    Ring ring{bar_w, bar_x, bar_empty, smem + a.off_ring, a.n_stages, a.stage_bytes, a.stage_bytes - F::kScaleBytes,
-              0, 0};
+    // the boxes' swizzle follows the address: 1024-byte alignment of the ring
+    Ring ring{moe::smem_addr(bar_w), moe::smem_addr(bar_x), moe::smem_addr(bar_empty),
+              (moe::smem_addr(smem) + a.off_ring + 1023) & ~1023u, a.n_stages, a.stage_bytes,
+              a.stage_bytes - F::kScaleBytes, 0, 0};
     int* bars = a.status + kBarWord;
     const int cta = blockIdx.x, G = gridDim.x;
     const Active shared{-1, (1u << a.T) - 1u, 0, a.T};
@@ -841,9 +936,11 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
     const int s0 = cut(a, cta, a.Is / NF), s1 = cut(a, cta + 1, a.Is / NF);
     const int shared_stages = (s1 - s0) * unit_stages(a, a.T);
     // a wait that every lane of the warp takes and leaves together
-    auto wait = [&](uint64_t* bar, uint32_t parity) {
-        return __all_sync(0xffffffffu, moe::wait_bar(bar, parity, abort_flag, a.status)) != 0;
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+        if (__all_sync(0xffffffffu, bar_try(bar, parity))) return true;
+        return bar_wait_slow(bar, parity, abort_flag, a.status, false);
     };
+    const uint32_t plan_bar = moe::smem_addr(&plan_ready);
 
     if (warp == 2 * kWarps) {
         // ---------------------------------------------------------- weight producer
@@ -854,12 +951,13 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
         bool window = true;
         auto stage = [&](int k0, int kn) {
             if (nth++ == kHeadStart) bar_sync(kBarRouted, kConsumers + 32);
-            if (!wait(&ring.empty[ring.slot], ring.phase ^ 1)) return false;
+            if (!wait(ring.empty + 8 * ring.slot, ring.phase ^ 1)) return false;
             if (window) {
                 // more copies under way than HBM's latency needs would only
                 // queue, and the router's barrier and loads behind them
-                const int back = ring.slot - kWindow;
-                if (!wait(&ring.w[back < 0 ? back + ring.n : back], back < 0 ? ring.phase ^ 1 : ring.phase)) return false;
+                const int back = ring.slot - min(kWindow, ring.n - 1);
+                if (!wait(ring.w + 8 * (back < 0 ? back + ring.n : back), back < 0 ? ring.phase ^ 1 : ring.phase))
+                    return false;
             }
             src.stage(ring, k0, kn, policy);
             issued |= 1u << ring.slot;
@@ -876,7 +974,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
             bar_sync(kBarRouted, kConsumers + 32);
             nth = kHeadStart + 1;
         }
-        ok = ok && wait(&plan_ready, 0);
+        ok = ok && wait(plan_bar, 0);
         window = false;
         if (ok) {
             for (int u = P.cut1[cta]; ok && u < P.cut1[cta + 1]; ++u) {
@@ -916,12 +1014,12 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
         // no copy may still be in flight when the block leaves
         if (!ok)
             for (int i = 0; i < a.n_stages; ++i)
-                if (issued >> i & 1u) moe::wait_bar(&bar_w[i], last_phase >> i & 1u, abort_flag, a.status, true);
+                if (issued >> i & 1u) bar_wait_slow(ring.w + 8 * i, last_phase >> i & 1u, abort_flag, a.status, true);
     } else if (warp > 2 * kWarps) {
         // ---------------------------------------------------------- activation producers
         const int feeder = warp - 2 * kWarps - 1;
         auto fed = [&]() {
-            arrive_copied(&ring.x[ring.slot]);
+            arrive_copied(ring.x + 8 * ring.slot);
         };
         uint32_t mask = 0;
         int xs = 0, off = 0;     // of the unit's stages
@@ -932,8 +1030,8 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
         };
         auto stage_x = [&](int k0, int kn) {
             if (ring.feeder() == feeder) {
-                if (!wait(&ring.empty[ring.slot], ring.phase ^ 1)) return false;
-                uint32_t dst = moe::smem_addr(ring.stage()) + off;
+                if (!wait(ring.empty + 8 * ring.slot, ring.phase ^ 1)) return false;
+                uint32_t dst = ring.stage() + off;
                 for (uint32_t m = mask; m; m &= m - 1, dst += xs)
                     copy_row(dst, a.x + (size_t)(__ffs(m) - 1) * a.H + k0, kn);
                 fed();
@@ -945,7 +1043,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
         mask = shared.mask;
         shape(false, a.T);
         for (int u = s0; ok && u < s1; ++u) ok = walk_unit(a, a.T, stage_x);
-        ok = ok && wait(&plan_ready, 0);
+        ok = ok && wait(plan_bar, 0);
         if (ok) {
             for (int u = P.cut1[cta]; ok && u < P.cut1[cta + 1]; ++u) {
                 const Active& act = P.active[first_routed + u / upe];
@@ -981,8 +1079,8 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
                           },
                           [&](int k0, int kn) {
                               if (ring.feeder() == feeder) {
-                                  if (!wait(&ring.empty[ring.slot], ring.phase ^ 1)) return false;
-                                  uint32_t dst = moe::smem_addr(ring.stage()) + off;
+                                  if (!wait(ring.empty + 8 * ring.slot, ring.phase ^ 1)) return false;
+                                  uint32_t dst = ring.stage() + off;
                                   const uint16_t *h = hi + k0, *l = lo + k0;
                                   const uint32_t tail = (uint32_t)(count * xs);
                                   for (int i = 0; i < count; ++i, dst += xs, h += a.ld_act, l += a.ld_act) {
@@ -1013,12 +1111,15 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
             Scratch S;
             S.keys = reinterpret_cast<unsigned long long*>(smem + a.off_scratch);
             S.scores = reinterpret_cast<double*>(S.keys + (size_t)a.batch * a.E);
-            S.sel = reinterpret_cast<int*>(S.scores + (size_t)a.batch * a.E);
-            S.selw = reinterpret_cast<float*>(S.sel + a.T * a.k);
-            S.emask = reinterpret_cast<uint32_t*>(S.selw + a.T * a.k);
+            S.sels = S.scores + (size_t)a.batch * a.E;
+            S.sel = reinterpret_cast<int*>(S.sels + a.T * a.k);
+            S.emask = reinterpret_cast<uint32_t*>(S.sel + a.T * a.k);
             S.apos = reinterpret_cast<int*>(S.emask + a.E);
             for (int i = cta * kTeam + rid; i < a.H / R; i += G * kTeam) a.joined[i] = 0;
             for (int e = rid; e < a.E; e += kTeam) S.emask[e] = 0;
+            float bias[4];           // of this thread's experts
+#pragma unroll
+            for (int j = 0; j < 4; ++j) bias[j] = __ldg(a.bias + (rid + j * kTeam) % a.E);
             __threadfence();
             bar_sync(kBarLogits, kConsumers);
             // barrier 0: every block's logits are written
@@ -1055,7 +1156,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
                         if (i >= nt * a.E) continue;
                         const double s = 1.0 / (1.0 + exp(-l[j]));
                         S.scores[i] = s;
-                        S.keys[i] = sortable(s + (double)__ldg(a.bias + i % a.E));
+                        S.keys[i] = sortable(s + (double)bias[j]);
                     }
                     group_any(kBarB, false);
                     if (t0 + a.batch < a.T) fetch(t0 + a.batch);
@@ -1065,6 +1166,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
                 build_plan<DT>(a, P, S, rid);
                 group_any(kBarB, false);
                 if (rid == 0) moe::mbar_arrive(&plan_ready);
+                pair_weights(a, P, S, rid);
             }
             // the shared expert's stages are the first team's
             ring.slot = shared_stages % a.n_stages;
@@ -1072,7 +1174,8 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
         }
         float acc[MT][NT][4];
         Columns<NT> col;
-        int count = 0;
+        bool both = false;       // warps 8-15 have joined
+        int flip = 0;            // a stage of half the columns goes to one half of the warps, then to the other
         auto clear = [&]() {
 #pragma unroll
             for (int m = 0; m < MT; ++m)
@@ -1081,15 +1184,31 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
 #pragma unroll
                     for (int j = 0; j < 4; ++j) acc[m][i][j] = 0.0f;
         };
-        auto ready = [&]() {
-            ok = wait(&ring.w[ring.slot], ring.phase) && wait(&ring.x[ring.slot], ring.phase);
-            return ok;
-        };
-        bool both = false;       // the second team has joined
-        auto my_stage = [&]() { return !both || ring.team() == team; };
         auto release = [&]() {
             __syncwarp();
-            if (lane == 0) moe::mbar_arrive(&ring.empty[ring.slot]);
+            // before they join, warps 0-7 answer for warps 8-15 too
+            if (lane < (both ? 1 : 2)) bar_done(ring.empty + 8 * ring.slot);
+            ring.next();
+        };
+        // one stage of kn columns; false when a wait was given up
+        auto step = [&](auto down, int kn) {
+            constexpr bool kDown = decltype(down)::value;
+            ok = wait(ring.w + 8 * ring.slot, ring.phase) && wait(ring.x + 8 * ring.slot, ring.phase);
+            if (!ok) return false;
+            const uint32_t st = ring.stage();
+            if (both) {
+                int slice = warp;
+                if (kn <= kChunk / 2) {
+                    slice = (warp + flip) & 15;
+                    flip ^= 8;
+                }
+                if (slice * kSlice < kn) mma_stage<DT, NT, kDown, FOLD>(st, st + ring.scales, slice, col, acc);
+            } else {
+                for (int slice = kw; slice * kSlice < kn; slice += kWarps)
+                    mma_stage<DT, NT, kDown, FOLD>(st, st + ring.scales, slice, col, acc);
+            }
+            release();
+            return true;
         };
         // Leaves the warps' sums in red (once the last ones have been read),
         // the second team's added to the first's, and waits for all of them;
@@ -1142,21 +1261,13 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
         };
         auto gate_up = [&](const Active& act, int f0) {
             clear();
-            count = act.count;
+            const int count = act.count, cols = chunk_cols(false, count);
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
-                col.row[i] = 8 * i + g < count ? 8 * i + g : 0;
+                col.x[i] = off_x(cols) + (8 * i + g < count ? 8 * i + g : 0) * x_stride<DT>(cols);
                 col.on[i] = count > 8 * i;
             }
-            walk_unit(a, count, [&](int, int kn) {
-                if (my_stage()) {
-                    if (!ready()) return false;
-                    if (kw * kSlice < kn) mma_stage<DT, NT, false, FOLD>(ring.stage(), ring.stage() + ring.scales, kw, count, col, acc);
-                    release();
-                }
-                ring.next();
-                return true;
-            });
+            walk_unit(a, count, [&](int, int kn) { return step(std::false_type{}, kn); });
             if (gather()) return false;
             if (tid < MT * NT * 32) {
                 const float4 s = reduced();
@@ -1181,7 +1292,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
 
         if (team == 0)
             for (int u = s0; good && u < s1; ++u) good = gate_up(shared, u * NF);
-        if (good) ok = wait(&plan_ready, 0);
+        if (good) ok = wait(plan_bar, 0);
         good = !group_any(kBarAll, !(good && ok));
         both = true;
         if (good)
@@ -1196,28 +1307,25 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
             const int wsum = a.Is / 128 + (n_active_sh - first_routed) * (a.I / 128);
             clear();
             auto item = [&](int, const Active& act) {
-                count = act.count;
+                const int cols = chunk_cols(true, act.count), xs = x_stride<DT>(cols);
+                col.tail = act.count * xs;
 #pragma unroll
                 for (int i = 0; i < NT; ++i) {
                     const int tok = FOLD ? g & 3 : 8 * i + g;
                     const bool has = act.mask >> tok & 1u;
+                    const int row = __popc(act.mask & ((1u << tok) - 1u)) + (FOLD && g >= 4 ? act.count : 0);
                     col.zero[i] = !has;
-                    col.row[i] = has ? __popc(act.mask & ((1u << tok) - 1u)) + (FOLD && g >= 4 ? count : 0) : 0;
+                    col.x[i] = off_x(cols) + (has ? row * xs : 0);
 #pragma unroll
                     for (int j = 0; j < 2; ++j)
                         col.own[i][j] = act.mask >> (FOLD ? (2 * t + j) & 3 : 8 * i + 2 * t + j) & 1u;
+                    col.on[i] = act.mask >> (8 * i) & 255u;
                 }
-#pragma unroll
-                for (int i = 0; i < NT; ++i) col.on[i] = act.mask >> (8 * i) & 255u;
                 return true;
             };
+            // a given-up wait ends in row_end, which all warps reach
             auto stage = [&](int, int kn) {
-                // a given-up wait ends in row_end, which all warps reach
-                if (my_stage() && ok && ready()) {
-                    if (kw * kSlice < kn) mma_stage<DT, NT, true, FOLD>(ring.stage(), ring.stage() + ring.scales, kw, count, col, acc);
-                    release();
-                }
-                ring.next();
+                if (ok) step(std::true_type{}, kn);
                 return true;
             };
             auto row_end = [&](int rb) {
@@ -1401,19 +1509,15 @@ moe_status_t few_smem(FewArgs& a, int limit, size_t* bytes) {
     // tokens chosen at a time, so that their keys and scores stay within 16 KB
     const int most = a.E <= 256 ? 4 : a.E <= 512 ? 2 : 1;
     a.batch = a.T < most ? a.T : most;
-    off = up(off + a.batch * a.E * 16 + n * 8 + a.E * 8, 16);
+    off = up(off + a.batch * a.E * 16 + n * 12 + a.E * 8, 16);
     a.off_red = off;
     off += kWarps * (F::kRows / 16) * NT * 512;
     a.off_ring = up(off, 1024);
-    // activation rows: 8 of a full stage, or in half a stage, behind its one
-    // box, as many as phase 2 can need
-    const int full = kChunk * 2 + F::kPad, half = kBox * 2 + F::kPad;
-    int x = (a.T <= 4 ? 2 * a.T : 8) * full;
-    if (a.T > 4 && 2 * a.T * half - kBoxBytes > x) x = 2 * a.T * half - kBoxBytes;
-    a.stage_bytes = up(2 * kBoxBytes + x + F::kScaleBytes, 1024);
+    // eight activation rows of a full stage; fewer columns leave room for more
+    a.stage_bytes = up(kChunk / kBox * kBoxBytes + (a.T <= 4 ? 2 * a.T : 8) * (kChunk * 2 + F::kPad) + F::kScaleBytes, 1024);
     const int stages = (limit - 1024 - a.off_ring) / a.stage_bytes;   // 1024: the boxes' alignment
     a.n_stages = stages < kMaxStages ? stages : kMaxStages;
-    if (a.n_stages < kFeeders)
+    if (a.n_stages < 2)
         return ffail(MOE_ERR_UNSUPPORTED, "%s: %lld bytes of shared memory hold too few stages", "few-token layer",
                      limit);
     *bytes = 1024 + (size_t)a.off_ring + (size_t)a.n_stages * a.stage_bytes;
