@@ -260,19 +260,22 @@ __device__ __forceinline__ void expect_bytes(uint32_t bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 
-// D += A B: bf16 operands for bf16 weights, binary16 for the others.
+// D = A B + C: bf16 operands for bf16 weights, binary16 for the others.
 template <bool BF16>
-__device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1,
+                                      const float (&c)[4]) {
     if (BF16)
         asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9},"
-            " {%0, %1, %2, %3};"
-            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+            " {%10, %11, %12, %13};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]),
+              "f"(c[3]));
     else
         asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9},"
-            " {%0, %1, %2, %3};"
-            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+            " {%10, %11, %12, %13};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]),
+              "f"(c[3]));
 }
 
 // Two e8m0 scale bytes -> binary32 (0 is 2^-127, 255 NaN): both are bf16 values.
@@ -708,7 +711,7 @@ __device__ __forceinline__ void widen_e2m1(uint32_t v, uint32_t (&p)[4]) {
 // The lane's activations of its column for the warp's 64 columns of K, in the
 // order of the weights' columns.
 template <int DT>
-__device__ __forceinline__ void load_acts(uint32_t row, int t, bool zero, uint32_t (&b)[8]) {
+__device__ __forceinline__ void load_acts(uint32_t row, int t, uint32_t (&b)[8]) {
     if (DT == MOE_DTYPE_FP8_E4M3_BLOCK128) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -722,9 +725,6 @@ __device__ __forceinline__ void load_acts(uint32_t row, int t, bool zero, uint32
         b[0] = v0.x, b[1] = v0.y, b[2] = v0.z, b[3] = v0.w;
         b[4] = v1.x, b[5] = v1.y, b[6] = v1.z, b[7] = v1.w;
     }
-    if (zero)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) b[i] = 0;
 }
 
 // Exponent field (biased) of the factor that takes the largest of the column's
@@ -748,53 +748,69 @@ __device__ __forceinline__ void to_f16(uint32_t (&b)[8], uint32_t lift) {
     }
 }
 
-// Two binary32 operations in one instruction.
-__device__ __forceinline__ uint64_t pack2(float x, float y) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
-    return r;
-}
-__device__ __forceinline__ void unpack2(uint64_t v, float& x, float& y) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-
 // Which activation rows a lane multiplies in phase 1 (its column's token's
-// place in the unit's list) or in phase 2 (a column is a token).  Tiles are 8
-// columns.  With at most four tokens (FOLD) phase 2's tile holds the heads in
-// columns 0-3 and the tails in 4-7, which are added at the end; otherwise heads
-// and tails are two products.
+// place in the unit's list) or in phase 2 (a column is a token; one that does
+// not use the expert multiplies some row, and its products are dropped).
+// Tiles are 8 columns.  With at most four tokens (FOLD) phase 2's tile holds
+// the heads in columns 0-3 and the tails in 4-7, which are added at the end;
+// otherwise heads and tails are two products.
 template <int NT>
 struct Columns {
     int x[NT];          // the lane's row in a stage
     int tail;           // from a head to its tail
-    bool zero[NT];      // not the expert's token: the column adds nothing
     bool own[NT][2];    // the lane's two result columns are the expert's tokens
     bool on[NT];        // the tile has any
 };
 
+// Sums of a warp.  `acc` is what its unit (or row block) has so far; bf16
+// products need no scale and run on in `run`, two chains, from the first stage
+// of an expert to its last.
+template <int DT, int NT>
+struct Sums {
+    static constexpr int MT = Fmt<DT>::kRows / 16;
+    static constexpr int RUN = DT == MOE_DTYPE_BF16 ? 2 : 0;
+    float acc[MT][NT][4];
+    float run[NT][RUN + 1][4];
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[m][i][j] = 0.0f;
+        restart();
+    }
+    __device__ __forceinline__ void restart() {
+        if constexpr (RUN > 0) {
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int h = 0; h < RUN; ++h)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) run[i][h][j] = 0.0f;
+        }
+    }
+    // The expert's products join the columns that are its tokens: an infinity
+    // or a NaN among its weights reaches no other.
+    __device__ __forceinline__ void fold(const Columns<NT>& col, bool all) {
+        if constexpr (RUN > 0) {
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (all || col.own[i][j & 1]) acc[0][i][j] += run[i][0][j] + run[i][1][j];
+            restart();
+        }
+    }
+};
+
 // One warp's part of a stage for one tile of tokens: all rows of the unit by
-// 64 columns of K.  In phase 2 only the expert's own tokens add the stage's
-// products: an infinity or a NaN among its weights reaches no other.  A stage
-// with tokens in both tiles does this twice: with 16 tokens 1.4 of them meet
-// an expert on average, and a branch at every product cost more.
+// 64 columns of K.  A stage with tokens in both tiles does this twice: with 16
+// tokens 1.4 of them meet an expert on average, and a branch at every product
+// cost more.
 template <int DT, int NT, bool DOWN, bool FOLD>
 __device__ __forceinline__ void mma_tile(uint32_t stage, uint32_t sc, int slice, const Columns<NT>& col, int nt,
-                                         float (&acc)[Fmt<DT>::kRows / 16][NT][4]) {
+                                         Sums<DT, NT>& sum) {
     using F = Fmt<DT>;
     constexpr int MT = F::kRows / 16;
     constexpr int PB = kBox * F::kBits / 1024;       // 128-byte pieces of a row in a box
@@ -803,16 +819,17 @@ __device__ __forceinline__ void mma_tile(uint32_t stage, uint32_t sc, int slice,
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const uint32_t x = stage + col.x[nt] + slice * (kSlice * 2);
     uint32_t b[8], bl[8];
-    load_acts<DT>(x, t, DOWN && col.zero[nt], b);
-    if (TAIL) load_acts<DT>(x + col.tail, t, col.zero[nt], bl);
-    uint64_t back = 0;              // undoes the lift of the lane's two result columns
+    load_acts<DT>(x, t, b);
+    if (TAIL) load_acts<DT>(x + col.tail, t, bl);
+    float back[2] = {1.0f, 1.0f};   // undoes the lift of the lane's two result columns
     if (!kBf16) {
         // a tail is at most 2^-8 of its head and takes the head's lift
         const uint32_t lift = block_lift(b);
         to_f16(b, lift);
         if (TAIL) to_f16(bl, lift);
         const float inv = __uint_as_float((254u - lift) << 23);
-        back = pack2(__shfl_sync(0xffffffffu, inv, 8 * t), __shfl_sync(0xffffffffu, inv, 8 * t + 4));
+        back[0] = __shfl_sync(0xffffffffu, inv, 8 * t);
+        back[1] = __shfl_sync(0xffffffffu, inv, 8 * t + 4);
     }
     // row g of the slice's piece; its 16-byte parts are swizzled by the row,
     // and the slice's first part is a multiple of a power of two of them
@@ -821,81 +838,77 @@ __device__ __forceinline__ void mma_tile(uint32_t stage, uint32_t sc, int slice,
     const uint32_t w = stage + slice / (kBox / kSlice) * kBoxBytes + in_box * kParts / 8 * 1024 + g * 128 +
                        (kBf16 ? 0 : t * 4);
     const int sw = (g ^ (in_box * kParts & 7)) << 4;
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-        const uint32_t w0 = w + (2 * mt) * PB * 1024, w1 = w0 + PB * 1024;
-        // products in independent chains: two halves of the slice, heads and tails
-        float c[2][4] = {}, cl[2][4] = {};
+    if constexpr (kBf16) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            uint32_t m[2][4];
-            if (kBf16) {
-                const uint4 p = lds128(w0 + ((2 * t + h) << 4 ^ sw)), q = lds128(w1 + ((2 * t + h) << 4 ^ sw));
-                m[0][0] = p.x, m[0][1] = q.x, m[0][2] = p.y, m[0][3] = q.y;
-                m[1][0] = p.z, m[1][1] = q.z, m[1][2] = p.w, m[1][3] = q.w;
-            } else if (DT == MOE_DTYPE_FP8_E4M3_BLOCK128) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    widen_e4m3(lds32(w0 + ((2 * h + i) << 4 ^ sw)), m[i][0], m[i][2]);
-                    widen_e4m3(lds32(w1 + ((2 * h + i) << 4 ^ sw)), m[i][1], m[i][3]);
-                }
-            } else {
-                uint32_t p[4], q[4];
-                widen_e2m1(lds32(w0 + (h << 4 ^ sw)), p);
-                widen_e2m1(lds32(w1 + (h << 4 ^ sw)), q);
-                m[0][0] = p[0], m[0][1] = q[0], m[0][2] = p[1], m[0][3] = q[1];
-                m[1][0] = p[2], m[1][1] = q[2], m[1][2] = p[3], m[1][3] = q[3];
-            }
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                mma16<kBf16>(c[h], m[i], b[4 * h + 2 * i], b[4 * h + 2 * i + 1]);
-                if (TAIL) mma16<kBf16>(cl[h], m[i], bl[4 * h + 2 * i], bl[4 * h + 2 * i + 1]);
-            }
-        }
-        uint64_t s[2][2];          // [half][rows g, rows g + 8]
-        if (DT == MOE_DTYPE_FP8_E4M3_BLOCK128) {
-            const float s0 = __uint_as_float(lds32(sc + slice / 2 * 4));
-            const float s1 = DOWN ? s0 : __uint_as_float(lds32(sc + slice / 2 * 4 + 32));
-            s[0][0] = pack2(s0, s0);
-            s[0][1] = pack2(s1, s1);
-        } else if (DT == MOE_DTYPE_MXFP4_BLOCK32) {
-            const uint32_t sr = sc + (mt * 16 + g) * 32 + slice * 2;
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                float lo, hi;
-                e8m0x2(lds16(sr + r * 256), lo, hi);
-                s[0][r] = pack2(lo, lo);
-                s[1][r] = pack2(hi, hi);
-            }
-        }
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            uint64_t v0 = pack2(c[0][2 * r], c[0][2 * r + 1]), v1 = pack2(c[1][2 * r], c[1][2 * r + 1]);
+            const uint4 p = lds128(w + ((2 * t + h) << 4 ^ sw)), q = lds128(w + PB * 1024 + ((2 * t + h) << 4 ^ sw));
+            const uint32_t m0[4] = {p.x, q.x, p.y, q.y}, m1[4] = {p.z, q.z, p.w, q.w};
+            float(&c)[4] = sum.run[nt][h];
+            mma16<true>(c, m0, b[4 * h], b[4 * h + 1], c);
+            mma16<true>(c, m1, b[4 * h + 2], b[4 * h + 3], c);
             if (TAIL) {
-                v0 = add2(v0, pack2(cl[0][2 * r], cl[0][2 * r + 1]));
-                v1 = add2(v1, pack2(cl[1][2 * r], cl[1][2 * r + 1]));
+                mma16<true>(c, m0, bl[4 * h], bl[4 * h + 1], c);
+                mma16<true>(c, m1, bl[4 * h + 2], bl[4 * h + 3], c);
             }
-            uint64_t v;
-            if (kBf16)
-                v = add2(v0, v1);
-            else if (DT == MOE_DTYPE_FP8_E4M3_BLOCK128)
-                v = mul2(mul2(add2(v0, v1), s[0][r]), back);
-            else
-                v = mul2(fma2(v0, s[0][r], mul2(v1, s[1][r])), back);
-            float x0, x1;
-            unpack2(v, x0, x1);
-            acc[mt][nt][2 * r] += !DOWN || col.own[nt][0] ? x0 : 0.0f;
-            acc[mt][nt][2 * r + 1] += !DOWN || col.own[nt][1] ? x1 : 0.0f;
+        }
+    } else {
+        float s0 = 0.0f, s1 = 0.0f;
+        if (DT == MOE_DTYPE_FP8_E4M3_BLOCK128) {
+            s0 = __uint_as_float(lds32(sc + slice / 2 * 4));
+            s1 = DOWN ? s0 : __uint_as_float(lds32(sc + slice / 2 * 4 + 32));
+        }
+        const float zero[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            const uint32_t w0 = w + (2 * mt) * PB * 1024, w1 = w0 + PB * 1024;
+            // products in independent chains: two halves of the slice, heads and tails
+            float c[2][4], cl[2][4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t m[2][4];
+                if (DT == MOE_DTYPE_FP8_E4M3_BLOCK128) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        widen_e4m3(lds32(w0 + ((2 * h + i) << 4 ^ sw)), m[i][0], m[i][2]);
+                        widen_e4m3(lds32(w1 + ((2 * h + i) << 4 ^ sw)), m[i][1], m[i][3]);
+                    }
+                } else {
+                    uint32_t p[4], q[4];
+                    widen_e2m1(lds32(w0 + (h << 4 ^ sw)), p);
+                    widen_e2m1(lds32(w1 + (h << 4 ^ sw)), q);
+                    m[0][0] = p[0], m[0][1] = q[0], m[0][2] = p[1], m[0][3] = q[1];
+                    m[1][0] = p[2], m[1][1] = q[2], m[1][2] = p[3], m[1][3] = q[3];
+                }
+                mma16<false>(c[h], m[0], b[4 * h], b[4 * h + 1], zero);
+                if (TAIL) mma16<false>(cl[h], m[0], bl[4 * h], bl[4 * h + 1], zero);
+                mma16<false>(c[h], m[1], b[4 * h + 2], b[4 * h + 3], c[h]);
+                if (TAIL) mma16<false>(cl[h], m[1], bl[4 * h + 2], bl[4 * h + 3], cl[h]);
+            }
+            float s[2][2] = {{s0, s1}, {s0, s1}};          // [half][rows g, rows g + 8]
+            if (DT == MOE_DTYPE_MXFP4_BLOCK32) {
+                const uint32_t sr = sc + (mt * 16 + g) * 32 + slice * 2;
+                e8m0x2(lds16(sr), s[0][0], s[1][0]);
+                e8m0x2(lds16(sr + 256), s[0][1], s[1][1]);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float v0 = TAIL ? c[0][j] + cl[0][j] : c[0][j], v1 = TAIL ? c[1][j] + cl[1][j] : c[1][j];
+                const float v = DT == MOE_DTYPE_FP8_E4M3_BLOCK128 ? (v0 + v1) * s[0][j >> 1]
+                                                                  : fmaf(v0, s[0][j >> 1], v1 * s[1][j >> 1]);
+                const float r = fmaf(v, back[j & 1], sum.acc[mt][nt][j]);
+                // an infinity or a NaN among the weights reaches the expert's own tokens only
+                if (!DOWN || col.own[nt][j & 1]) sum.acc[mt][nt][j] = r;
+            }
         }
     }
 }
 
 template <int DT, int NT, bool DOWN, bool FOLD>
 __device__ __forceinline__ void mma_stage(uint32_t stage, uint32_t sc, int slice, const Columns<NT>& col,
-                                          float (&acc)[Fmt<DT>::kRows / 16][NT][4]) {
+                                          Sums<DT, NT>& sum) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
-        if (NT == 1 || col.on[nt]) mma_tile<DT, NT, DOWN, FOLD>(stage, sc, slice, col, nt, acc);
+        if (NT == 1 || col.on[nt]) mma_tile<DT, NT, DOWN, FOLD>(stage, sc, slice, col, nt, sum);
 }
 
 // ------------------------------------------------------------------ the kernel
@@ -1172,18 +1185,10 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
             ring.slot = shared_stages % a.n_stages;
             ring.phase = (uint32_t)(shared_stages / a.n_stages) & 1u;
         }
-        float acc[MT][NT][4];
-        Columns<NT> col;
+        Sums<DT, NT> sum;
+        Columns<NT> col = {};
         bool both = false;       // warps 8-15 have joined
         int flip = 0;            // a stage of half the columns goes to one half of the warps, then to the other
-        auto clear = [&]() {
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int i = 0; i < NT; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) acc[m][i][j] = 0.0f;
-        };
         auto release = [&]() {
             __syncwarp();
             // before they join, warps 0-7 answer for warps 8-15 too
@@ -1193,8 +1198,11 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
         // one stage of kn columns; false when a wait was given up
         auto step = [&](auto down, int kn) {
             constexpr bool kDown = decltype(down)::value;
-            ok = wait(ring.w + 8 * ring.slot, ring.phase) && wait(ring.x + 8 * ring.slot, ring.phase);
-            if (!ok) return false;
+            const uint32_t bw = ring.w + 8 * ring.slot, bx = ring.x + 8 * ring.slot;
+            if (!__all_sync(0xffffffffu, bar_try(bw, ring.phase) && bar_try(bx, ring.phase))) {
+                ok = wait(bw, ring.phase) && wait(bx, ring.phase);
+                if (!ok) return false;
+            }
             const uint32_t st = ring.stage();
             if (both) {
                 int slice = warp;
@@ -1202,10 +1210,10 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
                     slice = (warp + flip) & 15;
                     flip ^= 8;
                 }
-                if (slice * kSlice < kn) mma_stage<DT, NT, kDown, FOLD>(st, st + ring.scales, slice, col, acc);
+                if (slice * kSlice < kn) mma_stage<DT, NT, kDown, FOLD>(st, st + ring.scales, slice, col, sum);
             } else {
                 for (int slice = kw; slice * kSlice < kn; slice += kWarps)
-                    mma_stage<DT, NT, kDown, FOLD>(st, st + ring.scales, slice, col, acc);
+                    mma_stage<DT, NT, kDown, FOLD>(st, st + ring.scales, slice, col, sum);
             }
             release();
             return true;
@@ -1221,7 +1229,8 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
                 for (int m = 0; m < MT; ++m)
 #pragma unroll
                     for (int i = 0; i < NT; ++i)
-                        red[kw][m][i][lane] = make_float4(acc[m][i][0], acc[m][i][1], acc[m][i][2], acc[m][i][3]);
+                        red[kw][m][i][lane] = make_float4(sum.acc[m][i][0], sum.acc[m][i][1], sum.acc[m][i][2],
+                                                          sum.acc[m][i][3]);
             };
             if (both) {
                 if (team) put();
@@ -1234,10 +1243,10 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
 #pragma unroll
                         for (int i = 0; i < NT; ++i) {
                             const float4 v = red[kw][m][i][lane];
-                            acc[m][i][0] += v.x;
-                            acc[m][i][1] += v.y;
-                            acc[m][i][2] += v.z;
-                            acc[m][i][3] += v.w;
+                            sum.acc[m][i][0] += v.x;
+                            sum.acc[m][i][1] += v.y;
+                            sum.acc[m][i][2] += v.z;
+                            sum.acc[m][i][3] += v.w;
                         }
                 }
                 put();
@@ -1260,7 +1269,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
             return s;
         };
         auto gate_up = [&](const Active& act, int f0) {
-            clear();
+            sum.clear();
             const int count = act.count, cols = chunk_cols(false, count);
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
@@ -1268,6 +1277,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
                 col.on[i] = count > 8 * i;
             }
             walk_unit(a, count, [&](int, int kn) { return step(std::false_type{}, kn); });
+            sum.fold(col, true);
             if (gather()) return false;
             if (tid < MT * NT * 32) {
                 const float4 s = reduced();
@@ -1305,8 +1315,9 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
             if (tid == 0) atomicAdd(bars + 1, 1);
             const int begin = P.cut2[cta], end = P.cut2[cta + 1];
             const int wsum = a.Is / 128 + (n_active_sh - first_routed) * (a.I / 128);
-            clear();
+            sum.clear();
             auto item = [&](int, const Active& act) {
+                sum.fold(col, false);   // the last expert's
                 const int cols = chunk_cols(true, act.count), xs = x_stride<DT>(cols);
                 col.tail = act.count * xs;
 #pragma unroll
@@ -1314,7 +1325,6 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
                     const int tok = FOLD ? g & 3 : 8 * i + g;
                     const bool has = act.mask >> tok & 1u;
                     const int row = __popc(act.mask & ((1u << tok) - 1u)) + (FOLD && g >= 4 ? act.count : 0);
-                    col.zero[i] = !has;
                     col.x[i] = off_x(cols) + (has ? row * xs : 0);
 #pragma unroll
                     for (int j = 0; j < 2; ++j)
@@ -1329,6 +1339,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
                 return true;
             };
             auto row_end = [&](int rb) {
+                sum.fold(col, false);
                 if (gather()) return false;
                 const int lo = rb * wsum, hi = lo + wsum;
                 const bool whole = begin <= lo && hi <= end;
@@ -1355,7 +1366,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
                         }
                     }
                 }
-                clear();
+                sum.clear();
                 if (whole) return true;
                 // a row block of several blocks: the last to leave its part
                 // adds them up in block order
