@@ -67,9 +67,8 @@ constexpr int kTeam = kWarps * 32, kConsumers = 2 * kTeam;
 constexpr int kThreads = kConsumers + 32 + kFeeders * 32;
 constexpr int kRouterVecs = 4;                   // 16-byte vectors of a router lane at a time
 constexpr int kMaxBlocks = 256;                  // blocks the join buffer has room for
-constexpr int kHeadStart = 2;                    // stages copied before the router's loads are in
-constexpr int kWindow = 2;                       // stages under way while the choice is made
-constexpr int kAhead = 24;                       // steps of 128 columns fetched into L2 across barrier 1
+constexpr int kHeadStart = 2;                    // stages copied before barrier 0 has been passed
+constexpr int kWindow = 2;                       // stages under way while a barrier or the choice is waited for
 // named barriers
 constexpr int kBarAll = 1, kBarB = 2, kBarRouted = 3, kBarA = 4, kBarLogits = 5;
 constexpr int kChunk = 1024;                     // K columns of a full stage
@@ -229,7 +228,7 @@ __device__ __noinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity, volati
     }
 }
 
-// Tensor copies of one box, with an L2 policy, or into L2 only.
+// Tensor copy of one box, with an L2 policy.
 __device__ __forceinline__ void box_load(uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1, int c2,
                                          int c3, int c4, uint64_t policy) {
     asm volatile(
@@ -238,13 +237,6 @@ __device__ __forceinline__ void box_load(uint32_t dst, const CUtensorMap* m, uin
         "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "l"(policy)
         : "memory");
 }
-__device__ __forceinline__ void box_fetch(const CUtensorMap* m, int c0, int c1, int c2, int c3, int c4) {
-    asm volatile("cp.async.bulk.prefetch.tensor.5d.L2.global.tile [%0, {%1, %2, %3, %4, %5}];" ::"l"(
-                     reinterpret_cast<uint64_t>(m)),
-                 "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
-                 : "memory");
-}
-
 // Asynchronous copies of 16 or 4 bytes by this thread, and its arrival on
 // `bar` once all of them have landed.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
@@ -643,11 +635,6 @@ struct Source {
     __device__ __forceinline__ int byte_of(int k) const { return F::kBits == 4 ? k / 2 : 0; }
     __device__ __forceinline__ int piece_of(int k) const { return F::kBits == 4 ? 0 : k * F::kBits / 1024; }
 
-    // Lane 0: the boxes of kn columns into L2.
-    __device__ __forceinline__ void fetch(int k0, int kn) const {
-        for (int k = k0; k < k0 + kn; k += kBox) box_fetch(map, byte_of(k), 0, piece_of(k), 0, group);
-    }
-
     // All lanes: one tensor copy for each 256 columns, and the scales.
     __device__ __forceinline__ void stage(const Ring& ring, int k0, int kn, uint64_t policy) const {
         const int lane = threadIdx.x & 31;
@@ -911,12 +898,15 @@ __device__ __forceinline__ void mma_stage(uint32_t stage, uint32_t sc, int slice
         if (NT == 1 || col.on[nt]) mma_tile<DT, NT, DOWN, FOLD>(stage, sc, slice, col, nt, sum);
 }
 
+// Warps that the reduction buffer has room for, with 512 bytes a tile: 32 KB at most.
+__host__ __device__ constexpr int red_warps(int tiles) { return tiles <= 4 ? 2 * kWarps : kWarps; }
+
 // ------------------------------------------------------------------ the kernel
 // NT: tiles of 8 tokens.  FOLD: at most four tokens.
 template <int DT, int NT, bool FOLD>
 __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant__ FewArgs a) {
     using F = Fmt<DT>;
-    constexpr int R = F::kRows, MT = R / 16, NF = R / 2;
+    constexpr int R = F::kRows, MT = R / 16, NF = R / 2, kRedWarps = red_warps(MT * NT);
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ uint64_t bar_w[kMaxStages], bar_x[kMaxStages], bar_empty[kMaxStages], plan_ready;
     __shared__ int n_active_sh, abort_sh, last_sh;
@@ -963,7 +953,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
         int nth = 0;
         bool window = true;
         auto stage = [&](int k0, int kn) {
-            if (nth++ == kHeadStart) bar_sync(kBarRouted, kConsumers + 32);
+            if (nth++ == kHeadStart) bar_sync(kBarRouted, kTeam + 32);
             if (!wait(ring.empty + 8 * ring.slot, ring.phase ^ 1)) return false;
             if (window) {
                 // more copies under way than HBM's latency needs would only
@@ -984,7 +974,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
             ok = walk_unit(a, a.T, stage);
         }
         if (ok && nth <= kHeadStart) {   // not met yet
-            bar_sync(kBarRouted, kConsumers + 32);
+            bar_sync(kBarRouted, kTeam + 32);
             nth = kHeadStart + 1;
         }
         ok = ok && wait(plan_bar, 0);
@@ -995,34 +985,20 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
                 src.unit(a, false, act.expert, (u % upe) * NF);
                 ok = walk_unit(a, act.count, stage);
             }
-            // Phase 2.  Until barrier 1 opens the ring fills and no further;
-            // meanwhile the next boxes go into L2.
-            auto item = [&](int rb, const Active& act) {
-                src.unit(a, true, act.expert, rb * R);
-                return true;
-            };
-            auto pass = [](int) { return true; };
-            const int begin = P.cut2[cta], end = P.cut2[cta + 1];
-            int left = a.n_stages, at = begin;
-            auto stage2 = [&](int k0, int kn) {
-                if (left-- == 0) {
-                    int open = 1;
-                    if (lane == 0) open = *reinterpret_cast<volatile int*>(bars + 1) >= G;
-                    if (!__shfl_sync(0xffffffffu, open, 0)) {
-                        const Source<DT> keep = src;
-                        walk_down(a, P, n_active_sh, at, min(end, at + kAhead), item,
-                                  [&](int f0, int fn) {
-                                      if (lane == 0) src.fetch(f0, fn);
-                                      return true;
-                                  },
-                                  pass);
-                        src = keep;
-                    }
-                }
-                at += kn / 128;
-                return stage(k0, kn);
-            };
-            ok = ok && walk_down(a, P, n_active_sh, begin, end, item, stage2, pass);
+            // Phase 2 does not wait for barrier 1; until the ring is full its
+            // copies leave HBM to the others' last ones and to the barrier.
+            window = true;
+            int left = a.n_stages;
+            ok = ok && walk_down(a, P, n_active_sh, P.cut2[cta], P.cut2[cta + 1],
+                                 [&](int rb, const Active& act) {
+                                     src.unit(a, true, act.expert, rb * R);
+                                     return true;
+                                 },
+                                 [&](int k0, int kn) {
+                                     window = left-- > 0;
+                                     return stage(k0, kn);
+                                 },
+                                 [](int) { return true; });
         }
         // no copy may still be in flight when the block leaves
         if (!ok)
@@ -1113,15 +1089,14 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
         const int tid = threadIdx.x, g = lane >> 2, t = lane & 3;
         const int team = warp / kWarps, kw = warp % kWarps;
         bool ok = true, good = true;
+        Scratch S;
         router_phase(a, team, kw, part[team]);
         __threadfence();
-        bar_arrive(kBarRouted, kConsumers + 32);
         if (team == 0) {
             bar_arrive(kBarLogits, kConsumers);
         } else {
             // ------------------------------------------------------ choice and plan
             const int rid = tid - kTeam;
-            Scratch S;
             S.keys = reinterpret_cast<unsigned long long*>(smem + a.off_scratch);
             S.scores = reinterpret_cast<double*>(S.keys + (size_t)a.batch * a.E);
             S.sels = S.scores + (size_t)a.batch * a.E;
@@ -1150,6 +1125,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
                 __threadfence();
             }
             good = !group_any(kBarB, !ok);
+            bar_arrive(kBarRouted, kTeam + 32);
             if (good) {
                 // batch * E is at most 4 kTeam; the next batch's logits are
                 // fetched while this one's experts are chosen
@@ -1179,7 +1155,6 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
                 build_plan<DT>(a, P, S, rid);
                 group_any(kBarB, false);
                 if (rid == 0) moe::mbar_arrive(&plan_ready);
-                pair_weights(a, P, S, rid);
             }
             // the shared expert's stages are the first team's
             ring.slot = shared_stages % a.n_stages;
@@ -1218,48 +1193,58 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
             release();
             return true;
         };
-        // Leaves the warps' sums in red (once the last ones have been read),
-        // the second team's added to the first's, and waits for all of them;
-        // true when any warp has given up.
+        // Leaves the warps' sums in red (once the last ones have been read)
+        // and waits for all of them; true when any warp has given up.  Where
+        // the buffer has no room for all 16, warps 8-15 are added to the others.
         auto gather = [&]() {
             const int bar = both ? kBarAll : kBarA;
             group_any(bar, false);
-            auto put = [&]() {
+            auto put = [&](int w) {
 #pragma unroll
                 for (int m = 0; m < MT; ++m)
 #pragma unroll
                     for (int i = 0; i < NT; ++i)
-                        red[kw][m][i][lane] = make_float4(sum.acc[m][i][0], sum.acc[m][i][1], sum.acc[m][i][2],
-                                                          sum.acc[m][i][3]);
+                        red[w][m][i][lane] = make_float4(sum.acc[m][i][0], sum.acc[m][i][1], sum.acc[m][i][2],
+                                                         sum.acc[m][i][3]);
             };
-            if (both) {
-                if (team) put();
-                group_any(bar, false);
-            }
-            if (!team) {
+            if (kRedWarps == 2 * kWarps) {
+                put(warp);
+            } else {
                 if (both) {
-#pragma unroll
-                    for (int m = 0; m < MT; ++m)
-#pragma unroll
-                        for (int i = 0; i < NT; ++i) {
-                            const float4 v = red[kw][m][i][lane];
-                            sum.acc[m][i][0] += v.x;
-                            sum.acc[m][i][1] += v.y;
-                            sum.acc[m][i][2] += v.z;
-                            sum.acc[m][i][3] += v.w;
-                        }
+                    if (team) put(kw);
+                    group_any(bar, false);
                 }
-                put();
+                if (!team) {
+                    if (both) {
+#pragma unroll
+                        for (int m = 0; m < MT; ++m)
+#pragma unroll
+                            for (int i = 0; i < NT; ++i) {
+                                const float4 v = red[kw][m][i][lane];
+                                sum.acc[m][i][0] += v.x;
+                                sum.acc[m][i][1] += v.y;
+                                sum.acc[m][i][2] += v.z;
+                                sum.acc[m][i][3] += v.w;
+                            }
+                    }
+                    put(kw);
+                }
             }
             return group_any(bar, !ok);
         };
-        // Sum over the K slices, in their order: thread tid takes row tile
-        // tid / (32 NT), column tile (tid / 32) % NT.
-        auto reduced = [&]() {
-            const int m = tid / (32 * NT), i = tid / 32 % NT;
+        // The sums are joined over the K slices, in their order, by MT * NT
+        // warps, one for each row tile and column tile; they take turns.
+        int shift = 0;
+        auto reader = [&]() {          // 0 .. MT * NT - 1 for the warps whose turn it is
+            const int n = both ? 2 * kWarps : kWarps, r = (warp + n - shift) % n;
+            shift = (shift + MT * NT) % n;
+            return r;
+        };
+        auto reduced = [&](int r) {
+            const int m = r / NT, i = r % NT, n = kRedWarps == 2 * kWarps && both ? 2 * kWarps : kWarps;
             float4 s = red[0][m][i][lane];
-#pragma unroll
-            for (int q = 1; q < kWarps; ++q) {
+#pragma unroll 7
+            for (int q = 1; q < n; ++q) {
                 const float4 v = red[q][m][i][lane];
                 s.x += v.x;
                 s.y += v.y;
@@ -1279,9 +1264,9 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
             walk_unit(a, count, [&](int, int kn) { return step(std::false_type{}, kn); });
             sum.fold(col, true);
             if (gather()) return false;
-            if (tid < MT * NT * 32) {
-                const float4 s = reduced();
-                const int f = f0 + tid / (32 * NT) * 8 + g, c0 = tid / 32 % NT * 8 + 2 * t;
+            if (const int r = reader(); r < MT * NT) {
+                const float4 s = reduced(r);
+                const int f = f0 + r / NT * 8 + g, c0 = r % NT * 8 + 2 * t;
                 const float gate[2] = {s.x, s.y}, up[2] = {s.z, s.w};
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
@@ -1305,6 +1290,8 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
         if (good) ok = wait(plan_bar, 0);
         good = !group_any(kBarAll, !(good && ok));
         both = true;
+        shift = 0;
+        if (good && team) pair_weights(a, P, S, tid - kTeam);   // read behind gather's barriers
         if (good)
             for (int u = P.cut1[cta]; good && u < P.cut1[cta + 1]; ++u)
                 good = gate_up(P.active[first_routed + u / upe], (u % upe) * NF);
@@ -1344,15 +1331,15 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
                 const int lo = rb * wsum, hi = lo + wsum;
                 const bool whole = begin <= lo && hi <= end;
                 float* mine = a.join + ((size_t)cta * 2 + (begin >= lo ? 0 : 1)) * a.T * R;
-                if (tid < MT * NT * 32) {
-                    float4 s = reduced();
+                if (const int rd = reader(); rd < MT * NT) {
+                    float4 s = reduced(rd);
                     if (FOLD) {   // columns 4-7 hold the tails' sums of columns 0-3
                         s.x += __shfl_down_sync(0xffffffffu, s.x, 2);
                         s.y += __shfl_down_sync(0xffffffffu, s.y, 2);
                         s.z += __shfl_down_sync(0xffffffffu, s.z, 2);
                         s.w += __shfl_down_sync(0xffffffffu, s.w, 2);
                     }
-                    const int r = tid / (32 * NT) * 16 + g, c0 = tid / 32 % NT * 8 + 2 * t;
+                    const int r = rd / NT * 16 + g, c0 = rd % NT * 8 + 2 * t;
                     const float v[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -1522,7 +1509,8 @@ moe_status_t few_smem(FewArgs& a, int limit, size_t* bytes) {
     a.batch = a.T < most ? a.T : most;
     off = up(off + a.batch * a.E * 16 + n * 12 + a.E * 8, 16);
     a.off_red = off;
-    off += kWarps * (F::kRows / 16) * NT * 512;
+    constexpr int tiles = F::kRows / 16 * NT;
+    off += red_warps(tiles) * tiles * 512;
     a.off_ring = up(off, 1024);
     // eight activation rows of a full stage; fewer columns leave room for more
     a.stage_bytes = up(kChunk / kBox * kBoxBytes + (a.T <= 4 ? 2 * a.T : 8) * (kChunk * 2 + F::kPad) + F::kScaleBytes, 1024);
