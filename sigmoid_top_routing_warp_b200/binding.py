@@ -199,7 +199,7 @@ def _ptr(t) -> int | None:
 
 def _stream(stream) -> int:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -409,19 +409,33 @@ def moe_backward(cfg, x, w_router, logits, topk_idx, topk_w, w13, w2, w13s, w2s,
 
 # The entry points below look their tensors over (type, size, dense layout,
 # current device) before they pass the pointers on: the C ABI sees none of it.
-def _want(where, name, t, dtype, numel, optional=False):
-    if t is None:
-        if optional:
-            return
-        raise ValueError("%s: %s is None" % (where, name))
+_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+
+
+def _complain(where, name, t, dtype, numel):
     if t.dtype is not dtype:
         raise TypeError("%s: %s must be %s, is %s" % (where, name, dtype, t.dtype))
     if t.numel() != numel:
         raise ValueError("%s: %s has %d elements, needs %d" % (where, name, t.numel(), numel))
     if not t.is_contiguous():
         raise ValueError("%s: %s must be dense and row-major" % (where, name))
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
-        raise ValueError("%s: %s must be on the current CUDA device" % (where, name))
+    raise ValueError("%s: %s must be on the current CUDA device" % (where, name))
+
+
+def _look(where, args):
+    """Pointers of `args`, each (name, tensor or None, dtype, elements); the C
+    ABI says which of them may be NULL."""
+    dev = torch.cuda.current_device() if torch.cuda.is_initialized() else -2
+    out = []
+    for name, t, dtype, numel in args:
+        if t is None:
+            out.append(None)
+            continue
+        if (t.dtype is not dtype or t.numel() != numel or not t.is_contiguous() or
+                t.get_device() != dev):
+            _complain(where, name, t, dtype, numel)
+        out.append(t.data_ptr())
+    return out
 
 
 def few_workspace_size(cfg: MoeConfig) -> int:
@@ -442,78 +456,54 @@ def moe_forward_few(cfg, x, w_router, bias, w13, w2, w13s, w2s, out, ws, topk_id
                     w2s_scale=None):
     """The whole layer for T <= MOE_FEW_MAX_T tokens in one launch; weights bf16,
     e4m3 (fp32 128x128 block scales) or MXFP4 (moe_quantize_mx)."""
-    c = cfg.c()
     T, H, E, k, I, Is = cfg.T, cfg.H, cfg.E, cfg.k, cfg.I, cfg.Is
-    f = "moe_forward_few"
-    mx = cfg.dtype == MOE_DTYPE_MXFP4_BLOCK32
-    bf = torch.bfloat16
-    wt = bf if cfg.dtype == MOE_DTYPE_BF16 else torch.uint8
-    pack = 2 if mx else 1
-    _want(f, "x", x, bf, T * H)
-    _want(f, "out", out, bf, T * H)
-    _want(f, "w_router", w_router, bf, E * H)
-    _want(f, "bias", bias, torch.float32, E)
-    _want(f, "topk_idx", topk_idx, torch.int32, T * k, True)
-    _want(f, "topk_w", topk_w, torch.float32, T * k, True)
-    _want(f, "w13", w13, wt, E * 2 * I * H // pack)
-    _want(f, "w2", w2, wt, E * H * I // pack)
-    if Is:
-        _want(f, "w13s", w13s, wt, 2 * Is * H // pack)
-        _want(f, "w2s", w2s, wt, H * Is // pack)
-    if cfg.dtype != MOE_DTYPE_BF16:
-        st, block = (torch.uint8, 32) if mx else (torch.float32, 128 * 128)
-        _want(f, "w13_scale", w13_scale, st, E * 2 * I * H // block)
-        _want(f, "w2_scale", w2_scale, st, E * H * I // block)
-        if Is:
-            _want(f, "w13s_scale", w13s_scale, st, 2 * Is * H // block)
-            _want(f, "w2s_scale", w2s_scale, st, H * Is // block)
-    _check(_lib.moe_forward_few(ctypes.byref(c), _ptr(x), _ptr(w_router), _ptr(bias), _ptr(w13),
-                                _ptr(w13_scale), _ptr(w2), _ptr(w2_scale), _ptr(w13s),
-                                _ptr(w13s_scale), _ptr(w2s), _ptr(w2s_scale), _ptr(out),
-                                _ptr(topk_idx), _ptr(topk_w), _ptr(ws), ws.numel(),
-                                _stream(stream)), f)
+    wt = _BF16 if cfg.dtype == MOE_DTYPE_BF16 else _U8
+    pack = 2 if cfg.dtype == MOE_DTYPE_MXFP4_BLOCK32 else 1
+    st, block = (_U8, 32) if pack == 2 else (_F32, 128 * 128)
+    n13, n2, n13s, n2s = E * 2 * I * H, E * H * I, 2 * Is * H, H * Is
+    p = _look("moe_forward_few", (
+        ("x", x, _BF16, T * H), ("w_router", w_router, _BF16, E * H), ("bias", bias, _F32, E),
+        ("w13", w13, wt, n13 // pack), ("w13_scale", w13_scale, st, n13 // block),
+        ("w2", w2, wt, n2 // pack), ("w2_scale", w2_scale, st, n2 // block),
+        ("w13s", w13s, wt, n13s // pack), ("w13s_scale", w13s_scale, st, n13s // block),
+        ("w2s", w2s, wt, n2s // pack), ("w2s_scale", w2s_scale, st, n2s // block),
+        ("out", out, _BF16, T * H), ("topk_idx", topk_idx, _I32, T * k),
+        ("topk_w", topk_w, _F32, T * k), ("workspace", ws, _U8, ws.numel())))
+    _check(_lib.moe_forward_few(ctypes.byref(cfg.c()), *p, ws.numel(), _stream(stream)),
+           "moe_forward_few")
 
 
 def moe_quantize_mx(x, q, scale, stream=None):
     """bf16 x [rows, cols] -> MXFP4: codes q uint8 [rows, cols/2] and e8m0 scale
     bytes uint8 [rows, cols/32]."""
     rows, cols = x.shape
-    _want("moe_quantize_mx", "x", x, torch.bfloat16, rows * cols)
-    _want("moe_quantize_mx", "q", q, torch.uint8, rows * cols // 2)
-    _want("moe_quantize_mx", "scale", scale, torch.uint8, rows * cols // 32)
-    _check(_lib.moe_quantize_mx(_ptr(x), rows, cols, _ptr(q), _ptr(scale), _stream(stream)),
-           "moe_quantize_mx")
+    n = rows * cols
+    px, pq, ps = _look("moe_quantize_mx", (("x", x, _BF16, n), ("q", q, _U8, n // 2),
+                                           ("scale", scale, _U8, n // 32)))
+    _check(_lib.moe_quantize_mx(px, rows, cols, pq, ps, _stream(stream)), "moe_quantize_mx")
 
 
 def moe_dequantize_mx(q, scale, x, stream=None):
     """MXFP4 codes and scales -> the bf16 values they stand for, x [rows, cols]."""
     rows, cols = x.shape
-    _want("moe_dequantize_mx", "x", x, torch.bfloat16, rows * cols)
-    _want("moe_dequantize_mx", "q", q, torch.uint8, rows * cols // 2)
-    _want("moe_dequantize_mx", "scale", scale, torch.uint8, rows * cols // 32)
-    _check(_lib.moe_dequantize_mx(_ptr(q), _ptr(scale), rows, cols, _ptr(x), _stream(stream)),
-           "moe_dequantize_mx")
-
-
-def _gate_numel(cfg, gate_mode):
-    return cfg.T * cfg.H if gate_mode == MOE_GATE_TOKEN else cfg.H
+    n = rows * cols
+    px, pq, ps = _look("moe_dequantize_mx", (("x", x, _BF16, n), ("q", q, _U8, n // 2),
+                                             ("scale", scale, _U8, n // 32)))
+    _check(_lib.moe_dequantize_mx(pq, ps, rows, cols, px, _stream(stream)), "moe_dequantize_mx")
 
 
 def moe_norm_residual(cfg, h, y, gamma_post, h_out, eps, gate=None, gate_mode=MOE_GATE_NONE,
                       res_scale=1.0, gamma_pre=None, u=None, rstd=None, stream=None):
     """h_out = res_scale * h + gate * norm(y); u = norm(h_out) (with gamma_pre)."""
-    c = cfg.c()
-    f, bf, n = "moe_norm_residual", torch.bfloat16, cfg.T * cfg.H
-    for name, t in (("h", h), ("y", y), ("h_out", h_out)):
-        _want(f, name, t, bf, n)
-    _want(f, "u", u, bf, n, True)
-    _want(f, "gamma_post", gamma_post, bf, cfg.H)
-    _want(f, "gamma_pre", gamma_pre, bf, cfg.H, True)
-    _want(f, "gate", gate, bf, _gate_numel(cfg, gate_mode), True)
-    _want(f, "rstd", rstd, torch.float32, 2 * cfg.T, True)
-    _check(_lib.moe_norm_residual(ctypes.byref(c), _ptr(h), _ptr(y), _ptr(gamma_post), _ptr(gate),
-                                  int(gate_mode), float(res_scale), float(eps), _ptr(gamma_pre),
-                                  _ptr(h_out), _ptr(u), _ptr(rstd), _stream(stream)), f)
+    T, H = cfg.T, cfg.H
+    n = T * H
+    p = _look("moe_norm_residual", (
+        ("h", h, _BF16, n), ("y", y, _BF16, n), ("gamma_post", gamma_post, _BF16, H),
+        ("gate", gate, _BF16, n if gate_mode == MOE_GATE_TOKEN else H),
+        ("gamma_pre", gamma_pre, _BF16, H), ("h_out", h_out, _BF16, n), ("u", u, _BF16, n),
+        ("rstd", rstd, _F32, 2 * T)))
+    _check(_lib.moe_norm_residual(ctypes.byref(cfg.c()), *p[:4], gate_mode, res_scale, eps, *p[4:],
+                                  _stream(stream)), "moe_norm_residual")
 
 
 def norm_residual_workspace_size(cfg: MoeConfig) -> int:
@@ -533,23 +523,20 @@ def moe_norm_residual_backward(cfg, h, y, gamma_post, rstd, dh_out, dh, dy, dgam
                                du=None, dgamma_pre=None, dgate=None, stream=None):
     """Gradients of moe_norm_residual: dh, dy (bf16), dgamma_post, dgamma_pre (fp32)
     and dgate (fp32 [H] for a gate per channel, bf16 [T, H] for one per token)."""
-    c = cfg.c()
-    f, bf, f32, n = "moe_norm_residual_backward", torch.bfloat16, torch.float32, cfg.T * cfg.H
-    for name, t in (("h", h), ("y", y), ("dh_out", dh_out), ("dh", dh), ("dy", dy)):
-        _want(f, name, t, bf, n)
-    _want(f, "du", du, bf, n, True)
-    _want(f, "rstd", rstd, f32, 2 * cfg.T)
-    _want(f, "gamma_post", gamma_post, bf, cfg.H)
-    _want(f, "gamma_pre", gamma_pre, bf, cfg.H, True)
-    _want(f, "dgamma_post", dgamma_post, f32, cfg.H)
-    _want(f, "dgamma_pre", dgamma_pre, f32, cfg.H, True)
-    _want(f, "gate", gate, bf, _gate_numel(cfg, gate_mode), True)
-    _want(f, "dgate", dgate, bf if gate_mode == MOE_GATE_TOKEN else f32,
-          _gate_numel(cfg, gate_mode), True)
-    _check(_lib.moe_norm_residual_backward(
-        ctypes.byref(c), _ptr(h), _ptr(y), _ptr(gamma_post), _ptr(gate), int(gate_mode),
-        float(res_scale), _ptr(gamma_pre), _ptr(rstd), _ptr(dh_out), _ptr(du), _ptr(dh), _ptr(dy),
-        _ptr(dgate), _ptr(dgamma_post), _ptr(dgamma_pre), _ptr(ws), ws.numel(), _stream(stream)), f)
+    T, H = cfg.T, cfg.H
+    n = T * H
+    ng = n if gate_mode == MOE_GATE_TOKEN else H
+    p = _look("moe_norm_residual_backward", (
+        ("h", h, _BF16, n), ("y", y, _BF16, n), ("gamma_post", gamma_post, _BF16, H),
+        ("gate", gate, _BF16, ng), ("gamma_pre", gamma_pre, _BF16, H), ("rstd", rstd, _F32, 2 * T),
+        ("dh_out", dh_out, _BF16, n), ("du", du, _BF16, n), ("dh", dh, _BF16, n),
+        ("dy", dy, _BF16, n),
+        ("dgate", dgate, _BF16 if gate_mode == MOE_GATE_TOKEN else _F32, ng),
+        ("dgamma_post", dgamma_post, _F32, H), ("dgamma_pre", dgamma_pre, _F32, H),
+        ("workspace", ws, _U8, ws.numel())))
+    _check(_lib.moe_norm_residual_backward(ctypes.byref(cfg.c()), *p[:4], gate_mode, res_scale,
+                                           *p[4:], ws.numel(), _stream(stream)),
+           "moe_norm_residual_backward")
 
 
 def moe_check_device_status(ws, stream=None):

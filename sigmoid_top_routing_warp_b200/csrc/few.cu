@@ -67,6 +67,7 @@ constexpr int kTeam = kWarps * 32, kConsumers = 2 * kTeam;
 constexpr int kThreads = kConsumers + 32 + kFeeders * 32;
 constexpr int kRouterVecs = 4;                   // 16-byte vectors of a router lane at a time
 constexpr int kMaxBlocks = 256;                  // blocks the join buffer has room for
+constexpr int kStaticSmem = 3072;                // the kernel's own variables (a launch with less left over fails)
 constexpr int kHeadStart = 2;                    // stages copied before barrier 0 has been passed
 constexpr int kWindow = 2;                       // stages under way while a barrier or the choice is waited for
 // named barriers
@@ -1530,11 +1531,9 @@ moe_status_t launch_few(FewArgs& a, cudaStream_t s) {
     FEW_TRY(moe::api_sm_count(&sms));
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
-    cudaFuncAttributes fa;
-    if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, kernel);
     if (e == cudaSuccess) {
         size_t smem = 0;
-        FEW_TRY((few_smem<DT, NT>(a, optin - (int)fa.sharedSizeBytes, &smem)));
+        FEW_TRY((few_smem<DT, NT>(a, optin - kStaticSmem, &smem)));
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e == cudaSuccess) {
             void* args[] = {&a};
