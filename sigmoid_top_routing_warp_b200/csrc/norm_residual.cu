@@ -35,6 +35,7 @@ moe_status_t api_sm_count(int* n);
 namespace {
 
 constexpr int kNrMaxH = 16384;
+constexpr int kNrWideThreads = 512;
 constexpr int kNrBwdBlocks = 148;   // row walkers of the backward pass, one partial sum each
 
 struct NrArgs {
@@ -49,7 +50,7 @@ struct NrArgs {
     uint16_t *dh, *dy;
     void* dgate;                       // fp32 [H] (channel) or bf16 [T, H] (token)
     float *dgamma_post, *dgamma_pre;
-    float* part;                       // [blocks][3][H]
+    float* part;                       // [blocks][2][H]
     int blocks;
 };
 
@@ -101,122 +102,285 @@ __device__ __forceinline__ float inv_norm(float ss, int H, float eps) {
     return __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(ss, (float)H), eps)));
 }
 
-// One block per row; a thread keeps NV 8-value vectors of the row in registers.
-template <int NV>
-__global__ void __launch_bounds__(1024) norm_residual_kernel(const NrArgs p) {
-    __shared__ float sh[2][32];
-    const int nvec = p.H / 8;
-    const size_t t = blockIdx.x;
-    uint4 yr[NV], hr[NV];
-    float ss[1] = {0.0f};
+// 16 bytes from global to this thread's own place in shared memory.  Only the
+// thread that issued a copy reads it back, behind copies_left: no barrier.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool ok) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_close() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// waits until at most N of the closed groups are still under way
+template <int N>
+__device__ __forceinline__ void copies_left() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t p) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(p));
+    return v;
+}
+
+// Two binary32 operations in one instruction (the same bits as two).
+struct F2 {
+    uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float x, float y) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ void split(F2 a, float& x, float& y) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a.v));
+}
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ F2 widen(uint32_t w) { return f2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)); }
+__device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+__device__ __forceinline__ uint32_t narrow(F2 a) {
+    float x, y;
+    split(a, x, y);
+    const __nv_bfloat162 b = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&b);
+}
+__device__ __forceinline__ float total(F2 a) {
+    float x, y;
+    split(a, x, y);
+    return x + y;
+}
+
+constexpr int kNrStages = 3;       // rows in a block's shared memory: one worked on, the others on their way
+
+// Blocks walk rows blockIdx.x, blockIdx.x + gridDim.x, ...; a thread keeps NV
+// 8-value vectors of the row, ST rows of them in shared memory.
+template <int NV, int ST, int THREADS, bool TOKEN>
+__global__ void __launch_bounds__(THREADS, 1280 / THREADS) norm_residual_kernel(const NrArgs p) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ float sh[2][2][32];
+    constexpr int NT = TOKEN ? 3 : 2;                 // tensors of a row: y, h, gate
+    const int nvec = p.H / 8, nthr = blockDim.x;
+    const uint32_t mine = (uint32_t)__cvta_generic_to_shared(smem) + threadIdx.x * 16;
+    auto place = [&](int st, int k, int i) { return mine + ((st * NT + k) * NV + i) * nthr * 16; };
+    auto fetch = [&](size_t t, int st) {
+        if (t < (size_t)p.T) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = threadIdx.x + i * blockDim.x;
-        yr[i] = c < nvec ? vec(p.y, t, p.H)[c] : make_uint4(0, 0, 0, 0);
-        hr[i] = c < nvec ? vec(p.h, t, p.H)[c] : make_uint4(0, 0, 0, 0);
-    }
+            for (int i = 0; i < NV; ++i) {
+                const int c = threadIdx.x + i * nthr;
+                const bool ok = c < nvec;
+                const int cc = ok ? c : 0;
+                copy16(place(st, 0, i), vec(p.y, t, p.H) + cc, ok);
+                copy16(place(st, 1, i), vec(p.h, t, p.H) + cc, ok);
+                if (TOKEN) copy16(place(st, 2, i), vec(p.gate, t, p.H) + cc, ok);
+            }
+        }
+        copies_close();
+    };
+    size_t t = blockIdx.x;
+    const size_t step = gridDim.x;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        float f[8];
-        unpack8(yr[i], f);
+    for (int d = 0; d < ST - 1; ++d) fetch(t + d * step, d);
+    const F2 a2 = f2(p.a, p.a);
+    int st = 0, half = 0;
+    for (; t < (size_t)p.T; t += step, half ^= 1) {
+        copies_left<ST - 2>();
+        uint4 yr[NV], hr[NV], gr[NV];
+        F2 ss = f2(0.0f, 0.0f);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) ss[0] = fmaf(f[j], f[j], ss[0]);
-    }
-    block_sum(ss, sh[0]);
-    const float rp = inv_norm(ss[0], p.H, p.eps);
-    float h2[NV][8];
-    float s2[1] = {0.0f};
+        for (int i = 0; i < NV; ++i) {
+            yr[i] = lds128(place(st, 0, i));
+            hr[i] = lds128(place(st, 1, i));
+            if (TOKEN) gr[i] = lds128(place(st, 2, i));
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = threadIdx.x + i * blockDim.x;
-        if (c >= nvec) {
+            for (int j = 0; j < 4; ++j) {
+                const F2 y = widen(word(yr[i], j));
+                ss = fma2(y, y, ss);
+            }
+        }
+        fetch(t + (ST - 1) * step, st == 0 ? ST - 1 : st - 1);   // the row before this one has left its place
+        st = st == ST - 1 ? 0 : st + 1;
+        float s1[1] = {total(ss)};
+        block_sum(s1, sh[half][0]);
+        const float rp = inv_norm(s1[0], p.H, p.eps);
+        const F2 rp2 = f2(rp, rp);
+        F2 h2[NV][4], s2 = f2(0.0f, 0.0f);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) h2[i][j] = 0.0f;
+        for (int i = 0; i < NV; ++i) {
+            const int c = threadIdx.x + i * nthr;
+            const bool ok = c < nvec;
+            const uint4 zero = make_uint4(0, 0, 0, 0);
+            const uint4 w = ok ? __ldg(vec(p.gamma_post, 0, p.H) + c) : zero;
+            if (!TOKEN) gr[i] = ok && p.gate ? __ldg(vec(p.gate, 0, p.H) + c)
+                                             : make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
+            uint32_t o[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const F2 n = widen(word(w, j)) * (widen(word(yr[i], j)) * rp2);
+                h2[i][j] = fma2(widen(word(gr[i], j)), n, a2 * widen(word(hr[i], j)));
+                s2 = fma2(h2[i][j], h2[i][j], s2);
+                o[j] = narrow(h2[i][j]);
+            }
+            if (ok) reinterpret_cast<uint4*>(p.h_out + t * p.H)[c] = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+        if (p.u == nullptr) {
+            if (threadIdx.x == 0 && p.rstd) p.rstd[t] = rp;
             continue;
         }
-        float y[8], h[8], g[8], w[8];
-        unpack8(yr[i], y);
-        unpack8(hr[i], h);
-        unpack8(__ldg(vec(p.gamma_post, 0, p.H) + c), w);
-        if (p.gate_mode == MOE_GATE_NONE) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) g[j] = 1.0f;
-        } else {
-            unpack8(__ldg(vec(p.gate, p.gate_mode == MOE_GATE_TOKEN ? t : 0, p.H) + c), g);
+        float s3[1] = {total(s2)};
+        block_sum(s3, sh[half][1]);
+        const float rq = inv_norm(s3[0], p.H, p.eps);
+        if (threadIdx.x == 0 && p.rstd) {
+            p.rstd[t] = rp;
+            p.rstd[p.T + t] = rq;
         }
+        const F2 rq2 = f2(rq, rq);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            h2[i][j] = fmaf(g[j], w[j] * (y[j] * rp), p.a * h[j]);
-            s2[0] = fmaf(h2[i][j], h2[i][j], s2[0]);
+        for (int i = 0; i < NV; ++i) {
+            const int c = threadIdx.x + i * nthr;
+            if (c >= nvec) continue;
+            const uint4 w = __ldg(vec(p.gamma_pre, 0, p.H) + c);
+            uint32_t o[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[j] = narrow(widen(word(w, j)) * (h2[i][j] * rq2));
+            reinterpret_cast<uint4*>(p.u + t * p.H)[c] = make_uint4(o[0], o[1], o[2], o[3]);
         }
-        reinterpret_cast<uint4*>(p.h_out + t * p.H)[c] = pack8(h2[i]);
-    }
-    if (p.u == nullptr) {
-        if (threadIdx.x == 0 && p.rstd) p.rstd[t] = rp;
-        return;
-    }
-    block_sum(s2, sh[1]);
-    const float rq = inv_norm(s2[0], p.H, p.eps);
-    if (threadIdx.x == 0 && p.rstd) {
-        p.rstd[t] = rp;
-        p.rstd[p.T + t] = rq;
-    }
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = threadIdx.x + i * blockDim.x;
-        if (c >= nvec) continue;
-        float w[8], o[8];
-        unpack8(__ldg(vec(p.gamma_pre, 0, p.H) + c), w);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] = w[j] * (h2[i][j] * rq);
-        reinterpret_cast<uint4*>(p.u + t * p.H)[c] = pack8(o);
     }
 }
 
-// Persistent blocks walk rows blockIdx.x, blockIdx.x + blocks, ...; a thread
-// owns the same columns in every row, so the column sums stay in its
-// registers and leave as one partial per block.
-template <int NV>
-__global__ void __launch_bounds__(1024) norm_residual_bwd_kernel(const NrArgs p) {
+// Persistent blocks, one 8-value vector of the row per thread; a thread owns
+// the same columns in every row, so the column sums stay in its registers and
+// leave as one partial per block.  A gate per channel and no gate are constant
+// down a column, so sum(D yn) alone gives both dgamma_post (times g) and dgate
+// (times gamma_post); with a gate per token it is sum(D g yn).
+template <int THREADS, bool TOKEN>
+__global__ void __launch_bounds__(THREADS) norm_residual_bwd_kernel(const NrArgs p) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ float sh[2][3 * 32];
+    constexpr int NT = TOKEN ? 5 : 4;                 // tensors of a row: y, h, dh_out, du, gate
+    const int c = threadIdx.x, nthr = blockDim.x;
+    const bool ok = c < p.H / 8;
+    const int cc = ok ? c : 0;
+    const float inv_h = 1.0f / (float)p.H;
+    const uint32_t mine = (uint32_t)__cvta_generic_to_shared(smem) + c * 16;
+    auto place = [&](int st, int k) { return mine + (st * NT + k) * nthr * 16; };
+    auto fetch = [&](size_t t, int st) {
+        if (t < (size_t)p.T) {
+            copy16(place(st, 0), vec(p.y, t, p.H) + cc, ok);
+            copy16(place(st, 1), vec(p.h, t, p.H) + cc, ok);
+            copy16(place(st, 2), vec(p.dh_out, t, p.H) + cc, ok);
+            copy16(place(st, 3), p.du ? vec(p.du, t, p.H) + cc : vec(p.y, t, p.H) + cc, ok && p.du);
+            if (TOKEN) copy16(place(st, 4), vec(p.gate, t, p.H) + cc, ok);
+        }
+        copies_close();
+    };
+    size_t t = blockIdx.x;
+    const size_t step = gridDim.x;
+    fetch(t, 0);
+    fetch(t + step, 1);
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    const uint4 one = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
+    const uint4 w1 = ok ? __ldg(vec(p.gamma_post, 0, p.H) + c) : zero;
+    const uint4 w2 = ok && p.du ? __ldg(vec(p.gamma_pre, 0, p.H) + c) : zero;
+    const uint4 gc = ok && p.gate_mode == MOE_GATE_CHANNEL ? __ldg(vec(p.gate, 0, p.H) + c) : one;
+    const F2 a2 = f2(p.a, p.a);
+    F2 sp[4], sq[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sp[j] = sq[j] = f2(0.0f, 0.0f);
+    int st = 0, half = 0;
+    for (; t < (size_t)p.T; t += step) {
+        const float rp = __ldg(p.rstd_in + t), rq = p.du ? __ldg(p.rstd_in + p.T + t) : 0.0f;
+        const F2 rp2 = f2(rp, rp), rq2 = f2(rq, rq);
+        copies_left<1>();
+        const uint4 yr = lds128(place(st, 0)), hr = lds128(place(st, 1)), dr = lds128(place(st, 2)),
+                    ur = lds128(place(st, 3));
+        const uint4 gr = TOKEN ? lds128(place(st, 4)) : gc;
+        fetch(t + 2 * step, st == 0 ? kNrStages - 1 : st - 1);
+        st = st == kNrStages - 1 ? 0 : st + 1;
+        F2 yn[4], hn[4], dq[4];                       // dq: dh' + rq q
+        F2 x0 = f2(0.0f, 0.0f), x1 = x0, x2 = x0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            yn[j] = widen(word(yr, j)) * rp2;
+            const F2 w = widen(word(gr, j)) * (widen(word(w1, j)) * yn[j]);
+            hn[j] = fma2(a2, widen(word(hr, j)), w) * rq2;
+            const F2 u = widen(word(ur, j));
+            const F2 q = u * widen(word(w2, j));
+            dq[j] = fma2(rq2, q, widen(word(dr, j)));
+            x0 = fma2(q, hn[j], x0);
+            x1 = fma2(w, dq[j], x1);
+            x2 = fma2(w, hn[j], x2);
+            sq[j] = fma2(u, hn[j], sq[j]);
+        }
+        float s[3] = {total(x0), total(x1), total(x2)};
+        block_sum(s, sh[half]);
+        half ^= 1;
+        const float c1 = s[0] * inv_h, c2 = (s[1] - rq * c1 * s[2]) * inv_h;
+        const F2 k1 = f2(-rq * c1, -rq * c1), k2 = f2(-c2, -c2);
+        uint32_t odh[4], ody[4], odg[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const F2 wp = widen(word(w1, j)), g = widen(word(gr, j));
+            const F2 D = fma2(hn[j], k1, dq[j]);
+            const F2 Dg = D * g;
+            odh[j] = narrow(a2 * D);
+            ody[j] = narrow(rp2 * fma2(yn[j], k2, Dg * wp));
+            if (TOKEN) odg[j] = narrow(D * (wp * yn[j]));
+            sp[j] = fma2(TOKEN ? Dg : D, yn[j], sp[j]);
+        }
+        if (ok) {
+            reinterpret_cast<uint4*>(p.dh + t * p.H)[c] = make_uint4(odh[0], odh[1], odh[2], odh[3]);
+            reinterpret_cast<uint4*>(p.dy + t * p.H)[c] = make_uint4(ody[0], ody[1], ody[2], ody[3]);
+            if (TOKEN)
+                reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.dgate) + t * p.H)[c] =
+                    make_uint4(odg[0], odg[1], odg[2], odg[3]);
+        }
+    }
+    if (!ok) return;
+    float* base = p.part + (size_t)blockIdx.x * 2 * p.H + 8 * c;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        float x, y;
+        split(sp[j], x, y);
+        *reinterpret_cast<float2*>(base + 2 * j) = make_float2(x, y);
+        split(sq[j], x, y);
+        *reinterpret_cast<float2*>(base + p.H + 2 * j) = make_float2(x, y);
+    }
+}
+
+// Rows longer than the registers hold (above 5120 columns): two passes over a
+// row, the second one from L1 and L2, and the column sums in shared memory
+// [2][H], each thread at its own columns.
+__global__ void __launch_bounds__(kNrWideThreads) norm_residual_bwd_wide_kernel(const NrArgs p) {
+    extern __shared__ float col[];
     __shared__ float sh[2][3 * 32];
     const int nvec = p.H / 8;
     const float inv_h = 1.0f / (float)p.H;
-    float sgp[NV][8], sgq[NV][8], sg[NV][8];
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sgp[i][j] = sgq[i][j] = sg[i][j] = 0.0f;
-    int half = 0;
+    for (int i = threadIdx.x; i < 2 * p.H; i += blockDim.x) col[i] = 0.0f;
+    __syncthreads();
     const uint4 zero = make_uint4(0, 0, 0, 0);
     const uint4 one = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
+    int half = 0;
     for (size_t t = blockIdx.x; t < (size_t)p.T; t += gridDim.x) {
         const float rp = p.rstd_in[t], rq = p.du ? p.rstd_in[p.T + t] : 0.0f;
-        uint4 yr[NV], hr[NV], dr[NV], ur[NV], gr[NV];
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = threadIdx.x + i * blockDim.x;
-            const bool ok = c < nvec;
-            yr[i] = ok ? vec(p.y, t, p.H)[c] : zero;
-            hr[i] = ok ? vec(p.h, t, p.H)[c] : zero;
-            dr[i] = ok ? vec(p.dh_out, t, p.H)[c] : zero;
-            ur[i] = ok && p.du ? vec(p.du, t, p.H)[c] : zero;
-            gr[i] = one;
-            if (ok && p.gate_mode != MOE_GATE_NONE)
-                gr[i] = vec(p.gate, p.gate_mode == MOE_GATE_TOKEN ? t : 0, p.H)[c];
-        }
-        float s[3] = {0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = threadIdx.x + i * blockDim.x;
-            if (c >= nvec) continue;
-            float y[8], h[8], d[8], u[8], g[8], wp[8], wq[8];
-            unpack8(yr[i], y);
-            unpack8(hr[i], h);
-            unpack8(dr[i], d);
-            unpack8(ur[i], u);
-            unpack8(gr[i], g);
+        float y[8], h[8], d[8], u[8], g[8], wp[8], wq[8];
+        auto load = [&](int c) {
+            unpack8(vec(p.y, t, p.H)[c], y);
+            unpack8(vec(p.h, t, p.H)[c], h);
+            unpack8(vec(p.dh_out, t, p.H)[c], d);
+            unpack8(p.du ? vec(p.du, t, p.H)[c] : zero, u);
+            unpack8(p.gate_mode == MOE_GATE_NONE ? one : vec(p.gate, p.gate_mode == MOE_GATE_TOKEN ? t : 0, p.H)[c],
+                    g);
             unpack8(__ldg(vec(p.gamma_post, 0, p.H) + c), wp);
-            unpack8(p.gamma_pre ? __ldg(vec(p.gamma_pre, 0, p.H) + c) : zero, wq);
+            unpack8(p.du ? __ldg(vec(p.gamma_pre, 0, p.H) + c) : zero, wq);
+        };
+        float s[3] = {0.0f, 0.0f, 0.0f};
+        for (int c = threadIdx.x; c < nvec; c += blockDim.x) {
+            load(c);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const float w = g[j] * (wp[j] * (y[j] * rp));
@@ -231,18 +395,9 @@ __global__ void __launch_bounds__(1024) norm_residual_bwd_kernel(const NrArgs p)
         half ^= 1;
         const float c1 = s[0] * inv_h;
         const float c2 = (s[1] - rq * c1 * s[2]) * inv_h;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = threadIdx.x + i * blockDim.x;
-            if (c >= nvec) continue;
-            float y[8], h[8], d[8], u[8], g[8], wp[8], wq[8], odh[8], ody[8], odg[8];
-            unpack8(yr[i], y);
-            unpack8(hr[i], h);
-            unpack8(dr[i], d);
-            unpack8(ur[i], u);
-            unpack8(gr[i], g);
-            unpack8(__ldg(vec(p.gamma_post, 0, p.H) + c), wp);
-            unpack8(p.gamma_pre ? __ldg(vec(p.gamma_pre, 0, p.H) + c) : zero, wq);
+        for (int c = threadIdx.x; c < nvec; c += blockDim.x) {
+            float odh[8], ody[8], odg[8];
+            load(c);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const float yn = y[j] * rp;
@@ -252,9 +407,8 @@ __global__ void __launch_bounds__(1024) norm_residual_bwd_kernel(const NrArgs p)
                 odh[j] = p.a * D;
                 ody[j] = rp * fmaf(Dg, wp[j], -yn * c2);
                 odg[j] = D * (wp[j] * yn);
-                sgp[i][j] = fmaf(Dg, yn, sgp[i][j]);
-                sgq[i][j] = fmaf(u[j], hn, sgq[i][j]);
-                sg[i][j] += odg[j];
+                col[8 * c + j] += (p.gate_mode == MOE_GATE_TOKEN ? Dg : D) * yn;
+                col[p.H + 8 * c + j] += u[j] * hn;
             }
             reinterpret_cast<uint4*>(p.dh + t * p.H)[c] = pack8(odh);
             reinterpret_cast<uint4*>(p.dy + t * p.H)[c] = pack8(ody);
@@ -262,52 +416,34 @@ __global__ void __launch_bounds__(1024) norm_residual_bwd_kernel(const NrArgs p)
                 reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.dgate) + t * p.H)[c] = pack8(odg);
         }
     }
-    float* base = p.part + (size_t)blockIdx.x * 3 * p.H;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = threadIdx.x + i * blockDim.x;
-        if (c >= nvec) continue;
-#pragma unroll
-        for (int j = 0; j < 8; j += 4) {
-            *reinterpret_cast<float4*>(base + 8 * c + j) =
-                make_float4(sgp[i][j], sgp[i][j + 1], sgp[i][j + 2], sgp[i][j + 3]);
-            *reinterpret_cast<float4*>(base + p.H + 8 * c + j) =
-                make_float4(sgq[i][j], sgq[i][j + 1], sgq[i][j + 2], sgq[i][j + 3]);
-            *reinterpret_cast<float4*>(base + 2 * p.H + 8 * c + j) =
-                make_float4(sg[i][j], sg[i][j + 1], sg[i][j + 2], sg[i][j + 3]);
-        }
-    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < 2 * p.H; i += blockDim.x) p.part[(size_t)blockIdx.x * 2 * p.H + i] = col[i];
 }
 
-// Column sums of the per-block partials in block order, in binary64.
+// Column sums of the per-block partials in block order, in binary64:
+// blockIdx.y 0 gives dgamma_post and a channel gate's dgate, 1 dgamma_pre.
 __global__ void __launch_bounds__(256) norm_residual_cols_kernel(const NrArgs p) {
     __shared__ double sh[8][33];
     const int which = blockIdx.y;
-    float* out = which == 0 ? p.dgamma_post : which == 1 ? p.dgamma_pre : static_cast<float*>(p.dgate);
-    if (which == 2 && p.gate_mode != MOE_GATE_CHANNEL) return;
-    if (out == nullptr) return;
     const int col = blockIdx.x * 32 + (threadIdx.x & 31), w = threadIdx.x >> 5;
     double s = 0.0;
-    if (col < p.H)
-        for (int b = w; b < p.blocks; b += 8) s += (double)p.part[((size_t)b * 3 + which) * p.H + col];
+    if (col < p.H) {
+#pragma unroll 8
+        for (int b = w; b < p.blocks; b += 8) s += (double)p.part[((size_t)b * 2 + which) * p.H + col];
+    }
     sh[w][threadIdx.x & 31] = s;
     __syncthreads();
-    if (w == 0 && col < p.H) {
+    if (w != 0 || col >= p.H) return;
 #pragma unroll
-        for (int i = 1; i < 8; ++i) s += sh[i][threadIdx.x];
-        out[col] = (float)s;
+    for (int i = 1; i < 8; ++i) s += sh[i][threadIdx.x];
+    if (which == 1) {
+        p.dgamma_pre[col] = (float)s;
+    } else if (p.gate_mode == MOE_GATE_CHANNEL) {
+        p.dgamma_post[col] = (float)(s * (double)__uint_as_float((uint32_t)p.gate[col] << 16));
+        static_cast<float*>(p.dgate)[col] = (float)(s * (double)__uint_as_float((uint32_t)p.gamma_post[col] << 16));
+    } else {
+        p.dgamma_post[col] = (float)s;
     }
-}
-
-// Threads of a block: one 8-value vector each up to 1024 threads, then as few
-// vectors each as cover the row.
-struct NrShape {
-    int nv, threads;
-};
-NrShape nr_shape(int H) {
-    const int nvec = H / 8;
-    const int nv = (nvec + 1023) / 1024;
-    return {nv, ((nvec + nv - 1) / nv + 31) / 32 * 32};
 }
 
 moe_status_t nfail(moe_status_t st, const char* fmt, const char* a, long long b = 0) {
@@ -368,6 +504,44 @@ moe_status_t launched(const char* what) {
     return nfail(MOE_ERR_CUDA, what, cudaGetErrorString(e));
 }
 
+template <int NV, int ST, int THREADS, bool TOKEN>
+moe_status_t launch_forward(const NrArgs& p, int threads, cudaStream_t s) {
+    auto* kernel = norm_residual_kernel<NV, ST, THREADS, TOKEN>;
+    const int smem = ST * (TOKEN ? 3 : 2) * NV * threads * 16;
+    int sms = 0, fit = 1;
+    NR_TRY(moe::api_sm_count(&sms));
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess && p.T > sms) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kernel, threads, smem);
+    if (e != cudaSuccess) return nfail(MOE_ERR_CUDA, "norm_residual: %s", cudaGetErrorString(e));
+    const int most = sms * (fit > 0 ? fit : 1);
+    kernel<<<p.T < most ? p.T : most, threads, smem, s>>>(p);
+    return launched("norm_residual launch: %s");
+}
+
+// One 8-value vector a thread, two up to 16384 columns, and as many blocks of
+// an SM as registers and shared memory hold (two of 640 threads for a row of
+// 5120: one leaves the SM idle while it waits for its sums, 131 against ... us
+// for 8192 rows).
+template <bool TOKEN>
+moe_status_t run_forward(const NrArgs& p, cudaStream_t s) {
+    const int nvec = p.H / 8, nv = nvec <= 1024 ? 1 : 2;
+    const int threads = ((nvec + nv - 1) / nv + 31) / 32 * 32;
+    if (nv == 2) return launch_forward<2, 2, 1024, TOKEN>(p, threads, s);
+    if (threads <= 320) return launch_forward<1, kNrStages, 320, TOKEN>(p, threads, s);
+    if (threads <= 640) return launch_forward<1, kNrStages, 640, TOKEN>(p, threads, s);
+    return launch_forward<1, kNrStages, 1024, TOKEN>(p, threads, s);
+}
+
+template <int THREADS, bool TOKEN>
+moe_status_t launch_backward(const NrArgs& p, int threads, cudaStream_t s) {
+    const int smem = kNrStages * (TOKEN ? 5 : 4) * threads * 16;
+    const cudaError_t e = cudaFuncSetAttribute(norm_residual_bwd_kernel<THREADS, TOKEN>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return nfail(MOE_ERR_CUDA, "norm_residual backward: %s", cudaGetErrorString(e));
+    norm_residual_bwd_kernel<THREADS, TOKEN><<<p.blocks, threads, smem, s>>>(p);
+    return MOE_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -411,19 +585,14 @@ moe_status_t moe_norm_residual(const moe_config_t* cfg, const void* h, const voi
     p.h_out = static_cast<uint16_t*>(h_out);
     p.u = static_cast<uint16_t*>(u);
     p.rstd = rstd;
-    const NrShape sh = nr_shape(p.H);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (sh.nv == 1)
-        norm_residual_kernel<1><<<p.T, sh.threads, 0, s>>>(p);
-    else
-        norm_residual_kernel<2><<<p.T, sh.threads, 0, s>>>(p);
-    return launched("norm_residual launch: %s");
+    return gate_mode == MOE_GATE_TOKEN ? run_forward<true>(p, s) : run_forward<false>(p, s);
 }
 
 size_t moe_norm_residual_workspace_size(const moe_config_t* cfg) {
     moe::api_clear_error();
     if (check_shape(cfg) != MOE_OK) return 0;
-    return (size_t)kNrBwdBlocks * 3 * cfg->H * 4;
+    return (size_t)kNrBwdBlocks * 2 * cfg->H * 4;
 }
 
 moe_status_t moe_norm_residual_backward(const moe_config_t* cfg, const void* h, const void* y,
@@ -468,7 +637,7 @@ moe_status_t moe_norm_residual_backward(const moe_config_t* cfg, const void* h, 
                 return nfail(MOE_ERR_INVALID_ARG, "%s overlaps another output", o.name);
     }
     NR_TRY(need(ws, "workspace", 256));
-    const size_t bytes = (size_t)kNrBwdBlocks * 3 * cfg->H * 4;
+    const size_t bytes = (size_t)kNrBwdBlocks * 2 * cfg->H * 4;
     if (ws_bytes < bytes)
         return nfail(MOE_ERR_WORKSPACE, "workspace too small, %s %lld bytes", "needs", (long long)bytes);
     NrArgs p = {};
@@ -491,17 +660,26 @@ moe_status_t moe_norm_residual_backward(const moe_config_t* cfg, const void* h, 
     p.dgamma_pre = dgamma_pre;
     p.part = static_cast<float*>(ws);
     p.blocks = cfg->T < kNrBwdBlocks ? cfg->T : kNrBwdBlocks;
-    const NrShape sh = nr_shape(p.H);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (p.T > 0) {
-        if (sh.nv == 1)
-            norm_residual_bwd_kernel<1><<<p.blocks, sh.threads, 0, s>>>(p);
-        else
-            norm_residual_bwd_kernel<2><<<p.blocks, sh.threads, 0, s>>>(p);
+        // one 8-value vector a thread while a row fits 640 threads
+        const int threads = (p.H / 8 + 31) / 32 * 32;
+        const bool token = gate_mode == MOE_GATE_TOKEN;
+        if (threads <= 320) {
+            NR_TRY((token ? launch_backward<320, true>(p, threads, s) : launch_backward<320, false>(p, threads, s)));
+        } else if (threads <= 640) {
+            NR_TRY((token ? launch_backward<640, true>(p, threads, s) : launch_backward<640, false>(p, threads, s)));
+        } else {
+            const int smem = 2 * p.H * 4;
+            const cudaError_t e = cudaFuncSetAttribute(norm_residual_bwd_wide_kernel,
+                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            if (e != cudaSuccess) return nfail(MOE_ERR_CUDA, "norm_residual backward: %s", cudaGetErrorString(e));
+            norm_residual_bwd_wide_kernel<<<p.blocks, kNrWideThreads, smem, s>>>(p);
+        }
         NR_TRY(launched("norm_residual backward launch: %s"));
     }
     // with no rows the sums are zero
-    norm_residual_cols_kernel<<<dim3((p.H + 31) / 32, 3), 256, 0, s>>>(p);
+    norm_residual_cols_kernel<<<dim3((p.H + 31) / 32, dgamma_pre ? 2 : 1), 256, 0, s>>>(p);
     return launched("norm_residual column-sum launch: %s");
 }
 
