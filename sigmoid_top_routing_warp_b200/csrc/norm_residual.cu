@@ -36,6 +36,7 @@ namespace {
 
 constexpr int kNrMaxH = 16384;
 constexpr int kNrWideThreads = 512;
+constexpr int kNrBwdThreads = 320; // of a block of the backward pass: one or two 8-value vectors each
 constexpr int kNrBwdBlocks = 148;   // row walkers of the backward pass, one partial sum each
 
 struct NrArgs {
@@ -252,29 +253,33 @@ __global__ void __launch_bounds__(THREADS, 1280 / THREADS) norm_residual_kernel(
     }
 }
 
-// Persistent blocks, one 8-value vector of the row per thread; a thread owns
+// Persistent blocks, NV 8-value vectors of the row per thread; a thread owns
 // the same columns in every row, so the column sums stay in its registers and
 // leave as one partial per block.  A gate per channel and no gate are constant
 // down a column, so sum(D yn) alone gives both dgamma_post (times g) and dgate
 // (times gamma_post); with a gate per token it is sum(D g yn).
-template <int THREADS, bool TOKEN>
-__global__ void __launch_bounds__(THREADS) norm_residual_bwd_kernel(const NrArgs p) {
+template <int NV, bool TOKEN>
+__global__ void __launch_bounds__(kNrBwdThreads) norm_residual_bwd_kernel(const NrArgs p) {
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float sh[2][3 * 32];
     constexpr int NT = TOKEN ? 5 : 4;                 // tensors of a row: y, h, dh_out, du, gate
-    const int c = threadIdx.x, nthr = blockDim.x;
-    const bool ok = c < p.H / 8;
-    const int cc = ok ? c : 0;
+    const int nthr = blockDim.x, nvec = p.H / 8;
     const float inv_h = 1.0f / (float)p.H;
-    const uint32_t mine = (uint32_t)__cvta_generic_to_shared(smem) + c * 16;
-    auto place = [&](int st, int k) { return mine + (st * NT + k) * nthr * 16; };
+    const uint32_t mine = (uint32_t)__cvta_generic_to_shared(smem) + threadIdx.x * 16;
+    auto place = [&](int st, int k, int i) { return mine + ((st * NT + k) * NV + i) * nthr * 16; };
     auto fetch = [&](size_t t, int st) {
         if (t < (size_t)p.T) {
-            copy16(place(st, 0), vec(p.y, t, p.H) + cc, ok);
-            copy16(place(st, 1), vec(p.h, t, p.H) + cc, ok);
-            copy16(place(st, 2), vec(p.dh_out, t, p.H) + cc, ok);
-            copy16(place(st, 3), p.du ? vec(p.du, t, p.H) + cc : vec(p.y, t, p.H) + cc, ok && p.du);
-            if (TOKEN) copy16(place(st, 4), vec(p.gate, t, p.H) + cc, ok);
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = threadIdx.x + i * nthr;
+                const bool ok = c < nvec;
+                const int cc = ok ? c : 0;
+                copy16(place(st, 0, i), vec(p.y, t, p.H) + cc, ok);
+                copy16(place(st, 1, i), vec(p.h, t, p.H) + cc, ok);
+                copy16(place(st, 2, i), vec(p.dh_out, t, p.H) + cc, ok);
+                copy16(place(st, 3, i), (p.du ? vec(p.du, t, p.H) : vec(p.y, t, p.H)) + cc, ok && p.du);
+                if (TOKEN) copy16(place(st, 4, i), vec(p.gate, t, p.H) + cc, ok);
+            }
         }
         copies_close();
     };
@@ -282,57 +287,79 @@ __global__ void __launch_bounds__(THREADS) norm_residual_bwd_kernel(const NrArgs
     const size_t step = gridDim.x;
     fetch(t, 0);
     fetch(t + step, 1);
-    const uint4 zero = make_uint4(0, 0, 0, 0);
-    const uint4 one = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
-    const uint4 w1 = ok ? __ldg(vec(p.gamma_post, 0, p.H) + c) : zero;
-    const uint4 w2 = ok && p.du ? __ldg(vec(p.gamma_pre, 0, p.H) + c) : zero;
-    const uint4 gc = ok && p.gate_mode == MOE_GATE_CHANNEL ? __ldg(vec(p.gate, 0, p.H) + c) : one;
-    const F2 a2 = f2(p.a, p.a);
-    F2 sp[4], sq[4];
+    // the columns' weights; a gate that is the same in every row is part of wp
+    F2 wp[NV][4], wq[NV][4], sp[NV][4], sq[NV][4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) sp[j] = sq[j] = f2(0.0f, 0.0f);
-    int st = 0, half = 0;
-    for (; t < (size_t)p.T; t += step) {
-        const float rp = __ldg(p.rstd_in + t), rq = p.du ? __ldg(p.rstd_in + p.T + t) : 0.0f;
-        const F2 rp2 = f2(rp, rp), rq2 = f2(rq, rq);
-        copies_left<1>();
-        const uint4 yr = lds128(place(st, 0)), hr = lds128(place(st, 1)), dr = lds128(place(st, 2)),
-                    ur = lds128(place(st, 3));
-        const uint4 gr = TOKEN ? lds128(place(st, 4)) : gc;
-        fetch(t + 2 * step, st == 0 ? kNrStages - 1 : st - 1);
-        st = st == kNrStages - 1 ? 0 : st + 1;
-        F2 yn[4], hn[4], dq[4];                       // dq: dh' + rq q
-        F2 x0 = f2(0.0f, 0.0f), x1 = x0, x2 = x0;
+    for (int i = 0; i < NV; ++i) {
+        const int c = threadIdx.x + i * nthr;
+        const bool ok = c < nvec;
+        const uint4 zero = make_uint4(0, 0, 0, 0);
+        const uint4 one = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
+        const uint4 w1 = ok ? __ldg(vec(p.gamma_post, 0, p.H) + c) : zero;
+        const uint4 w2 = ok && p.du ? __ldg(vec(p.gamma_pre, 0, p.H) + c) : zero;
+        const uint4 gc = ok && p.gate_mode == MOE_GATE_CHANNEL ? __ldg(vec(p.gate, 0, p.H) + c) : one;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            yn[j] = widen(word(yr, j)) * rp2;
-            const F2 w = widen(word(gr, j)) * (widen(word(w1, j)) * yn[j]);
-            hn[j] = fma2(a2, widen(word(hr, j)), w) * rq2;
-            const F2 u = widen(word(ur, j));
-            const F2 q = u * widen(word(w2, j));
-            dq[j] = fma2(rq2, q, widen(word(dr, j)));
-            x0 = fma2(q, hn[j], x0);
-            x1 = fma2(w, dq[j], x1);
-            x2 = fma2(w, hn[j], x2);
-            sq[j] = fma2(u, hn[j], sq[j]);
+            wp[i][j] = TOKEN ? widen(word(w1, j)) : widen(word(gc, j)) * widen(word(w1, j));
+            wq[i][j] = widen(word(w2, j));
+            sp[i][j] = sq[i][j] = f2(0.0f, 0.0f);
         }
+    }
+    const F2 a2 = f2(p.a, p.a);
+    int st = 0, half = 0;
+    float rp_next = __ldg(p.rstd_in + t), rq_next = p.du ? __ldg(p.rstd_in + p.T + t) : 0.0f;
+    for (; t < (size_t)p.T; t += step) {
+        const float rp = rp_next, rq = rq_next;
+        const F2 rp2 = f2(rp, rp), rq2 = f2(rq, rq);
+        copies_left<1>();
+        if (t + step < (size_t)p.T) {
+            rp_next = __ldg(p.rstd_in + t + step);
+            rq_next = p.du ? __ldg(p.rstd_in + p.T + t + step) : 0.0f;
+        }
+        F2 yn[NV][4], hn[NV][4], dq[NV][4];           // dq: dh' + rq q
+        uint4 gr[NV];
+        F2 x0 = f2(0.0f, 0.0f), x1 = x0, x2 = x0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const uint4 yr = lds128(place(st, 0, i)), hr = lds128(place(st, 1, i)), dr = lds128(place(st, 2, i)),
+                        ur = lds128(place(st, 3, i));
+            if (TOKEN) gr[i] = lds128(place(st, 4, i));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                yn[i][j] = widen(word(yr, j)) * rp2;
+                F2 w = wp[i][j] * yn[i][j];
+                if (TOKEN) w = widen(word(gr[i], j)) * w;
+                hn[i][j] = fma2(a2, widen(word(hr, j)), w) * rq2;
+                const F2 u = widen(word(ur, j));
+                const F2 q = u * wq[i][j];
+                dq[i][j] = fma2(rq2, q, widen(word(dr, j)));
+                x0 = fma2(q, hn[i][j], x0);
+                x1 = fma2(w, dq[i][j], x1);
+                x2 = fma2(w, hn[i][j], x2);
+                sq[i][j] = fma2(u, hn[i][j], sq[i][j]);
+            }
+        }
+        fetch(t + 2 * step, st == 0 ? kNrStages - 1 : st - 1);
+        st = st == kNrStages - 1 ? 0 : st + 1;
         float s[3] = {total(x0), total(x1), total(x2)};
         block_sum(s, sh[half]);
         half ^= 1;
         const float c1 = s[0] * inv_h, c2 = (s[1] - rq * c1 * s[2]) * inv_h;
         const F2 k1 = f2(-rq * c1, -rq * c1), k2 = f2(-c2, -c2);
-        uint32_t odh[4], ody[4], odg[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const F2 wp = widen(word(w1, j)), g = widen(word(gr, j));
-            const F2 D = fma2(hn[j], k1, dq[j]);
-            const F2 Dg = D * g;
-            odh[j] = narrow(a2 * D);
-            ody[j] = narrow(rp2 * fma2(yn[j], k2, Dg * wp));
-            if (TOKEN) odg[j] = narrow(D * (wp * yn[j]));
-            sp[j] = fma2(TOKEN ? Dg : D, yn[j], sp[j]);
-        }
-        if (ok) {
+        for (int i = 0; i < NV; ++i) {
+            const int c = threadIdx.x + i * nthr;
+            uint32_t odh[4], ody[4], odg[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const F2 D = fma2(hn[i][j], k1, dq[i][j]);
+                const F2 Dg = TOKEN ? D * widen(word(gr[i], j)) : D;
+                odh[j] = narrow(a2 * D);
+                ody[j] = narrow(rp2 * fma2(yn[i][j], k2, Dg * wp[i][j]));
+                if (TOKEN) odg[j] = narrow(D * (wp[i][j] * yn[i][j]));
+                sp[i][j] = fma2(Dg, yn[i][j], sp[i][j]);
+            }
+            if (c >= nvec) continue;
             reinterpret_cast<uint4*>(p.dh + t * p.H)[c] = make_uint4(odh[0], odh[1], odh[2], odh[3]);
             reinterpret_cast<uint4*>(p.dy + t * p.H)[c] = make_uint4(ody[0], ody[1], ody[2], ody[3]);
             if (TOKEN)
@@ -340,15 +367,19 @@ __global__ void __launch_bounds__(THREADS) norm_residual_bwd_kernel(const NrArgs
                     make_uint4(odg[0], odg[1], odg[2], odg[3]);
         }
     }
-    if (!ok) return;
-    float* base = p.part + (size_t)blockIdx.x * 2 * p.H + 8 * c;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        float x, y;
-        split(sp[j], x, y);
-        *reinterpret_cast<float2*>(base + 2 * j) = make_float2(x, y);
-        split(sq[j], x, y);
-        *reinterpret_cast<float2*>(base + p.H + 2 * j) = make_float2(x, y);
+    for (int i = 0; i < NV; ++i) {
+        const int c = threadIdx.x + i * nthr;
+        if (c >= nvec) continue;
+        float* base = p.part + (size_t)blockIdx.x * 2 * p.H + 8 * c;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float x, y;
+            split(sp[i][j], x, y);
+            *reinterpret_cast<float2*>(base + 2 * j) = make_float2(x, y);
+            split(sq[i][j], x, y);
+            *reinterpret_cast<float2*>(base + p.H + 2 * j) = make_float2(x, y);
+        }
     }
 }
 
@@ -518,10 +549,10 @@ moe_status_t launch_forward(const NrArgs& p, int threads, cudaStream_t s) {
     return launched("norm_residual launch: %s");
 }
 
-// One 8-value vector a thread, two up to 16384 columns, and as many blocks of
-// an SM as registers and shared memory hold (two of 640 threads for a row of
-// 5120: one leaves the SM idle while it waits for its sums, 131 against ... us
-// for 8192 rows).
+// One 8-value vector a thread, two above 8192 columns, and as many blocks of
+// an SM as registers and shared memory hold: with one block of 640 threads the
+// SM idles while it waits for a row's sums (8192 rows of 5120: 131 us against
+// 82 with two).
 template <bool TOKEN>
 moe_status_t run_forward(const NrArgs& p, cudaStream_t s) {
     const int nvec = p.H / 8, nv = nvec <= 1024 ? 1 : 2;
@@ -532,13 +563,14 @@ moe_status_t run_forward(const NrArgs& p, cudaStream_t s) {
     return launch_forward<1, kNrStages, 1024, TOKEN>(p, threads, s);
 }
 
-template <int THREADS, bool TOKEN>
-moe_status_t launch_backward(const NrArgs& p, int threads, cudaStream_t s) {
-    const int smem = kNrStages * (TOKEN ? 5 : 4) * threads * 16;
-    const cudaError_t e = cudaFuncSetAttribute(norm_residual_bwd_kernel<THREADS, TOKEN>,
+template <int NV, bool TOKEN>
+moe_status_t launch_backward(const NrArgs& p, cudaStream_t s) {
+    const int threads = ((p.H / 8 + NV - 1) / NV + 31) / 32 * 32;
+    const int smem = kNrStages * (TOKEN ? 5 : 4) * NV * threads * 16;
+    const cudaError_t e = cudaFuncSetAttribute(norm_residual_bwd_kernel<NV, TOKEN>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return nfail(MOE_ERR_CUDA, "norm_residual backward: %s", cudaGetErrorString(e));
-    norm_residual_bwd_kernel<THREADS, TOKEN><<<p.blocks, threads, smem, s>>>(p);
+    norm_residual_bwd_kernel<NV, TOKEN><<<p.blocks, threads, smem, s>>>(p);
     return MOE_OK;
 }
 
@@ -662,13 +694,11 @@ moe_status_t moe_norm_residual_backward(const moe_config_t* cfg, const void* h, 
     p.blocks = cfg->T < kNrBwdBlocks ? cfg->T : kNrBwdBlocks;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (p.T > 0) {
-        // one 8-value vector a thread while a row fits 640 threads
-        const int threads = (p.H / 8 + 31) / 32 * 32;
         const bool token = gate_mode == MOE_GATE_TOKEN;
-        if (threads <= 320) {
-            NR_TRY((token ? launch_backward<320, true>(p, threads, s) : launch_backward<320, false>(p, threads, s)));
-        } else if (threads <= 640) {
-            NR_TRY((token ? launch_backward<640, true>(p, threads, s) : launch_backward<640, false>(p, threads, s)));
+        if (p.H <= 8 * kNrBwdThreads) {
+            NR_TRY((token ? launch_backward<1, true>(p, s) : launch_backward<1, false>(p, s)));
+        } else if (p.H <= 16 * kNrBwdThreads) {
+            NR_TRY((token ? launch_backward<2, true>(p, s) : launch_backward<2, false>(p, s)));
         } else {
             const int smem = 2 * p.H * 4;
             const cudaError_t e = cudaFuncSetAttribute(norm_residual_bwd_wide_kernel,
