@@ -33,10 +33,10 @@
 //
 // 8- and 4-bit weights become binary16 by one conversion for two weights
 // (exact: both types lie inside it), and the activations meet them in binary16
-// too: a warp scales its 64 columns of a token by the power of two that takes
-// the largest to 2^14, which keeps every bit of a bf16 value down to 2^-28 of
-// the largest and is off by 2^-39 of it below; the sums are brought back in
-// fp32 together with the weights' block scales.
+// too: their producer scales 64 columns of a token by the power of two that
+// takes the largest to 2^14, which keeps every bit of a bf16 value down to
+// 2^-28 of the largest and is off by 2^-39 of it below; the sums are brought
+// back in fp32 together with the weights' block scales.
 #include "moe.h"
 #include "kernels.cuh"
 #include "ptx.cuh"
@@ -80,8 +80,8 @@ constexpr int kMaxStages = 8;
 constexpr int kBarWord = moe::kSchedFirstWord;   // grid barriers (2) and the exit count, in the status block
 
 // Per weight type: rows of a unit, bits of a weight, bytes of a stage's
-// scales, and the activation rows' padding in a stage.  A stage holds 32 KB of
-// weights, as 128-byte pieces of 8 rows (1024 bytes, 128-byte swizzle: 64-byte
+// scales and of its activations' factors (one for 64 columns of a row), and the
+// activation rows' padding.  A stage holds 32 KB of weights, as 128-byte pieces of 8 rows (1024 bytes, 128-byte swizzle: 64-byte
 // pieces ran at 5 TB/s at most).  A lane's part of a piece, and the padding of
 // the activation rows, are chosen so that a load's lanes (8 rows by 4) fall on
 // different banks:
@@ -92,15 +92,15 @@ template <int DT>
 struct Fmt;
 template <>
 struct Fmt<MOE_DTYPE_BF16> {
-    static constexpr int kRows = 16, kBits = 16, kScaleBytes = 0, kPad = 16;
+    static constexpr int kRows = 16, kBits = 16, kScaleBytes = 0, kInvBytes = 0, kPad = 16;
 };
 template <>
 struct Fmt<MOE_DTYPE_FP8_E4M3_BLOCK128> {
-    static constexpr int kRows = 32, kBits = 8, kScaleBytes = 128, kPad = 32;  // scales: [2][8] fp32
+    static constexpr int kRows = 32, kBits = 8, kScaleBytes = 128, kInvBytes = 512, kPad = 32;  // scales: [2][8] fp32
 };
 template <>
 struct Fmt<MOE_DTYPE_MXFP4_BLOCK32> {
-    static constexpr int kRows = 64, kBits = 4, kScaleBytes = 2048, kPad = 64;  // [64][32] e8m0
+    static constexpr int kRows = 64, kBits = 4, kScaleBytes = 2048, kInvBytes = 512, kPad = 64;  // [64][32] e8m0
 };
 
 struct FewArgs {
@@ -679,6 +679,60 @@ __device__ __forceinline__ void copy_row(uint32_t dst, const uint16_t* src, int 
     }
 }
 
+// Exponent field (biased) of the factor that takes the largest of 64 values,
+// eight in each of eight lanes, to 2^14 .. 2^15: an infinity or NaN counts as
+// 2^128, and tiny ones are lifted by at most 2^126.
+__device__ __forceinline__ uint32_t block_lift(const uint4& v) {
+    uint32_t m = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
+                          __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+#pragma unroll
+    for (int off = 1; off < 8; off <<= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, off));
+    const uint32_t e = max(m & 0xffffu, m >> 16) >> 7;
+    return min(268u - e, 253u);
+}
+__device__ __forceinline__ uint32_t lifted(uint32_t w, float f) {
+    const float lo = __uint_as_float(w << 16) * f, hi = __uint_as_float(w & 0xffff0000u) * f;
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ void put_lifted(uint32_t dst, const uint4& v, float f) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(lifted(v.x, f)), "r"(lifted(v.y, f)),
+                 "r"(lifted(v.z, f)), "r"(lifted(v.w, f))
+                 : "memory");
+}
+
+// The same rows in binary16, lifted: `src` to `dst` and, with TAIL, `tail` to
+// `dst + to_tail` with the factors of its head (a tail is at most 2^-8 of it).
+// `inv`: what undoes the factors, one value for 64 columns.
+template <bool TAIL>
+__device__ __forceinline__ void lift_row(uint32_t dst, uint32_t to_tail, const uint16_t* src, const uint16_t* tail,
+                                         int kn, uint32_t inv) {
+    const int lane = threadIdx.x & 31;
+    uint4 v[kChunk / 256], l[kChunk / 256];
+#pragma unroll
+    for (int j = 0; j < kChunk / 256; ++j) {
+        const int c = lane * 8 + j * 256;
+        v[j] = l[j] = make_uint4(0, 0, 0, 0);
+        if (c < kn) {
+            v[j] = __ldcg(reinterpret_cast<const uint4*>(src + c));
+            if (TAIL) l[j] = __ldcg(reinterpret_cast<const uint4*>(tail + c));
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < kChunk / 256; ++j) {
+        if (j * 256 >= kn) break;
+        const uint32_t lift = block_lift(v[j]);
+        const float f = __uint_as_float(lift << 23);
+        if (lane * 8 + j * 256 >= kn) continue;
+        put_lifted(dst + lane * 16 + j * 512, v[j], f);
+        if (TAIL) put_lifted(dst + to_tail + lane * 16 + j * 512, l[j], f);
+        if ((lane & 7) == 0)
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(inv + (j * 4 + (lane >> 3)) * 4), "r"((254u - lift) << 23)
+                         : "memory");
+    }
+}
+
 // ------------------------------------------------------------------ multiplication
 // four e4m3 codes -> two binary16 pairs
 __device__ __forceinline__ void widen_e4m3(uint32_t v, uint32_t& p0, uint32_t& p1) {
@@ -715,27 +769,6 @@ __device__ __forceinline__ void load_acts(uint32_t row, int t, uint32_t (&b)[8])
     }
 }
 
-// Exponent field (biased) of the factor that takes the largest of the column's
-// 64 values to 2^14 .. 2^15: an infinity or NaN counts as 2^128, and tiny ones
-// are lifted by at most 2^126.
-__device__ __forceinline__ uint32_t block_lift(const uint32_t (&b)[8]) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = __vmaxu2(m, b[i] & 0x7fff7fffu);
-    m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    const uint32_t e = max(m & 0xffffu, m >> 16) >> 7;
-    return min(268u - e, 253u);
-}
-__device__ __forceinline__ void to_f16(uint32_t (&b)[8], uint32_t lift) {
-    const float f = __uint_as_float(lift << 23);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float lo = __uint_as_float(b[i] << 16) * f, hi = __uint_as_float(b[i] & 0xffff0000u) * f;
-        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(b[i]) : "f"(hi), "f"(lo));
-    }
-}
-
 // Which activation rows a lane multiplies in phase 1 (its column's token's
 // place in the unit's list) or in phase 2 (a column is a token; one that does
 // not use the expert multiplies some row, and its products are dropped).
@@ -746,6 +779,7 @@ template <int NT>
 struct Columns {
     int x[NT];          // the lane's row in a stage
     int tail;           // from a head to its tail
+    int inv[NT][2];     // the factors of the lane's two result columns
     bool own[NT][2];    // the lane's two result columns are the expert's tokens
     bool on[NT];        // the tile has any
 };
@@ -811,13 +845,8 @@ __device__ __forceinline__ void mma_tile(uint32_t stage, uint32_t sc, int slice,
     if (TAIL) load_acts<DT>(x + col.tail, t, bl);
     float back[2] = {1.0f, 1.0f};   // undoes the lift of the lane's two result columns
     if (!kBf16) {
-        // a tail is at most 2^-8 of its head and takes the head's lift
-        const uint32_t lift = block_lift(b);
-        to_f16(b, lift);
-        if (TAIL) to_f16(bl, lift);
-        const float inv = __uint_as_float((254u - lift) << 23);
-        back[0] = __shfl_sync(0xffffffffu, inv, 8 * t);
-        back[1] = __shfl_sync(0xffffffffu, inv, 8 * t + 4);
+        back[0] = __uint_as_float(lds32(sc - F::kInvBytes + col.inv[nt][0] + slice * 4));
+        back[1] = __uint_as_float(lds32(sc - F::kInvBytes + col.inv[nt][1] + slice * 4));
     }
     // row g of the slice's piece; its 16-byte parts are swizzled by the row,
     // and the slice's first part is a multiple of a power of two of them
@@ -1008,13 +1037,20 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
     } else if (warp > 2 * kWarps) {
         // ---------------------------------------------------------- activation producers
         const int feeder = warp - 2 * kWarps - 1;
+        constexpr bool kLift = F::kInvBytes > 0;
         auto fed = [&]() {
-            arrive_copied(ring.x + 8 * ring.slot);
+            if (kLift)
+                bar_done(ring.x + 8 * ring.slot);
+            else
+                arrive_copied(ring.x + 8 * ring.slot);
+        };
+        auto factors = [&](int row, int cols) {     // of an activation row of the stage
+            return ring.stage() + ring.scales - F::kInvBytes + row * (cols / kSlice * 4);
         };
         uint32_t mask = 0;
-        int xs = 0, off = 0;     // of the unit's stages
+        int cols = 0, xs = 0, off = 0;     // of the unit's stages
         auto shape = [&](bool down, int count) {
-            const int cols = chunk_cols(down, count);
+            cols = chunk_cols(down, count);
             xs = x_stride<DT>(cols);
             off = off_x(cols);
         };
@@ -1022,8 +1058,14 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
             if (ring.feeder() == feeder) {
                 if (!wait(ring.empty + 8 * ring.slot, ring.phase ^ 1)) return false;
                 uint32_t dst = ring.stage() + off;
-                for (uint32_t m = mask; m; m &= m - 1, dst += xs)
-                    copy_row(dst, a.x + (size_t)(__ffs(m) - 1) * a.H + k0, kn);
+                int i = 0;
+                for (uint32_t m = mask; m; m &= m - 1, dst += xs, ++i) {
+                    const uint16_t* src = a.x + (size_t)(__ffs(m) - 1) * a.H + k0;
+                    if (kLift)
+                        lift_row<false>(dst, 0, src, nullptr, kn, factors(i, cols));
+                    else
+                        copy_row(dst, src, kn);
+                }
                 fed();
             }
             ring.next();
@@ -1074,8 +1116,12 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
                                   const uint16_t *h = hi + k0, *l = lo + k0;
                                   const uint32_t tail = (uint32_t)(count * xs);
                                   for (int i = 0; i < count; ++i, dst += xs, h += a.ld_act, l += a.ld_act) {
-                                      copy_row(dst, h, kn);
-                                      copy_row(dst + tail, l, kn);
+                                      if (kLift) {
+                                          lift_row<true>(dst, tail, h, l, kn, factors(i, cols));
+                                      } else {
+                                          copy_row(dst, h, kn);
+                                          copy_row(dst + tail, l, kn);
+                                      }
                                   }
                                   fed();
                               }
@@ -1261,6 +1307,11 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
             for (int i = 0; i < NT; ++i) {
                 col.x[i] = off_x(cols) + (8 * i + g < count ? 8 * i + g : 0) * x_stride<DT>(cols);
                 col.on[i] = count > 8 * i;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int c = 8 * i + 2 * t + j;
+                    col.inv[i][j] = (c < count ? c : 0) * (cols / kSlice * 4);
+                }
             }
             walk_unit(a, count, [&](int, int kn) { return step(std::false_type{}, kn); });
             sum.fold(col, true);
@@ -1315,8 +1366,11 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
                     const int row = __popc(act.mask & ((1u << tok) - 1u)) + (FOLD && g >= 4 ? act.count : 0);
                     col.x[i] = off_x(cols) + (has ? row * xs : 0);
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        col.own[i][j] = act.mask >> (FOLD ? (2 * t + j) & 3 : 8 * i + 2 * t + j) & 1u;
+                    for (int j = 0; j < 2; ++j) {
+                        const int c = FOLD ? (2 * t + j) & 3 : 8 * i + 2 * t + j;
+                        col.own[i][j] = act.mask >> c & 1u;
+                        col.inv[i][j] = col.own[i][j] ? __popc(act.mask & ((1u << c) - 1u)) * (cols / kSlice * 4) : 0;
+                    }
                     col.on[i] = act.mask >> (8 * i) & 255u;
                 }
                 return true;
@@ -1514,7 +1568,7 @@ moe_status_t few_smem(FewArgs& a, int limit, size_t* bytes) {
     off += red_warps(tiles) * tiles * 512;
     a.off_ring = up(off, 1024);
     // eight activation rows of a full stage; fewer columns leave room for more
-    a.stage_bytes = up(kChunk / kBox * kBoxBytes + (a.T <= 4 ? 2 * a.T : 8) * (kChunk * 2 + F::kPad) + F::kScaleBytes, 1024);
+    a.stage_bytes = up(kChunk / kBox * kBoxBytes + (a.T <= 4 ? 2 * a.T : 8) * (kChunk * 2 + F::kPad) + F::kInvBytes + F::kScaleBytes, 1024);
     const int stages = (limit - 1024 - a.off_ring) / a.stage_bytes;   // 1024: the boxes' alignment
     a.n_stages = stages < kMaxStages ? stages : kMaxStages;
     if (a.n_stages < 2)
