@@ -33,16 +33,20 @@
 //
 // 8- and 4-bit weights become binary16 by one conversion for two weights
 // (exact: both types lie inside it), and the activations meet them in binary16
-// too: their producer scales 64 columns of a token by the power of two that
-// takes the largest to 2^14, which keeps every bit of a bf16 value down to
-// 2^-28 of the largest and is off by 2^-39 of it below; the sums are brought
-// back in fp32 together with the weights' block scales.
+// too, lifted: 64 columns of a token, or one unit's features of a SwiGLU
+// output, are scaled by the power of two that takes the largest of them to
+// 2^14, which keeps every bit of a bf16 value down to 2^-28 of the largest and
+// is off by 2^-39 of it below; the sums are brought back in fp32 together with
+// the weights' block scales.  Phase R lifts the tokens once for all (the shared
+// expert's stages, which do not wait for it, lift theirs on the way), phase 1's
+// epilogue its outputs.
 #include "moe.h"
 #include "kernels.cuh"
 #include "ptx.cuh"
 #include "tiles.cuh"
 
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <cstdio>
@@ -67,11 +71,11 @@ constexpr int kTeam = kWarps * 32, kConsumers = 2 * kTeam;
 constexpr int kThreads = kConsumers + 32 + kFeeders * 32;
 constexpr int kRouterVecs = 4;                   // 16-byte vectors of a router lane at a time
 constexpr int kMaxBlocks = 256;                  // blocks the join buffer has room for
-constexpr int kStaticSmem = 3072;                // the kernel's own variables (a launch with less left over fails)
+constexpr int kStaticSmem = 4096;                // the kernel's own variables (a launch with less left over fails)
 constexpr int kHeadStart = 2;                    // stages copied before barrier 0 has been passed
 constexpr int kWindow = 2;                       // stages under way while a barrier or the choice is waited for
 // named barriers
-constexpr int kBarAll = 1, kBarB = 2, kBarRouted = 3, kBarA = 4, kBarLogits = 5;
+constexpr int kBarAll = 1, kBarB = 2, kBarRouted = 3, kBarA = 4, kBarLogits = 5, kBarReaders = 6;
 constexpr int kChunk = 1024;                     // K columns of a full stage
 constexpr int kBox = 256;                        // K columns of one tensor copy
 constexpr int kBoxBytes = 8192;                  // its bytes, for every weight type
@@ -80,7 +84,7 @@ constexpr int kMaxStages = 8;
 constexpr int kBarWord = moe::kSchedFirstWord;   // grid barriers (2) and the exit count, in the status block
 
 // Per weight type: rows of a unit, bits of a weight, bytes of a stage's
-// scales and of its activations' factors (one for 64 columns of a row), and the
+// scales and of its activations' factors, and the
 // activation rows' padding.  A stage holds 32 KB of weights, as 128-byte pieces of 8 rows (1024 bytes, 128-byte swizzle: 64-byte
 // pieces ran at 5 TB/s at most).  A lane's part of a piece, and the padding of
 // the activation rows, are chosen so that a load's lanes (8 rows by 4) fall on
@@ -96,7 +100,7 @@ struct Fmt<MOE_DTYPE_BF16> {
 };
 template <>
 struct Fmt<MOE_DTYPE_FP8_E4M3_BLOCK128> {
-    static constexpr int kRows = 32, kBits = 8, kScaleBytes = 128, kInvBytes = 512, kPad = 32;  // scales: [2][8] fp32
+    static constexpr int kRows = 32, kBits = 8, kScaleBytes = 128, kInvBytes = 1024, kPad = 32;  // scales: [2][8] fp32
 };
 template <>
 struct Fmt<MOE_DTYPE_MXFP4_BLOCK32> {
@@ -114,6 +118,8 @@ struct FewArgs {
     int* status;
     double* logits;             // [T][E]
     uint16_t *act_hi, *act_lo;  // [pairs][ld_act] weighted SwiGLU outputs, head and tail
+    uint16_t* x16;              // [T][H] lifted tokens, and what undoes their factors and
+    float *xinv, *ainv;         // the outputs': [T][H / 64], [pairs][ld_act / features of a unit]
     float* join;                // [blocks][2][T][rows] partial sums of shared row blocks
     int* joined;                // [row blocks] blocks that have left theirs
     int T, H, E, k, I, Is, n_group, topk_group, group_topn, norm, stall, ld_act, batch;
@@ -702,35 +708,47 @@ __device__ __forceinline__ void put_lifted(uint32_t dst, const uint4& v, float f
                  : "memory");
 }
 
-// The same rows in binary16, lifted: `src` to `dst` and, with TAIL, `tail` to
-// `dst + to_tail` with the factors of its head (a tail is at most 2^-8 of it).
-// `inv`: what undoes the factors, one value for 64 columns.
-template <bool TAIL>
-__device__ __forceinline__ void lift_row(uint32_t dst, uint32_t to_tail, const uint16_t* src, const uint16_t* tail,
-                                         int kn, uint32_t inv) {
+// A row of the shared expert's stage in binary16, lifted on the way; `inv`:
+// what undoes the factors, one value for 64 columns.
+__device__ __forceinline__ void lift_row(uint32_t dst, const uint16_t* src, int kn, uint32_t inv) {
     const int lane = threadIdx.x & 31;
-    uint4 v[kChunk / 256], l[kChunk / 256];
+    uint4 v[kChunk / 256];
 #pragma unroll
     for (int j = 0; j < kChunk / 256; ++j) {
         const int c = lane * 8 + j * 256;
-        v[j] = l[j] = make_uint4(0, 0, 0, 0);
-        if (c < kn) {
-            v[j] = __ldcg(reinterpret_cast<const uint4*>(src + c));
-            if (TAIL) l[j] = __ldcg(reinterpret_cast<const uint4*>(tail + c));
-        }
+        v[j] = c < kn ? __ldg(reinterpret_cast<const uint4*>(src + c)) : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
     for (int j = 0; j < kChunk / 256; ++j) {
         if (j * 256 >= kn) break;
         const uint32_t lift = block_lift(v[j]);
-        const float f = __uint_as_float(lift << 23);
         if (lane * 8 + j * 256 >= kn) continue;
-        put_lifted(dst + lane * 16 + j * 512, v[j], f);
-        if (TAIL) put_lifted(dst + to_tail + lane * 16 + j * 512, l[j], f);
+        put_lifted(dst + lane * 16 + j * 512, v[j], __uint_as_float(lift << 23));
         if ((lane & 7) == 0)
             asm volatile("st.shared.u32 [%0], %1;" ::"r"(inv + (j * 4 + (lane >> 3)) * 4), "r"((254u - lift) << 23)
                          : "memory");
     }
+}
+
+// Phase R: the tokens lifted into the workspace, a warp for 256 columns of one.
+__device__ void lift_tokens(const FewArgs& a, int id, int n) {
+    const int lane = threadIdx.x & 31, per = (a.H + 255) / 256;
+    for (int u = id; u < a.T * per; u += n) {
+        const int t = u / per, c = u % per * 256 + lane * 8;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (c < a.H) v = __ldg(reinterpret_cast<const uint4*>(a.x + (size_t)t * a.H + c));
+        const uint32_t lift = block_lift(v);
+        const float f = __uint_as_float(lift << 23);
+        if (c >= a.H) continue;
+        *reinterpret_cast<uint4*>(a.x16 + (size_t)t * a.H + c) =
+            make_uint4(lifted(v.x, f), lifted(v.y, f), lifted(v.z, f), lifted(v.w, f));
+        if ((lane & 7) == 0) a.xinv[(size_t)t * (a.H / 64) + c / 64] = __uint_as_float((254u - lift) << 23);
+    }
+}
+
+// n factors of a row, by the warp.
+__device__ __forceinline__ void copy_factors(uint32_t dst, const float* src, int n) {
+    for (int i = threadIdx.x & 31; i < n; i += 32) copy4(dst + i * 4, src + i);
 }
 
 // ------------------------------------------------------------------ multiplication
@@ -843,11 +861,6 @@ __device__ __forceinline__ void mma_tile(uint32_t stage, uint32_t sc, int slice,
     uint32_t b[8], bl[8];
     load_acts<DT>(x, t, b);
     if (TAIL) load_acts<DT>(x + col.tail, t, bl);
-    float back[2] = {1.0f, 1.0f};   // undoes the lift of the lane's two result columns
-    if (!kBf16) {
-        back[0] = __uint_as_float(lds32(sc - F::kInvBytes + col.inv[nt][0] + slice * 4));
-        back[1] = __uint_as_float(lds32(sc - F::kInvBytes + col.inv[nt][1] + slice * 4));
-    }
     // row g of the slice's piece; its 16-byte parts are swizzled by the row,
     // and the slice's first part is a multiple of a power of two of them
     constexpr int kParts = kSlice * F::kBits / 128;  // 8, 4, 2
@@ -869,8 +882,27 @@ __device__ __forceinline__ void mma_tile(uint32_t stage, uint32_t sc, int slice,
             }
         }
     } else {
+        constexpr bool kFp8 = DT == MOE_DTYPE_FP8_E4M3_BLOCK128;
+        // Sums with one factor: phase 1's are the slice's; phase 2's are a
+        // unit's features, 16 (an MMA) or 32 (two).  An e2m1 scale is for 32.
+        constexpr int CH = kFp8 ? (DOWN ? 4 : 1) : 2;
+        float back[DOWN ? CH : 1][2];   // undo the lift of the lane's two result columns
+        const uint32_t inv = sc - F::kInvBytes;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            if constexpr (!DOWN) {
+                back[0][j] = __uint_as_float(lds32(inv + col.inv[nt][j] + slice * 4));
+            } else if constexpr (kFp8) {
+                const uint4 v = lds128(inv + col.inv[nt][j] + slice * 16);
+                back[0][j] = __uint_as_float(v.x), back[1][j] = __uint_as_float(v.y);
+                back[2][j] = __uint_as_float(v.z), back[3][j] = __uint_as_float(v.w);
+            } else {
+                const uint2 v = lds64(inv + col.inv[nt][j] + slice * 8);
+                back[0][j] = __uint_as_float(v.x), back[1][j] = __uint_as_float(v.y);
+            }
+        }
         float s0 = 0.0f, s1 = 0.0f;
-        if (DT == MOE_DTYPE_FP8_E4M3_BLOCK128) {
+        if (kFp8) {
             s0 = __uint_as_float(lds32(sc + slice / 2 * 4));
             s1 = DOWN ? s0 : __uint_as_float(lds32(sc + slice / 2 * 4 + 32));
         }
@@ -878,12 +910,11 @@ __device__ __forceinline__ void mma_tile(uint32_t stage, uint32_t sc, int slice,
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
             const uint32_t w0 = w + (2 * mt) * PB * 1024, w1 = w0 + PB * 1024;
-            // products in independent chains: two halves of the slice, heads and tails
-            float c[2][4], cl[2][4];
+            float c[4][4];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 uint32_t m[2][4];
-                if (DT == MOE_DTYPE_FP8_E4M3_BLOCK128) {
+                if (kFp8) {
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         widen_e4m3(lds32(w0 + ((2 * h + i) << 4 ^ sw)), m[i][0], m[i][2]);
@@ -896,25 +927,41 @@ __device__ __forceinline__ void mma_tile(uint32_t stage, uint32_t sc, int slice,
                     m[0][0] = p[0], m[0][1] = q[0], m[0][2] = p[1], m[0][3] = q[1];
                     m[1][0] = p[2], m[1][1] = q[2], m[1][2] = p[3], m[1][3] = q[3];
                 }
-                mma16<false>(c[h], m[0], b[4 * h], b[4 * h + 1], zero);
-                if (TAIL) mma16<false>(cl[h], m[0], bl[4 * h], bl[4 * h + 1], zero);
-                mma16<false>(c[h], m[1], b[4 * h + 2], b[4 * h + 3], c[h]);
-                if (TAIL) mma16<false>(cl[h], m[1], bl[4 * h + 2], bl[4 * h + 3], cl[h]);
+                // independent chains where the factors allow them
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    constexpr bool kOwn = kFp8;           // a chain for each MMA, or for each half
+                    float(&d)[4] = c[kOwn ? 2 * h + i : h];
+                    if (kOwn || i == 0)
+                        mma16<false>(d, m[i], b[4 * h + 2 * i], b[4 * h + 2 * i + 1], zero);
+                    else
+                        mma16<false>(d, m[i], b[4 * h + 2 * i], b[4 * h + 2 * i + 1], d);
+                    if (TAIL) mma16<false>(d, m[i], bl[4 * h + 2 * i], bl[4 * h + 2 * i + 1], d);
+                }
             }
             float s[2][2] = {{s0, s1}, {s0, s1}};          // [half][rows g, rows g + 8]
-            if (DT == MOE_DTYPE_MXFP4_BLOCK32) {
+            if (!kFp8) {
                 const uint32_t sr = sc + (mt * 16 + g) * 32 + slice * 2;
                 e8m0x2(lds16(sr), s[0][0], s[1][0]);
                 e8m0x2(lds16(sr + 256), s[0][1], s[1][1]);
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float v0 = TAIL ? c[0][j] + cl[0][j] : c[0][j], v1 = TAIL ? c[1][j] + cl[1][j] : c[1][j];
-                const float v = DT == MOE_DTYPE_FP8_E4M3_BLOCK128 ? (v0 + v1) * s[0][j >> 1]
-                                                                  : fmaf(v0, s[0][j >> 1], v1 * s[1][j >> 1]);
-                const float r = fmaf(v, back[j & 1], sum.acc[mt][nt][j]);
+                float v;
+                if constexpr (kFp8 && DOWN) {
+                    v = c[0][j] * back[0][j & 1];
+#pragma unroll
+                    for (int q = 1; q < 4; ++q) v = fmaf(c[q][j], back[q][j & 1], v);
+                    v *= s[0][j >> 1];
+                } else if constexpr (kFp8) {
+                    v = ((c[0][j] + c[1][j]) + (c[2][j] + c[3][j])) * s[0][j >> 1] * back[0][j & 1];
+                } else if constexpr (DOWN) {
+                    v = fmaf(c[0][j] * back[0][j & 1], s[0][j >> 1], c[1][j] * back[1][j & 1] * s[1][j >> 1]);
+                } else {
+                    v = fmaf(c[0][j], s[0][j >> 1], c[1][j] * s[1][j >> 1]) * back[0][j & 1];
+                }
                 // an infinity or a NaN among the weights reaches the expert's own tokens only
-                if (!DOWN || col.own[nt][j & 1]) sum.acc[mt][nt][j] = r;
+                sum.acc[mt][nt][j] += !DOWN || col.own[nt][j & 1] ? v : 0.0f;
             }
         }
     }
@@ -941,6 +988,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
     __shared__ uint64_t bar_w[kMaxStages], bar_x[kMaxStages], bar_empty[kMaxStages], plan_ready;
     __shared__ int n_active_sh, abort_sh, last_sh;
     __shared__ double part[2][kWarps][kT];
+    __shared__ uint32_t top_sh[MT][NT][8];
     float4(*red)[MT][NT][32] = reinterpret_cast<float4(*)[MT][NT][32]>(smem + a.off_red);   // [warp]
     volatile int* abort_flag = &abort_sh;
     const Plan P{reinterpret_cast<Active*>(smem + a.off_active), reinterpret_cast<float*>(smem + a.off_pairw),
@@ -1038,17 +1086,12 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
         // ---------------------------------------------------------- activation producers
         const int feeder = warp - 2 * kWarps - 1;
         constexpr bool kLift = F::kInvBytes > 0;
-        auto fed = [&]() {
-            if (kLift)
-                bar_done(ring.x + 8 * ring.slot);
-            else
-                arrive_copied(ring.x + 8 * ring.slot);
-        };
-        auto factors = [&](int row, int cols) {     // of an activation row of the stage
-            return ring.stage() + ring.scales - F::kInvBytes + row * (cols / kSlice * 4);
+        int cols = 0, xs = 0, off = 0;     // of the unit's stages
+        bool lifting = kLift;      // the shared expert's tokens are lifted here
+        auto factors = [&](int row, int group) {     // of an activation row of the stage, `group` columns each
+            return ring.stage() + ring.scales - F::kInvBytes + row * (cols / group * 4);
         };
         uint32_t mask = 0;
-        int cols = 0, xs = 0, off = 0;     // of the unit's stages
         auto shape = [&](bool down, int count) {
             cols = chunk_cols(down, count);
             xs = x_stride<DT>(cols);
@@ -1060,13 +1103,18 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
                 uint32_t dst = ring.stage() + off;
                 int i = 0;
                 for (uint32_t m = mask; m; m &= m - 1, dst += xs, ++i) {
-                    const uint16_t* src = a.x + (size_t)(__ffs(m) - 1) * a.H + k0;
-                    if (kLift)
-                        lift_row<false>(dst, 0, src, nullptr, kn, factors(i, cols));
-                    else
-                        copy_row(dst, src, kn);
+                    const size_t tok = __ffs(m) - 1;
+                    if (lifting) {
+                        lift_row(dst, a.x + tok * a.H + k0, kn, factors(i, 64));
+                    } else {
+                        copy_row(dst, (kLift ? a.x16 : a.x) + tok * a.H + k0, kn);
+                        if (kLift) copy_factors(factors(i, 64), a.xinv + tok * (a.H / 64) + k0 / 64, kn / 64);
+                    }
                 }
-                fed();
+                if (lifting)
+                    bar_done(ring.x + 8 * ring.slot);
+                else
+                    arrive_copied(ring.x + 8 * ring.slot);
             }
             ring.next();
             return true;
@@ -1076,7 +1124,9 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
         shape(false, a.T);
         for (int u = s0; ok && u < s1; ++u) ok = walk_unit(a, a.T, stage_x);
         ok = ok && wait(plan_bar, 0);
+        lifting = false;
         if (ok) {
+            __threadfence();       // the lifted tokens are read after barrier 0 (plan_bar is behind it)
             for (int u = P.cut1[cta]; ok && u < P.cut1[cta + 1]; ++u) {
                 const Active& act = P.active[first_routed + u / upe];
                 mask = act.mask;
@@ -1099,12 +1149,15 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
             ok = ok && !__any_sync(0xffffffffu, late);
             __threadfence();
             const uint16_t *hi = nullptr, *lo = nullptr;
+            const float* inv = nullptr;
+            const int ld_inv = a.ld_act / NF;
             int count = 0;
             if (ok)
                 walk_down(a, P, n_active_sh, P.cut2[cta], P.cut2[cta + 1],
                           [&](int, const Active& act) {
                               hi = a.act_hi + (size_t)act.base * a.ld_act;
                               lo = a.act_lo + (size_t)act.base * a.ld_act;
+                              inv = a.ainv + (size_t)act.base * ld_inv;
                               count = act.count;
                               shape(true, count);
                               return true;
@@ -1116,14 +1169,12 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
                                   const uint16_t *h = hi + k0, *l = lo + k0;
                                   const uint32_t tail = (uint32_t)(count * xs);
                                   for (int i = 0; i < count; ++i, dst += xs, h += a.ld_act, l += a.ld_act) {
-                                      if (kLift) {
-                                          lift_row<true>(dst, tail, h, l, kn, factors(i, cols));
-                                      } else {
-                                          copy_row(dst, h, kn);
-                                          copy_row(dst + tail, l, kn);
-                                      }
+                                      copy_row(dst, h, kn);
+                                      copy_row(dst + tail, l, kn);
+                                      if (kLift)
+                                          copy_factors(factors(i, NF), inv + (size_t)i * ld_inv + k0 / NF, kn / NF);
                                   }
-                                  fed();
+                                  arrive_copied(ring.x + 8 * ring.slot);
                               }
                               ring.next();
                               return true;
@@ -1138,6 +1189,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
         bool ok = true, good = true;
         Scratch S;
         router_phase(a, team, kw, part[team]);
+        if (F::kInvBytes) lift_tokens(a, (2 * kWarps - 1 - warp) * G + cta, 2 * kWarps * G);
         __threadfence();
         if (team == 0) {
             bar_arrive(kBarLogits, kConsumers);
@@ -1318,20 +1370,55 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
             if (gather()) return false;
             if (const int r = reader(); r < MT * NT) {
                 const float4 s = reduced(r);
-                const int f = f0 + r / NT * 8 + g, c0 = r % NT * 8 + 2 * t;
+                const int m = r / NT, tile = r % NT, f = f0 + m * 8 + g;
                 const float gate[2] = {s.x, s.y}, up[2] = {s.z, s.w};
+                float v[2];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    if (c0 + j >= count) continue;
-                    const int pair = act.base + c0 + j;
-                    float v = gate[j] / (1.0f + expf(-gate[j])) * up[j];
-                    if (act.expert >= 0) v *= P.pairw[pair];
-                    // head and tail: together 16 significand bits
-                    const __nv_bfloat16 hi = __float2bfloat16_rn(v);
-                    const __nv_bfloat16 lo = __float2bfloat16_rn(v - __bfloat162float(hi));
-                    const size_t at = (size_t)pair * a.ld_act + f;
-                    a.act_hi[at] = *reinterpret_cast<const uint16_t*>(&hi);
-                    a.act_lo[at] = *reinterpret_cast<const uint16_t*>(&lo);
+                    const int c = 8 * tile + 2 * t + j;
+                    v[j] = gate[j] / (1.0f + expf(-gate[j])) * up[j];
+                    if (act.expert >= 0) v[j] *= P.pairw[act.base + (c < count ? c : 0)];
+                }
+                if constexpr (F::kInvBytes > 0) {
+                    // one factor for the unit's features: the readers of its
+                    // row tiles exchange their largest
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        uint32_t top = __float_as_uint(v[j]) & 0x7fffffffu;
+#pragma unroll
+                        for (int off = 4; off < 32; off <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
+                        if (g == 0) top_sh[m][tile][2 * t + j] = top;
+                    }
+                    bar_sync(kBarReaders, MT * NT * 32);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const int c = 8 * tile + 2 * t + j;
+                        if (c >= count) continue;
+                        uint32_t top = top_sh[0][tile][2 * t + j];
+#pragma unroll
+                        for (int q = 1; q < MT; ++q) top = max(top, top_sh[q][tile][2 * t + j]);
+                        const uint32_t lift = min(268u - (top >> 23), 253u);
+                        // head and tail: together 22 significand bits
+                        const float x = v[j] * __uint_as_float(lift << 23);
+                        const __half hi = __float2half_rn(x), lo = __float2half_rn(x - __half2float(hi));
+                        const size_t pair = act.base + c, at = pair * a.ld_act + f;
+                        a.act_hi[at] = __half_as_ushort(hi);
+                        a.act_lo[at] = __half_as_ushort(lo);
+                        if (m == 0 && g == 0)
+                            a.ainv[pair * (a.ld_act / NF) + f0 / NF] = __uint_as_float((254u - lift) << 23);
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const int c = 8 * tile + 2 * t + j;
+                        if (c >= count) continue;
+                        // head and tail: together 16 significand bits
+                        const __nv_bfloat16 hi = __float2bfloat16_rn(v[j]);
+                        const __nv_bfloat16 lo = __float2bfloat16_rn(v[j] - __bfloat162float(hi));
+                        const size_t at = (size_t)(act.base + c) * a.ld_act + f;
+                        a.act_hi[at] = __bfloat16_as_ushort(hi);
+                        a.act_lo[at] = __bfloat16_as_ushort(lo);
+                    }
                 }
             }
             return true;
@@ -1369,7 +1456,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
                     for (int j = 0; j < 2; ++j) {
                         const int c = FOLD ? (2 * t + j) & 3 : 8 * i + 2 * t + j;
                         col.own[i][j] = act.mask >> c & 1u;
-                        col.inv[i][j] = col.own[i][j] ? __popc(act.mask & ((1u << c) - 1u)) * (cols / kSlice * 4) : 0;
+                        col.inv[i][j] = col.own[i][j] ? __popc(act.mask & ((1u << c) - 1u)) * (cols / NF * 4) : 0;
                     }
                     col.on[i] = act.mask >> (8 * i) & 255u;
                 }
@@ -1452,7 +1539,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
 size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
 
 struct FewLayout {
-    size_t logits, hi, lo, join, joined, total;
+    size_t logits, hi, lo, x16, xinv, ainv, join, joined, total;
     int ld_act;
 };
 
@@ -1469,6 +1556,9 @@ FewLayout few_layout(const moe_config_t* c) {
     L.logits = take((size_t)c->T * c->E * 8);
     L.hi = take((size_t)c->T * (c->k + 1) * L.ld_act * 2);
     L.lo = take((size_t)c->T * (c->k + 1) * L.ld_act * 2);
+    L.x16 = take((size_t)c->T * c->H * 2);
+    L.xinv = take((size_t)c->T * (c->H / 64) * 4);
+    L.ainv = take((size_t)c->T * (c->k + 1) * (L.ld_act / 16) * 4);
     L.join = take((size_t)kMaxBlocks * 2 * c->T * 64 * 4);
     L.joined = take((size_t)c->H / 16 * 4);
     L.total = off;
@@ -1673,6 +1763,9 @@ moe_status_t moe_forward_few(const moe_config_t* cfg, const void* x, const void*
     a.logits = reinterpret_cast<double*>(base + L.logits);
     a.act_hi = reinterpret_cast<uint16_t*>(base + L.hi);
     a.act_lo = reinterpret_cast<uint16_t*>(base + L.lo);
+    a.x16 = reinterpret_cast<uint16_t*>(base + L.x16);
+    a.xinv = reinterpret_cast<float*>(base + L.xinv);
+    a.ainv = reinterpret_cast<float*>(base + L.ainv);
     a.join = reinterpret_cast<float*>(base + L.join);
     a.joined = reinterpret_cast<int*>(base + L.joined);
     a.T = cfg->T;
