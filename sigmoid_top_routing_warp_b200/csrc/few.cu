@@ -79,6 +79,7 @@ constexpr int kBarAll = 1, kBarB = 2, kBarRouted = 3, kBarA = 4, kBarLogits = 5,
 constexpr int kChunk = 1024;                     // K columns of a full stage
 constexpr int kBox = 256;                        // K columns of one tensor copy
 constexpr int kBoxBytes = 8192;                  // its bytes, for every weight type
+constexpr int kRowsX = 4;                        // activation rows of a full stage
 constexpr int kSlice = 64;                       // K columns of a warp in a stage
 constexpr int kMaxStages = 8;
 constexpr int kBarWord = moe::kSchedFirstWord;   // grid barriers (2) and the exit count, in the status block
@@ -538,11 +539,13 @@ struct Ring {
     __device__ __forceinline__ uint32_t stage() const { return base + slot * bytes; }
 };
 
-// Columns of a stage: above eight activation rows (heads and tails of every
-// pair in phase 2) there is room for half of them, above 16 for a quarter.
+// Columns of a stage: it has room for kRowsX activation rows (heads and tails
+// of every pair in phase 2) beside all of its weights; more rows take half of
+// the columns, above 16 a quarter.  Most experts have one or two tokens, and a
+// deeper ring is worth more than whole stages for the others.
 __device__ __forceinline__ int chunk_cols(bool down, int count) {
     const int rows = down ? 2 * count : count;
-    return rows <= 8 ? kChunk : rows <= 16 ? kChunk / 2 : kChunk / 4;
+    return rows <= kRowsX ? kChunk : rows <= 16 ? kChunk / 2 : kChunk / 4;
 }
 template <int DT>
 __device__ __forceinline__ int x_stride(int cols) {
@@ -1657,8 +1660,9 @@ moe_status_t few_smem(FewArgs& a, int limit, size_t* bytes) {
     constexpr int tiles = F::kRows / 16 * NT;
     off += red_warps(tiles) * tiles * 512;
     a.off_ring = up(off, 1024);
-    // eight activation rows of a full stage; fewer columns leave room for more
-    a.stage_bytes = up(kChunk / kBox * kBoxBytes + (a.T <= 4 ? 2 * a.T : 8) * (kChunk * 2 + F::kPad) + F::kInvBytes + F::kScaleBytes, 1024);
+    // fewer columns leave room for more activation rows than a full stage has
+    a.stage_bytes = up(kChunk / kBox * kBoxBytes + (a.T == 1 ? 2 : kRowsX) * (kChunk * 2 + F::kPad) + F::kInvBytes +
+                           F::kScaleBytes, 1024);
     const int stages = (limit - 1024 - a.off_ring) / a.stage_bytes;   // 1024: the boxes' alignment
     a.n_stages = stages < kMaxStages ? stages : kMaxStages;
     if (a.n_stages < 2)
