@@ -76,7 +76,7 @@ constexpr int kStaticSmem = 4096;                // the kernel's own variables (
 constexpr int kHeadStart = 2;                    // stages copied before barrier 0 has been passed
 constexpr int kWindow = 2;                       // stages under way while a barrier or the choice is waited for
 // named barriers
-constexpr int kBarAll = 1, kBarB = 2, kBarRouted = 3, kBarA = 4, kBarLogits = 5, kBarReaders = 6;
+constexpr int kBarAll = 1, kBarB = 2, kBarRouted = 3, kBarA = 4, kBarLogits = 5, kBarReaders = 6, kBarLift = 7, kBarTops = 8;
 constexpr int kChunk = 1024;                     // K columns of a full stage
 constexpr int kBox = 256;                        // K columns of one tensor copy
 constexpr int kBoxBytes = 8192;                  // its bytes, for every weight type
@@ -120,15 +120,15 @@ struct FewArgs {
     int* status;
     double* logits;             // [T][E]
     uint16_t *act_hi, *act_lo;  // [pairs][ld_act] weighted SwiGLU outputs, head and tail
-    uint16_t* x16;              // [T][H] lifted tokens, and what undoes their factors and
-    float *xinv, *ainv;         // the outputs': [T][H / 64], [pairs][ld_act / features of a unit]
+    uint16_t* x16;              // [T][H] lifted tokens
+    float* ainv;                // what undoes the outputs' factors: [pairs][ld_act / features of a unit]
     float* join;                // [blocks][2][T][rows] partial sums of shared row blocks
     int* joined;                // [row blocks] blocks that have left theirs
     int T, H, E, k, I, Is, n_group, topk_group, group_topn, norm, stall, ld_act, batch;
     float rsf;
     double inv_g;               // 1 / blocks
     // shared-memory layout (bytes)
-    int off_active, off_pairw, off_cuts, off_scratch, off_red, off_ring, stage_bytes, n_stages;
+    int off_active, off_pairw, off_pairx, off_cuts, off_scratch, off_red, off_ring, stage_bytes, n_stages;
 };
 
 // One touched expert: its tokens (bit mask), their number and its first
@@ -143,6 +143,7 @@ struct Active {
 struct Plan {
     Active* active;
     float* pairw;      // routing weight of a pair
+    float* pairx;      // what undoes its token's lift
     int *cut1, *cut2;  // [blocks + 1] shares of the routed units and of phase 2
     int* n_active;
 };
@@ -532,7 +533,8 @@ __device__ void build_plan(const FewArgs& a, const Plan& P, const Scratch& S, in
 }
 
 // Routing weights of the pairs (the producers need not wait for them).
-__device__ void pair_weights(const FewArgs& a, const Plan& P, const Scratch& S, int tid) {
+template <bool LIFT>
+__device__ void pair_weights(const FewArgs& a, const Plan& P, const Scratch& S, int tid, const uint32_t* lift) {
     for (int i = tid; i < a.T * a.k; i += kTeam) {
         const int t = i / a.k;
         double sum = 0.0;
@@ -540,7 +542,9 @@ __device__ void pair_weights(const FewArgs& a, const Plan& P, const Scratch& S, 
         const double v = a.norm ? S.sels[i] / sum : S.sels[i];
         const float w = (float)(v * (double)a.rsf);
         const Active act = P.active[S.apos[S.sel[i]]];
-        P.pairw[act.base + __popc(act.mask & ((1u << t) - 1u))] = w;
+        const int pair = act.base + __popc(act.mask & ((1u << t) - 1u));
+        P.pairw[pair] = w;
+        if (LIFT) P.pairx[pair] = __uint_as_float((254u - lift[t]) << 23);
         if (blockIdx.x == 0) {
             if (a.idx) a.idx[i] = S.sel[i];
             if (a.w) a.w[i] = w;
@@ -717,16 +721,15 @@ __device__ __forceinline__ void copy_row(uint32_t dst, const uint16_t* src, int 
     }
 }
 
-// Exponent field (biased) of the factor that takes the largest of 64 values,
-// eight in each of eight lanes, to 2^14 .. 2^15: an infinity or NaN counts as
+// Exponent field (biased) of the factor that takes a token's largest value to
+// 2^14 .. 2^15, from its bits without the sign: an infinity or NaN counts as
 // 2^128, and tiny ones are lifted by at most 2^126.
-__device__ __forceinline__ uint32_t block_lift(const uint4& v) {
-    uint32_t m = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
-                          __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
-#pragma unroll
-    for (int off = 1; off < 8; off <<= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, off));
-    const uint32_t e = max(m & 0xffffu, m >> 16) >> 7;
-    return min(268u - e, 253u);
+__device__ __forceinline__ uint32_t lift_of(uint32_t top) { return min(268u - (top >> 7), 253u); }
+// Largest of the values' bits (bf16, without the sign).
+__device__ __forceinline__ uint32_t top_of(const uint4& v) {
+    const uint32_t m = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
+                                __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+    return max(m & 0xffffu, m >> 16);
 }
 __device__ __forceinline__ uint32_t lifted(uint32_t w, float f) {
     const float lo = __uint_as_float(w << 16) * f, hi = __uint_as_float(w & 0xffff0000u) * f;
@@ -740,9 +743,8 @@ __device__ __forceinline__ void put_lifted(uint32_t dst, const uint4& v, float f
                  : "memory");
 }
 
-// A row of the shared expert's stage in binary16, lifted on the way; `inv`:
-// what undoes the factors, one value for 64 columns.
-__device__ __forceinline__ void lift_row(uint32_t dst, const uint16_t* src, int kn, uint32_t inv) {
+// A row of the shared expert's stage in binary16, lifted on the way by f.
+__device__ __forceinline__ void lift_row(uint32_t dst, const uint16_t* src, int kn, float f) {
     const int lane = threadIdx.x & 31;
     uint4 v[kChunk / 256];
 #pragma unroll
@@ -751,30 +753,33 @@ __device__ __forceinline__ void lift_row(uint32_t dst, const uint16_t* src, int 
         v[j] = c < kn ? __ldg(reinterpret_cast<const uint4*>(src + c)) : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
-    for (int j = 0; j < kChunk / 256; ++j) {
-        if (j * 256 >= kn) break;
-        const uint32_t lift = block_lift(v[j]);
-        if (lane * 8 + j * 256 >= kn) continue;
-        put_lifted(dst + lane * 16 + j * 512, v[j], __uint_as_float(lift << 23));
-        if ((lane & 7) == 0)
-            asm volatile("st.shared.u32 [%0], %1;" ::"r"(inv + (j * 4 + (lane >> 3)) * 4), "r"((254u - lift) << 23)
-                         : "memory");
+    for (int j = 0; j < kChunk / 256; ++j)
+        if (lane * 8 + j * 256 < kn) put_lifted(dst + lane * 16 + j * 512, v[j], f);
+}
+
+// The tokens' largest values, by the kFeeders warps: part[warp][token].
+__device__ void token_tops(const FewArgs& a, int feeder, uint32_t (*part)[kT]) {
+    const int lane = threadIdx.x & 31;
+    for (int t = 0; t < a.T; ++t) {
+        const uint4* x = reinterpret_cast<const uint4*>(a.x + (size_t)t * a.H);
+        uint32_t top = 0;
+#pragma unroll 8
+        for (int c = feeder * 32 + lane; c < a.H / 8; c += kFeeders * 32) top = max(top, top_of(__ldg(x + c)));
+        top = __reduce_max_sync(0xffffffffu, top);
+        if (lane == 0) part[feeder][t] = top;
     }
 }
 
 // Phase R: the tokens lifted into the workspace, a warp for 256 columns of one.
-__device__ void lift_tokens(const FewArgs& a, int id, int n) {
+__device__ void lift_tokens(const FewArgs& a, int id, int n, const uint32_t* lift) {
     const int lane = threadIdx.x & 31, per = (a.H + 255) / 256;
     for (int u = id; u < a.T * per; u += n) {
         const int t = u / per, c = u % per * 256 + lane * 8;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (c < a.H) v = __ldg(reinterpret_cast<const uint4*>(a.x + (size_t)t * a.H + c));
-        const uint32_t lift = block_lift(v);
-        const float f = __uint_as_float(lift << 23);
         if (c >= a.H) continue;
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(a.x + (size_t)t * a.H + c));
+        const float f = __uint_as_float(lift[t] << 23);
         *reinterpret_cast<uint4*>(a.x16 + (size_t)t * a.H + c) =
             make_uint4(lifted(v.x, f), lifted(v.y, f), lifted(v.z, f), lifted(v.w, f));
-        if ((lane & 7) == 0) a.xinv[(size_t)t * (a.H / 64) + c / 64] = __uint_as_float((254u - lift) << 23);
     }
 }
 
@@ -915,22 +920,24 @@ __device__ __forceinline__ void mma_tile(uint32_t stage, uint32_t sc, int slice,
         }
     } else {
         constexpr bool kFp8 = DT == MOE_DTYPE_FP8_E4M3_BLOCK128;
-        // Sums with one factor: phase 1's are the slice's; phase 2's are a
-        // unit's features, 16 (an MMA) or 32 (two).  An e2m1 scale is for 32.
-        constexpr int CH = kFp8 ? (DOWN ? 4 : 1) : 2;
-        float back[DOWN ? CH : 1][2];   // undo the lift of the lane's two result columns
-        const uint32_t inv = sc - F::kInvBytes;
+        // Chains of sums with one factor: a token's lift is undone in the
+        // epilogue; phase 2 has a factor for a unit's features, 16 (an MMA) or
+        // 32 (two), and an e2m1 scale is for 32.
+        constexpr int CH = !kFp8 ? 2 : DOWN ? 4 : 1;
+        float back[CH][2];              // phase 2: undo the lift of the lane's two result columns
+        if (DOWN) {
+            const uint32_t inv = sc - F::kInvBytes;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            if constexpr (!DOWN) {
-                back[0][j] = __uint_as_float(lds32(inv + col.inv[nt][j] + slice * 4));
-            } else if constexpr (kFp8) {
-                const uint4 v = lds128(inv + col.inv[nt][j] + slice * 16);
-                back[0][j] = __uint_as_float(v.x), back[1][j] = __uint_as_float(v.y);
-                back[2][j] = __uint_as_float(v.z), back[3][j] = __uint_as_float(v.w);
-            } else {
-                const uint2 v = lds64(inv + col.inv[nt][j] + slice * 8);
-                back[0][j] = __uint_as_float(v.x), back[1][j] = __uint_as_float(v.y);
+            for (int j = 0; j < 2; ++j) {
+                if (kFp8) {
+                    const uint4 v = lds128(inv + col.inv[nt][j] + slice * 16);
+                    const uint32_t f[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int q = 0; q < CH; ++q) back[q][j] = __uint_as_float(f[q]);
+                } else {
+                    const uint2 v = lds64(inv + col.inv[nt][j] + slice * 8);
+                    back[0][j] = __uint_as_float(v.x), back[1][j] = __uint_as_float(v.y);
+                }
             }
         }
         float s0 = 0.0f, s1 = 0.0f;
@@ -942,7 +949,7 @@ __device__ __forceinline__ void mma_tile(uint32_t stage, uint32_t sc, int slice,
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
             const uint32_t w0 = w + (2 * mt) * PB * 1024, w1 = w0 + PB * 1024;
-            float c[4][4];
+            float c[CH][4];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 uint32_t m[2][4];
@@ -959,12 +966,11 @@ __device__ __forceinline__ void mma_tile(uint32_t stage, uint32_t sc, int slice,
                     m[0][0] = p[0], m[0][1] = q[0], m[0][2] = p[1], m[0][3] = q[1];
                     m[1][0] = p[2], m[1][1] = q[2], m[1][2] = p[3], m[1][3] = q[3];
                 }
-                // independent chains where the factors allow them
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    constexpr bool kOwn = kFp8;           // a chain for each MMA, or for each half
-                    float(&d)[4] = c[kOwn ? 2 * h + i : h];
-                    if (kOwn || i == 0)
+                    constexpr int kLong = 4 / CH;         // MMAs of a chain
+                    float(&d)[4] = c[(2 * h + i) / kLong];
+                    if ((2 * h + i) % kLong == 0)
                         mma16<false>(d, m[i], b[4 * h + 2 * i], b[4 * h + 2 * i + 1], zero);
                     else
                         mma16<false>(d, m[i], b[4 * h + 2 * i], b[4 * h + 2 * i + 1], d);
@@ -979,21 +985,19 @@ __device__ __forceinline__ void mma_tile(uint32_t stage, uint32_t sc, int slice,
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                float v;
-                if constexpr (kFp8 && DOWN) {
-                    v = c[0][j] * back[0][j & 1];
-#pragma unroll
-                    for (int q = 1; q < 4; ++q) v = fmaf(c[q][j], back[q][j & 1], v);
-                    v *= s[0][j >> 1];
-                } else if constexpr (kFp8) {
-                    v = ((c[0][j] + c[1][j]) + (c[2][j] + c[3][j])) * s[0][j >> 1] * back[0][j & 1];
-                } else if constexpr (DOWN) {
-                    v = fmaf(c[0][j] * back[0][j & 1], s[0][j >> 1], c[1][j] * back[1][j & 1] * s[1][j >> 1]);
-                } else {
-                    v = fmaf(c[0][j], s[0][j >> 1], c[1][j] * s[1][j >> 1]) * back[0][j & 1];
-                }
                 // an infinity or a NaN among the weights reaches the expert's own tokens only
-                sum.acc[mt][nt][j] += !DOWN || col.own[nt][j & 1] ? v : 0.0f;
+                float v = sum.acc[mt][nt][j];
+                if constexpr (kFp8 && DOWN) {
+                    float u = c[0][j] * back[0][j & 1];
+#pragma unroll
+                    for (int q = 1; q < CH; ++q) u = fmaf(c[q][j], back[q][j & 1], u);
+                    v = fmaf(u, s[0][j >> 1], v);
+                } else {
+#pragma unroll
+                    for (int q = 0; q < CH; ++q)
+                        v = fmaf(DOWN ? c[q][j] * back[q][j & 1] : c[q][j], s[q][j >> 1], v);
+                }
+                if (!DOWN || col.own[nt][j & 1]) sum.acc[mt][nt][j] = v;
             }
         }
     }
@@ -1021,9 +1025,11 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
     __shared__ int n_active_sh, abort_sh, last_sh;
     __shared__ double part[2][kWarps][kT];
     __shared__ uint32_t top_sh[MT][NT][8];
+    __shared__ uint32_t x_top[kFeeders][kT], lift_sh[kT];   // of the tokens: largest values, factors
     float4(*red)[MT][NT][32] = reinterpret_cast<float4(*)[MT][NT][32]>(smem + a.off_red);   // [warp]
     volatile int* abort_flag = &abort_sh;
     const Plan P{reinterpret_cast<Active*>(smem + a.off_active), reinterpret_cast<float*>(smem + a.off_pairw),
+                 reinterpret_cast<float*>(smem + a.off_pairx),
                  reinterpret_cast<int*>(smem + a.off_cuts), reinterpret_cast<int*>(smem + a.off_cuts) + kMaxBlocks + 1,
                  &n_active_sh};
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1120,8 +1126,8 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
         constexpr bool kLift = F::kInvBytes > 0;
         int cols = 0, xs = 0, off = 0;     // of the unit's stages
         bool lifting = kLift;      // the shared expert's tokens are lifted here
-        auto factors = [&](int row, int group) {     // of an activation row of the stage, `group` columns each
-            return ring.stage() + ring.scales - F::kInvBytes + row * (cols / group * 4);
+        auto factors = [&](int row) {     // of a pair's heads and tails in phase 2, one for a unit's features
+            return ring.stage() + ring.scales - F::kInvBytes + row * (cols / NF * 4);
         };
         uint32_t mask = 0;
         auto shape = [&](bool down, int count) {
@@ -1133,15 +1139,12 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
             if (ring.feeder() == feeder) {
                 if (!wait(ring.empty + 8 * ring.slot, ring.phase ^ 1)) return false;
                 uint32_t dst = ring.stage() + off;
-                int i = 0;
-                for (uint32_t m = mask; m; m &= m - 1, dst += xs, ++i) {
+                for (uint32_t m = mask; m; m &= m - 1, dst += xs) {
                     const size_t tok = __ffs(m) - 1;
-                    if (lifting) {
-                        lift_row(dst, a.x + tok * a.H + k0, kn, factors(i, 64));
-                    } else {
+                    if (lifting)
+                        lift_row(dst, a.x + tok * a.H + k0, kn, __uint_as_float(lift_sh[tok] << 23));
+                    else
                         copy_row(dst, (kLift ? a.x16 : a.x) + tok * a.H + k0, kn);
-                        if (kLift) copy_factors(factors(i, 64), a.xinv + tok * (a.H / 64) + k0 / 64, kn / 64);
-                    }
                 }
                 if (lifting)
                     bar_done(ring.x + 8 * ring.slot);
@@ -1152,6 +1155,18 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
             return true;
         };
         bool ok = true;
+        if (kLift) {
+            token_tops(a, feeder, x_top);
+            bar_sync(kBarTops, kFeeders * 32);
+            if (lane < a.T && feeder == 0) {
+                uint32_t top = x_top[0][lane];
+#pragma unroll
+                for (int i = 1; i < kFeeders; ++i) top = max(top, x_top[i][lane]);
+                lift_sh[lane] = lift_of(top);
+            }
+            bar_sync(kBarTops, kFeeders * 32);
+            bar_arrive(kBarLift, kFeeders * 32 + kConsumers);
+        }
         mask = shared.mask;
         shape(false, a.T);
         for (int u = s0; ok && u < s1; ++u) ok = walk_unit(a, a.T, stage_x);
@@ -1204,7 +1219,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
                                       copy_row(dst, h, kn);
                                       copy_row(dst + tail, l, kn);
                                       if (kLift)
-                                          copy_factors(factors(i, NF), inv + (size_t)i * ld_inv + k0 / NF, kn / NF);
+                                          copy_factors(factors(i), inv + (size_t)i * ld_inv + k0 / NF, kn / NF);
                                   }
                                   arrive_copied(ring.x + 8 * ring.slot);
                               }
@@ -1221,7 +1236,10 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
         bool ok = true, good = true;
         Scratch S;
         router_phase(a, team, kw, part[team]);
-        if (F::kInvBytes) lift_tokens(a, (2 * kWarps - 1 - warp) * G + cta, 2 * kWarps * G);
+        if (F::kInvBytes) {
+            bar_sync(kBarLift, kFeeders * 32 + kConsumers);
+            lift_tokens(a, (2 * kWarps - 1 - warp) * G + cta, 2 * kWarps * G, lift_sh);
+        }
         __threadfence();
         if (team == 0) {
             bar_arrive(kBarLogits, kConsumers);
@@ -1391,11 +1409,6 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
             for (int i = 0; i < NT; ++i) {
                 col.x[i] = off_x(cols) + (8 * i + g < count ? 8 * i + g : 0) * x_stride<DT>(cols);
                 col.on[i] = count > 8 * i;
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int c = 8 * i + 2 * t + j;
-                    col.inv[i][j] = (c < count ? c : 0) * (cols / kSlice * 4);
-                }
             }
             walk_unit(a, count, [&](int, int kn) { return step(std::false_type{}, kn); });
             sum.fold(col, true);
@@ -1403,11 +1416,16 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
             if (const int r = reader(); r < MT * NT) {
                 const float4 s = reduced(r);
                 const int m = r / NT, tile = r % NT, f = f0 + m * 8 + g;
-                const float gate[2] = {s.x, s.y}, up[2] = {s.z, s.w};
+                float gate[2] = {s.x, s.y}, up[2] = {s.z, s.w};
                 float v[2];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     const int c = 8 * tile + 2 * t + j;
+                    if (F::kInvBytes) {
+                        const float back = act.expert < 0 ? __uint_as_float((254u - lift_sh[c < count ? c : 0]) << 23)
+                                                          : P.pairx[act.base + (c < count ? c : 0)];
+                        gate[j] *= back, up[j] *= back;
+                    }
                     v[j] = gate[j] / (1.0f + expf(-gate[j])) * up[j];
                     if (act.expert >= 0) v[j] *= P.pairw[act.base + (c < count ? c : 0)];
                 }
@@ -1462,7 +1480,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
         good = !group_any(kBarAll, !(good && ok));
         both = true;
         shift = 0;
-        if (good && team) pair_weights(a, P, S, tid - kTeam);   // read behind gather's barriers
+        if (good && team) pair_weights<(F::kInvBytes > 0)>(a, P, S, tid - kTeam, lift_sh);   // read behind gather's barriers
         if (good)
             for (int u = P.cut1[cta]; good && u < P.cut1[cta + 1]; ++u)
                 good = gate_up(P.active[first_routed + u / upe], (u % upe) * NF);
@@ -1571,7 +1589,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
 size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
 
 struct FewLayout {
-    size_t logits, hi, lo, x16, xinv, ainv, join, joined, total;
+    size_t logits, hi, lo, x16, ainv, join, joined, total;
     int ld_act;
 };
 
@@ -1589,7 +1607,6 @@ FewLayout few_layout(const moe_config_t* c) {
     L.hi = take((size_t)c->T * (c->k + 1) * L.ld_act * 2);
     L.lo = take((size_t)c->T * (c->k + 1) * L.ld_act * 2);
     L.x16 = take((size_t)c->T * c->H * 2);
-    L.xinv = take((size_t)c->T * (c->H / 64) * 4);
     L.ainv = take((size_t)c->T * (c->k + 1) * (L.ld_act / 16) * 4);
     L.join = take((size_t)kMaxBlocks * 2 * c->T * 64 * 4);
     L.joined = take((size_t)c->H / 16 * 4);
@@ -1678,6 +1695,8 @@ moe_status_t few_smem(FewArgs& a, int limit, size_t* bytes) {
     off += active * (int)sizeof(Active);
     a.off_pairw = off;
     off += (n + a.T) * 4;
+    a.off_pairx = off;
+    if (F::kInvBytes) off += (n + a.T) * 4;
     a.off_cuts = off;
     off = up(off + 2 * (kMaxBlocks + 1) * 4, 16);
     a.off_scratch = off;
@@ -1797,7 +1816,6 @@ moe_status_t moe_forward_few(const moe_config_t* cfg, const void* x, const void*
     a.act_hi = reinterpret_cast<uint16_t*>(base + L.hi);
     a.act_lo = reinterpret_cast<uint16_t*>(base + L.lo);
     a.x16 = reinterpret_cast<uint16_t*>(base + L.x16);
-    a.xinv = reinterpret_cast<float*>(base + L.xinv);
     a.ainv = reinterpret_cast<float*>(base + L.ainv);
     a.join = reinterpret_cast<float*>(base + L.join);
     a.joined = reinterpret_cast<int*>(base + L.joined);
