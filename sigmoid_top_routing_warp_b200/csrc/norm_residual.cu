@@ -108,6 +108,11 @@ __device__ __forceinline__ float inv_norm(float ss, int H, float eps) {
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool ok) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
 }
+// The column sums are launched as a programmatic dependent: their blocks come
+// up while the rows are still worked on, and wait here for the end of that
+// kernel, whose writes they then see.
+__device__ __forceinline__ void let_dependents_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void after_primary() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void copies_close() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // waits until at most N of the closed groups are still under way
 template <int N>
@@ -260,6 +265,7 @@ __global__ void __launch_bounds__(THREADS, 1280 / THREADS) norm_residual_kernel(
 // (times gamma_post); with a gate per token it is sum(D g yn).
 template <int NV, bool TOKEN>
 __global__ void __launch_bounds__(kNrBwdThreads) norm_residual_bwd_kernel(const NrArgs p) {
+    let_dependents_launch();
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float sh[2][3 * 32];
     constexpr int NT = TOKEN ? 5 : 4;                 // tensors of a row: y, h, dh_out, du, gate
@@ -387,6 +393,7 @@ __global__ void __launch_bounds__(kNrBwdThreads) norm_residual_bwd_kernel(const 
 // row, the second one from L1 and L2, and the column sums in shared memory
 // [2][H], each thread at its own columns.
 __global__ void __launch_bounds__(kNrWideThreads) norm_residual_bwd_wide_kernel(const NrArgs p) {
+    let_dependents_launch();
     extern __shared__ float col[];
     __shared__ float sh[2][3 * 32];
     const int nvec = p.H / 8;
@@ -457,6 +464,7 @@ __global__ void __launch_bounds__(256) norm_residual_cols_kernel(const NrArgs p)
     __shared__ double sh[8][33];
     const int which = blockIdx.y;
     const int col = blockIdx.x * 32 + (threadIdx.x & 31), w = threadIdx.x >> 5;
+    after_primary();
     double s = 0.0;
     if (col < p.H) {
 #pragma unroll 8
@@ -709,8 +717,18 @@ moe_status_t moe_norm_residual_backward(const moe_config_t* cfg, const void* h, 
         NR_TRY(launched("norm_residual backward launch: %s"));
     }
     // with no rows the sums are zero
-    norm_residual_cols_kernel<<<dim3((p.H + 31) / 32, dgamma_pre ? 2 : 1), 256, 0, s>>>(p);
-    return launched("norm_residual column-sum launch: %s");
+    cudaLaunchConfig_t cols = {};
+    cols.gridDim = dim3((p.H + 31) / 32, dgamma_pre ? 2 : 1);
+    cols.blockDim = dim3(256);
+    cols.stream = s;
+    cudaLaunchAttribute early = {};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cols.attrs = &early;
+    cols.numAttrs = p.T > 0 ? 1 : 0;
+    const cudaError_t e = cudaLaunchKernelEx(&cols, norm_residual_cols_kernel, p);
+    if (e != cudaSuccess) return nfail(MOE_ERR_CUDA, "norm_residual column-sum launch: %s", cudaGetErrorString(e));
+    return MOE_OK;
 }
 
 }  // extern "C"
