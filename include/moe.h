@@ -240,8 +240,8 @@ moe_status_t moe_quantize_act(const void* x, int32_t rows, int32_t cols, uint8_t
  *   scale uint8 [rows, cols/32]
  * moe_dequantize_mx writes the bf16 values code * 2^(s - 127), which are
  * exact for every scale moe_quantize_mx produces (a scale byte of 253 or 254
- * can overflow to infinity; 255 gives NaN).  x and q 16-byte aligned; no
- * workspace; rows or cols of 0 launch nothing.                            */
+ * can overflow to infinity; 255 gives NaN).  x and q 16-byte aligned, no
+ * buffer overlaps another; no workspace; rows or cols of 0 launch nothing.  */
 moe_status_t moe_quantize_mx(const void* x, int32_t rows, int32_t cols, uint8_t* q, uint8_t* scale,
                              moe_stream_t stream);
 moe_status_t moe_dequantize_mx(const uint8_t* q, const uint8_t* scale, int32_t rows, int32_t cols,
@@ -308,15 +308,20 @@ moe_status_t moe_forward_block(const moe_config_t* cfg, const void* h, const voi
  *   - nothing is rounded between the steps: logits, scores, the choice and the
  *     routing weights are computed in binary64 (topk_w is rounded to fp32
  *     once; equal keys take the lower expert, NaN keys rank below numbers),
- *     the SwiGLU outputs are carried with 16 significand bits, every sum is
- *     fp32, and out is rounded once.  Where two keys lie within fp32 rounding
- *     of each other moe_route may choose differently.
+ *     the SwiGLU outputs are carried with 16 significand bits (22 with 8- and
+ *     4-bit weights), every sum is fp32, and out is rounded once.  Where two
+ *     keys lie within fp32 rounding of each other moe_route may choose
+ *     differently;
+ *   - with 8- and 4-bit weights a token is multiplied as binary16 scaled by a
+ *     power of two of its own: a value below 2^-28 of the token's largest is
+ *     off by up to 2^-39 of the largest.
  * Arguments as moe_forward, except:
  *   *_scale   fp32 block scales (FP8), uint8 e8m0 scales (MXFP4: w13_scale
  *             [E, 2I, H/32], w2_scale [E, H, I/32], w13s_scale [2Is, H/32],
  *             w2s_scale [H, Is/32]), NULL for bf16; MXFP4 codes are
  *             [E, 2I, H/2], [E, H, I/2], [2Is, H/2], [H, Is/2] bytes.  Weight
  *             and MXFP4 scale pointers 16-byte aligned
+ *   out       bf16 [T, H] out (may be x itself)
  *   topk_idx  int32 [T, k] out, or NULL    the choice, slot order
  *   topk_w    fp32 [T, k] out, or NULL     its routing weights
  *   ws        moe_few_workspace_size bytes, 256-byte aligned, zero-filled

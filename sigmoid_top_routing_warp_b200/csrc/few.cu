@@ -80,7 +80,6 @@ constexpr int kBarAll = 1, kBarB = 2, kBarRouted = 3, kBarA = 4, kBarLogits = 5,
 constexpr int kChunk = 1024;                     // K columns of a full stage
 constexpr int kBox = 256;                        // K columns of one tensor copy
 constexpr int kBoxBytes = 8192;                  // its bytes, for every weight type
-constexpr int kRowsX = 4;                        // activation rows of a full stage
 constexpr int kSlice = 64;                       // K columns of a warp in a stage
 constexpr int kMaxStages = 8;
 constexpr int kBarWord = moe::kSchedFirstWord;   // grid barriers (2) and the exit count, in the status block
@@ -129,6 +128,7 @@ struct FewArgs {
     double inv_g;               // 1 / blocks
     // shared-memory layout (bytes)
     int off_active, off_pairw, off_pairx, off_cuts, off_scratch, off_red, off_ring, stage_bytes, n_stages;
+    int rows_full;              // activation rows of a full stage
 };
 
 // One touched expert: its tokens (bit mask), their number and its first
@@ -572,13 +572,12 @@ struct Ring {
     __device__ __forceinline__ uint32_t stage() const { return base + slot * bytes; }
 };
 
-// Columns of a stage: it has room for kRowsX activation rows (heads and tails
-// of every pair in phase 2) beside all of its weights; more rows take half of
-// the columns, above 16 a quarter.  Most experts have one or two tokens, and a
-// deeper ring is worth more than whole stages for the others.
-__device__ __forceinline__ int chunk_cols(bool down, int count) {
+// Columns of a stage: it has room for rows_full activation rows (heads and
+// tails of every pair in phase 2) beside all of its weights; more rows take
+// half of the columns, above 16 a quarter.
+__device__ __forceinline__ int chunk_cols(const FewArgs& a, bool down, int count) {
     const int rows = down ? 2 * count : count;
-    return rows <= kRowsX ? kChunk : rows <= 16 ? kChunk / 2 : kChunk / 4;
+    return rows <= a.rows_full ? kChunk : rows <= 16 ? kChunk / 2 : kChunk / 4;
 }
 template <int DT>
 __device__ __forceinline__ int x_stride(int cols) {
@@ -591,13 +590,13 @@ __device__ __forceinline__ int off_x(int cols) { return cols / kBox * kBoxBytes;
 // The stages of phase 1's unit with `count` tokens: stage(k0, kn).
 template <class Stage>
 __device__ __forceinline__ bool walk_unit(const FewArgs& a, int count, Stage stage) {
-    const int cols = chunk_cols(false, count);
+    const int cols = chunk_cols(a, false, count);
     for (int k0 = 0; k0 < a.H; k0 += cols)
         if (!stage(k0, min(cols, a.H - k0))) return false;
     return true;
 }
 __device__ __forceinline__ int unit_stages(const FewArgs& a, int count) {
-    const int cols = chunk_cols(false, count);
+    const int cols = chunk_cols(a, false, count);
     return (a.H + cols - 1) / cols;
 }
 
@@ -618,7 +617,7 @@ __device__ __forceinline__ bool walk_down(const FewArgs& a, const Plan& P, int n
     int pos = begin;
     while (true) {
         const Active act = P.active[p];
-        const int steps = act.expert < 0 ? ws : wi, most = chunk_cols(true, act.count) / 128;
+        const int steps = act.expert < 0 ? ws : wi, most = chunk_cols(a, true, act.count) / 128;
         if (!item(rb, act)) return false;
         while (off < steps && pos < end) {
             const int n = min(most, min(steps - off, end - pos));
@@ -1131,7 +1130,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
         };
         uint32_t mask = 0;
         auto shape = [&](bool down, int count) {
-            cols = chunk_cols(down, count);
+            cols = chunk_cols(a, down, count);
             xs = x_stride<DT>(cols);
             off = off_x(cols);
         };
@@ -1404,7 +1403,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
         };
         auto gate_up = [&](const Active& act, int f0) {
             sum.clear();
-            const int count = act.count, cols = chunk_cols(false, count);
+            const int count = act.count, cols = chunk_cols(a, false, count);
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
                 col.x[i] = off_x(cols) + (8 * i + g < count ? 8 * i + g : 0) * x_stride<DT>(cols);
@@ -1494,7 +1493,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
             sum.clear();
             auto item = [&](int, const Active& act) {
                 sum.fold(col, false);   // the last expert's
-                const int cols = chunk_cols(true, act.count), xs = x_stride<DT>(cols);
+                const int cols = chunk_cols(a, true, act.count), xs = x_stride<DT>(cols);
                 col.tail = act.count * xs;
 #pragma unroll
                 for (int i = 0; i < NT; ++i) {
@@ -1708,11 +1707,20 @@ moe_status_t few_smem(FewArgs& a, int limit, size_t* bytes) {
     constexpr int tiles = F::kRows / 16 * NT;
     off += red_warps(tiles) * tiles * 512;
     a.off_ring = up(off, 1024);
-    // fewer columns leave room for more activation rows than a full stage has
-    a.stage_bytes = up(kChunk / kBox * kBoxBytes + (a.T == 1 ? 2 : kRowsX) * (kChunk * 2 + F::kPad) + F::kInvBytes +
-                           F::kScaleBytes, 1024);
-    const int stages = (limit - 1024 - a.off_ring) / a.stage_bytes;   // 1024: the boxes' alignment
+    // As many stages as there is room for with four activation rows in a full
+    // one (most experts have one or two tokens), then as many rows, up to
+    // eight, as these stages have room for.  (16 tokens, bf16: three stages of
+    // eight rows took 690 us, four of four 663; where the tokens crowd onto few
+    // experts, more rows than a full stage holds cost half stages.)
+    auto bytes_of = [&](int rows) {
+        return up(kChunk / kBox * kBoxBytes + rows * (kChunk * 2 + F::kPad) + F::kInvBytes + F::kScaleBytes, 1024);
+    };
+    const int room = limit - 1024 - a.off_ring, all = a.T < 4 ? 2 * a.T : 8;   // 1024: the boxes' alignment
+    a.rows_full = all < 4 ? all : 4;
+    const int stages = room / bytes_of(a.rows_full);
     a.n_stages = stages < kMaxStages ? stages : kMaxStages;
+    while (a.rows_full < all && a.n_stages * bytes_of(a.rows_full + 1) <= room) ++a.rows_full;
+    a.stage_bytes = bytes_of(a.rows_full);
     if (a.n_stages < 2)
         return ffail(MOE_ERR_UNSUPPORTED, "%s: %lld bytes of shared memory hold too few stages", "few-token layer",
                      limit);
@@ -1775,6 +1783,11 @@ moe_status_t moe_forward_few(const moe_config_t* cfg, const void* x, const void*
     FEW_TRY(need(w13, "w13", 16));
     FEW_TRY(need(w2, "w2", 16));
     FEW_TRY(need(out, "out", 16));
+    // out is written when every block has read its tokens
+    const uintptr_t xp = reinterpret_cast<uintptr_t>(x), op = reinterpret_cast<uintptr_t>(out);
+    const size_t bytes = (size_t)cfg->T * cfg->H * 2;
+    if (xp != op && xp < op + bytes && op < xp + bytes)
+        return moe::api_fail(MOE_ERR_INVALID_ARG, "out must be x or not overlap it");
     if (topk_idx) FEW_TRY(need(topk_idx, "topk_idx", 4));
     if (topk_w) FEW_TRY(need(topk_w, "topk_w", 4));
     const bool shared = cfg->n_shared > 0;

@@ -80,6 +80,9 @@ def test_few_refuses_scales_and_small_workspaces(B):
             assert few(B, q, **bad) == B.MOE_ERR_INVALID_ARG and "scale" in B.get_last_error()
             bad[name] = 18
             assert few(B, q, **bad) == B.MOE_ERR_INVALID_ARG and "aligned" in B.get_last_error()
+    # out over x is allowed, over a part of it refused
+    assert few(B, c, x=4096, out=4096 + 16) == B.MOE_ERR_INVALID_ARG and "overlap" in B.get_last_error()
+    assert few(B, c, x=4096 + 32, out=4096) == B.MOE_ERR_INVALID_ARG and "overlap" in B.get_last_error()
     # no tokens: nothing to do, nothing is looked at
     assert few(B, cfg(B, T=0), ws_bytes=0, x=None, out=None, ws=None) == B.MOE_OK
 

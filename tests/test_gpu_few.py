@@ -235,6 +235,51 @@ def test_optional_outputs_and_dirty_workspace_contents(B):
     assert torch.equal(p["out"], first)
 
 
+@pytest.mark.parametrize("kind,T", [("bf16", 3), ("bf16", 12), ("fp8", 2), ("mxfp4", 7)])
+def test_out_over_x(B, kind, T):
+    """The same bits when out is x itself."""
+    p = make(B, kind, T, 512, 64, 4, 256, seed=29)
+    call(B, p)
+    apart = p["out"].clone()
+    call(B, p, out=p["x"])
+    torch.cuda.synchronize()
+    assert torch.equal(p["x"], apart)
+
+
+@pytest.mark.parametrize("kind", ("fp8", "mxfp4"))
+def test_one_value_far_above_the_others(B, kind):
+    """A token whose largest value is 2^20 times the others keeps the others' bits: the lift is for the
+    whole token, and what it drops is below 2^-39 of the largest, 2^-19 of the others.  Columns where the
+    large value meets a zero weight show it."""
+    p = make(B, kind, 2, 256, 32, 2, 128, n_shared=0, seed=31)
+    p["w_router"].zero_()
+    big = 8
+    p["x"][0, big] = 2.0 ** 20
+    pack = 2 if kind == "mxfp4" else 1
+    p["w13"][0][:, :, big // pack] = 0         # (its neighbour's codes too, for MXFP4)
+    vals = p["w13"][2]
+    vals[:, :, big] = 0
+    if pack == 2:
+        vals[:, :, big + 1] = 0
+    call(B, p)
+    torch.cuda.synchronize()
+    out, tol, idx, _ = reference(p)
+    assert torch.equal(p["idx"].cpu(), idx)
+    # the token's values are off by half a binary16 step below 2^-14 of the lift, 2^-39 of the
+    # largest: less than 2^-9 (half a bf16 step) of a value of 2^-10 or more; the sums of 256
+    # terms by 2^-39 * 2^20 * sum |w|, which the SwiGLU and the down projection carry on
+    e = 2.0 ** -19
+    for t in range(2):
+        extra = torch.zeros_like(out[t])
+        for j in range(2):
+            w13, w2 = vals[int(idx[t, j])], p["w2"][2][int(idx[t, j])]
+            g, u = (p["x"][t].cpu().double() @ w13.T).split(128)
+            dg, du = (e * w13.abs().sum(1)).split(128)
+            extra += (w2.abs() @ (1.1 * dg * (u.abs() + du) + g.abs() * du))
+        err = (p["out"][t].cpu().double() - out[t]).abs()
+        assert bool((err <= tol[t] + 2 * extra).all()), float((err / (tol[t] + 2 * extra)).max())
+
+
 def test_stalled_block_times_out_and_the_next_call_is_clean(B):
     p = make(B, "bf16", 1, 256, 32, 2, 128, seed=23)
     call(B, p)

@@ -101,3 +101,20 @@ def test_graph_and_stream(B):
     B.moe_quantize_mx(x, q, s, stream=side)
     side.synchronize()
     assert torch.equal(q.cpu(), rq)
+
+
+def test_offsets_beyond_32_bits(B):
+    """2^31 elements and more: the last rows are right."""
+    R, C, last = 262200, 8192, 3
+    x = torch.zeros((R, C), dtype=torch.bfloat16, device="cuda")
+    x[-last:] = torch.randn((last, C), device="cuda").to(torch.bfloat16)
+    q = torch.empty((R, C // 2), dtype=torch.uint8, device="cuda")
+    s = torch.empty((R, C // 32), dtype=torch.uint8, device="cuda")
+    B.moe_quantize_mx(x, q, s)
+    rq, rs = F.mx_quantize(x[-last:].cpu())
+    assert torch.equal(q[-last:].cpu(), rq) and torch.equal(s[-last:].cpu(), rs)
+    assert not bool(q[:-last].any()) and bool((s[:-last] == 127).all())
+    x.fill_(1.0)
+    B.moe_dequantize_mx(q, s, x)
+    torch.cuda.synchronize()
+    assert torch.equal(x[-last:].cpu().double(), F.mx_values(rq, rs)) and not bool(x[:-last].any())

@@ -242,3 +242,34 @@ def test_same_bits_from_graph_and_stream(B):
     check_forward(d, T, H, 1.0, h_out, u, r2)
     check_backward(d, T, H, "channel", 1.0, r2, got)
     del g
+
+
+def test_offsets_beyond_32_bits(B):
+    """2^31 elements and more in a tensor: the last rows are right, and the column sums."""
+    T, H, last = 262200, 8192, 5
+    cfg = cfg_of(B, T, H)
+    h, y = (torch.zeros((T, H), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    d = make(last, H, "token", True, seed=6)
+    h[-last:], y[-last:] = d["h"], d["y"]
+    gate = torch.zeros_like(h)
+    gate[-last:] = d["gate"]
+    h_out, u = torch.empty_like(h), torch.empty_like(h)
+    rstd = torch.empty((2, T), device="cuda")
+    B.moe_norm_residual(cfg, h, y, d["gamma_post"], h_out, EPS, gate=gate, gate_mode=B.MOE_GATE_TOKEN,
+                        res_scale=0.5, gamma_pre=d["gamma_pre"], u=u, rstd=rstd)
+    torch.cuda.synchronize()
+    r2 = rstd[:, -last:].contiguous()
+    check_forward(d, last, H, 0.5, h_out[-last:], u[-last:], r2)
+    assert not bool(h_out[:-last].any()) and not bool(u[:-last].any())
+    # the other rows' gradients are zero, so the sums are the last rows'
+    dh_out, du = h_out.zero_(), u.zero_()
+    dh_out[-last:], du[-last:] = d["dh_out"], d["du"]
+    o = {"dh": torch.empty_like(h), "dy": torch.empty_like(h), "dgate": torch.empty_like(h),
+         "dgamma_post": torch.empty(H, device="cuda"), "dgamma_pre": torch.empty(H, device="cuda")}
+    B.moe_norm_residual_backward(cfg, h, y, d["gamma_post"], rstd, dh_out, o["dh"], o["dy"], o["dgamma_post"],
+                                 B.alloc_norm_residual_workspace(cfg), gate=gate, gate_mode=B.MOE_GATE_TOKEN,
+                                 res_scale=0.5, gamma_pre=d["gamma_pre"], du=du, dgamma_pre=o["dgamma_pre"],
+                                 dgate=o["dgate"])
+    torch.cuda.synchronize()
+    assert not any(bool(o[n][:-last].any()) for n in ("dh", "dy", "dgate"))
+    check_backward(d, last, H, "token", 0.5, r2, {n: v[-last:] if v.dim() == 2 else v for n, v in o.items()})
