@@ -1711,12 +1711,16 @@ moe_status_t few_smem(FewArgs& a, int limit, size_t* bytes) {
     // one (most experts have one or two tokens), then as many rows, up to
     // eight, as these stages have room for.  (16 tokens, bf16: three stages of
     // eight rows took 690 us, four of four 663; where the tokens crowd onto few
-    // experts, more rows than a full stage holds cost half stages.)
+    // experts, more rows than a full stage holds cost half stages: 8 tokens
+    // 502 us with four rows, 412 with seven.  Up to four tokens only the shared
+    // expert has more than two, and MXFP4 took 123 us with eight rows, 119 with
+    // four.)
     auto bytes_of = [&](int rows) {
         return up(kChunk / kBox * kBoxBytes + rows * (kChunk * 2 + F::kPad) + F::kInvBytes + F::kScaleBytes, 1024);
     };
-    const int room = limit - 1024 - a.off_ring, all = a.T < 4 ? 2 * a.T : 8;   // 1024: the boxes' alignment
-    a.rows_full = all < 4 ? all : 4;
+    const int room = limit - 1024 - a.off_ring;   // 1024: the boxes' alignment
+    a.rows_full = a.T == 1 ? 2 : 4;
+    const int all = a.T <= 4 ? a.rows_full : 8;
     const int stages = room / bytes_of(a.rows_full);
     a.n_stages = stages < kMaxStages ? stages : kMaxStages;
     while (a.rows_full < all && a.n_stages * bytes_of(a.rows_full + 1) <= room) ++a.rows_full;
