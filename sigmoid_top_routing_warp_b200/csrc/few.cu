@@ -238,6 +238,28 @@ __device__ __noinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity, volati
     }
 }
 
+// Grid barriers and the join: one thread publishes what its block has written
+// (the block's barrier in front of it orders that before), one thread looks,
+// and the barrier behind it hands on what it sees.
+__device__ __forceinline__ void publish(int* p) {
+    asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(p) : "memory");
+}
+__device__ __forceinline__ int look(const int* p) {
+    int v;
+    asm volatile("ld.relaxed.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ int acquire(const int* p) {
+    int v;
+    asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ int publish_and_acquire(int* p) {
+    int v;
+    asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+
 // Tensor copy of one box, with an L2 policy.
 __device__ __forceinline__ void box_load(uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1, int c2,
                                          int c3, int c4, uint64_t policy) {
@@ -1172,7 +1194,6 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
         ok = ok && wait(plan_bar, 0);
         lifting = false;
         if (ok) {
-            __threadfence();       // the lifted tokens are read after barrier 0 (plan_bar is behind it)
             for (int u = P.cut1[cta]; ok && u < P.cut1[cta + 1]; ++u) {
                 const Active& act = P.active[first_routed + u / upe];
                 mask = act.mask;
@@ -1183,7 +1204,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
             bool late = false;
             if (ok && lane == 0) {
                 const long long t0 = clock64();
-                while (*reinterpret_cast<volatile int*>(bars + 1) < G) {
+                while (look(bars + 1) < G) {
                     if (*abort_flag || clock64() - t0 > moe::kWaitLimit) {
                         if (!*abort_flag) atomicOr(a.status, moe::DEV_STATUS_TIMEOUT);
                         *abort_flag = 1;
@@ -1192,8 +1213,9 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
                     }
                 }
             }
+            if (lane == 0) acquire(bars + 1);
             ok = ok && !__any_sync(0xffffffffu, late);
-            __threadfence();
+            __syncwarp();
             const uint16_t *hi = nullptr, *lo = nullptr;
             const float* inv = nullptr;
             const int ld_inv = a.ld_act / NF;
@@ -1239,7 +1261,6 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
             bar_sync(kBarLift, kFeeders * 32 + kConsumers);
             lift_tokens(a, (2 * kWarps - 1 - warp) * G + cta, 2 * kWarps * G, lift_sh);
         }
-        __threadfence();
         if (team == 0) {
             bar_arrive(kBarLogits, kConsumers);
         } else {
@@ -1256,13 +1277,12 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
             float bias[4];           // of this thread's experts
 #pragma unroll
             for (int j = 0; j < 4; ++j) bias[j] = __ldg(a.bias + (rid + j * kTeam) % a.E);
-            __threadfence();
             bar_sync(kBarLogits, kConsumers);
             // barrier 0: every block's logits are written
             if (rid == 0) {
-                if (!(a.stall && cta == 0)) atomicAdd(bars, 1);
+                if (!(a.stall && cta == 0)) publish(bars);
                 const long long t0 = clock64();
-                while (*reinterpret_cast<volatile int*>(bars) < G) {
+                while (look(bars) < G) {
                     if (clock64() - t0 > moe::kWaitLimit) {
                         atomicOr(a.status, moe::DEV_STATUS_TIMEOUT);
                         *abort_flag = 1;
@@ -1270,7 +1290,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
                         break;
                     }
                 }
-                __threadfence();
+                acquire(bars);
             }
             good = !group_any(kBarB, !ok);
             bar_arrive(kBarRouted, kTeam + 32);
@@ -1485,9 +1505,8 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
                 good = gate_up(P.active[first_routed + u / upe], (u % upe) * NF);
         if (good) {
             // barrier 1: this block's heads and tails are written
-            __threadfence();
             group_any(kBarAll, false);
-            if (tid == 0) atomicAdd(bars + 1, 1);
+            if (tid == 0) publish(bars + 1);
             const int begin = P.cut2[cta], end = P.cut2[cta + 1];
             const int wsum = a.Is / 128 + (n_active_sh - first_routed) * (a.I / 128);
             sum.clear();
@@ -1553,12 +1572,8 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
                 while (P.cut2[c1] < hi) ++c1;
                 int parts = 0;
                 for (int c = c0; c < c1; ++c) parts += P.cut2[c] < P.cut2[c + 1];
-                __threadfence();
                 group_any(kBarAll, false);
-                if (tid == 0) {
-                    last_sh = atomicAdd(a.joined + rb, 1) == parts - 1;
-                    __threadfence();
-                }
+                if (tid == 0) last_sh = publish_and_acquire(a.joined + rb) == parts - 1;
                 group_any(kBarAll, false);
                 if (last_sh) {
                     for (int i = tid; i < a.T * R; i += kConsumers) {
