@@ -299,8 +299,8 @@ moe_status_t moe_forward_block(const moe_config_t* cfg, const void* h, const voi
 
 /* The whole layer for a few tokens (decode of 1..MOE_FEW_MAX_T users), in one
  * launch: the same steps a1-a9 as moe_forward, for batches so small that the
- * weights of the touched experts are all the traffic.  Differences from
- * moe_forward:
+ * weights of the touched experts are all the traffic (from about 12 tokens on
+ * moe_forward is as fast or faster).  Differences from moe_forward:
  *   - T <= MOE_FEW_MAX_T (above it MOE_ERR_UNSUPPORTED: use moe_forward);
  *   - dtype may also be MOE_DTYPE_MXFP4_BLOCK32, and activations stay bf16
  *     for every weight type (no moe_quantize_act step: nothing here is bound

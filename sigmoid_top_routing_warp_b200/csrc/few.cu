@@ -18,7 +18,8 @@
 //               warps 0-7 work on the shared expert, which needs neither
 //   warp 16     weight producer: tensor copies of the weights (and scales),
 //               stage by stage, as far ahead as the ring is deep
-//   warps 17-19 activation producers: the rows that the weights meet
+//   warps 17-19 activation producers: the rows that the weights meet (one such
+//               warp took 3 % longer with 4-bit weights, two as long as three)
 //
 // Phases:
 //   R   half a block per expert's logits; grid barrier 0; then every block repeats
@@ -33,13 +34,34 @@
 //
 // 8- and 4-bit weights become binary16 by one conversion for two weights
 // (exact: both types lie inside it), and the activations meet them in binary16
-// too, lifted: 64 columns of a token, or one unit's features of a SwiGLU
-// output, are scaled by the power of two that takes the largest of them to
-// 2^14, which keeps every bit of a bf16 value down to 2^-28 of the largest and
-// is off by 2^-39 of it below; the sums are brought back in fp32 together with
-// the weights' block scales.  Phase R lifts the tokens once for all (the shared
-// expert's stages, which do not wait for it, lift theirs on the way), phase 1's
-// epilogue its outputs.
+// too, lifted: a token, or one unit's features of a SwiGLU output (head and
+// tail, 22 significand bits), is scaled by the power of two that takes its
+// largest value to 2^14, which keeps every bit of a bf16 value down to 2^-28 of
+// the largest and is off by 2^-39 of it below.  A token's lift is undone in
+// phase 1's epilogue, a unit's in phase 2 together with the weights' block
+// scales.  Phase R lifts the tokens once for all (the shared expert's stages,
+// which do not wait for it, lift theirs on the way), phase 1's epilogue its
+// outputs.
+//
+// What it takes and what bounds it (H = 5120, I = 1536, 256 experts, top 8 and
+// a shared one, cold L2; in brackets the weights' bytes at the rate of a plain
+// copy, 6.53 TB/s):
+//   bf16   1 token 87 us (65): HBM, and 10 us until the choice is known, in
+//          which only the shared expert's weights can be fetched; a cooperative
+//          launch is 6 us by itself.  16 tokens 649 us (596): HBM, with four
+//          stages in flight; without the products the stream took 593
+//   FP8    1 token 61 us (33): the same 16 us, then half the consumers'
+//          instructions; without the products 55
+//   MXFP4  4 tokens 118 us (58): the consumers' instructions, 340 of a warp for
+//          a stage, 64 of them conversions, where HBM leaves time for 370;
+//          without the products 91
+//   H = 512, I = 128, 32 experts, 1 token: 18.7 us: the launch, two grid
+//          barriers of 2 us and code that comes from L2 in every launch
+// Tried and not kept: half stages that alternate between the teams (bf16 +4 %,
+// FP8 +12 %), looking at the next stage's barriers ahead (+2 %), two reduction
+// buffers in turn (0), loading activations only in the lanes that have a token
+// (+2 %), the shared expert's down projection fetched into L2 during the choice
+// (1 token +1.5 us, 16 tokens -3).
 #include "moe.h"
 #include "kernels.cuh"
 #include "ptx.cuh"
@@ -84,12 +106,12 @@ constexpr int kSlice = 64;                       // K columns of a warp in a sta
 constexpr int kMaxStages = 8;
 constexpr int kBarWord = moe::kSchedFirstWord;   // grid barriers (2) and the exit count, in the status block
 
-// Per weight type: rows of a unit, bits of a weight, bytes of a stage's
-// scales and of its activations' factors, and the
-// activation rows' padding.  A stage holds 32 KB of weights, as 128-byte pieces of 8 rows (1024 bytes, 128-byte swizzle: 64-byte
-// pieces ran at 5 TB/s at most).  A lane's part of a piece, and the padding of
-// the activation rows, are chosen so that a load's lanes (8 rows by 4) fall on
-// different banks:
+// Per weight type: rows of a unit, bits of a weight, bytes of a stage's scales
+// and of phase 2's factors (which undo the outputs' lifts), and the activation
+// rows' padding.  A stage holds 32 KB of weights, as 128-byte pieces of 8 rows
+// (1024 bytes, 128-byte swizzle: 64-byte pieces ran at 5 TB/s at most).  A
+// lane's part of a piece, and the padding of the activation rows, are chosen so
+// that a load's lanes (8 rows by 4) fall on different banks:
 //   bf16   the 16-byte parts 2 t and 2 t + 1: 16 columns in a row
 //   e4m3   word t of each 16-byte part: 4 columns of each 16
 //   MXFP4  word t of each 16-byte part: 8 columns of each 32

@@ -17,6 +17,17 @@
 // mean(p yn) needs D, which needs mean(q hn); expanding D makes both come out
 // of one reduction over three sums:
 //   sum(p yn) = sum(w (dh' + rq q)) - rq mean(q hn) sum(w hn),   w = g gamma_post yn
+//
+// Both are bound by HBM and by the latency of a row's sums (load, sum over the
+// block, store), which rows copied ahead into shared memory hide in part:
+//   forward   8192 x 5120, gate per token: 82 us for 420 MB, 5.1 TB/s (a copy
+//             runs at 6.53); 4 x 5120: 8 us, a launch
+//   backward  8192 x 5120, gate per channel: 107-110 us for 503 MB, 4.6-4.7 TB/s;
+//             777 x 4096, gate per token: 22 us for 51 MB, two launches, the
+//             second one's start hidden behind the first (27 us without that)
+// Tried and not kept: the next row's loads issued across the sum (126-140 us
+// for the backward, registers), four rows in flight, 256-byte L2 fetches and
+// streaming stores (no change), column sums by blocks of 1024 threads (+2 us).
 #include "moe.h"
 #include "kernels.cuh"
 
