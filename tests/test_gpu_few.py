@@ -312,3 +312,13 @@ def test_flagship_shape_agrees_with_moe_forward(B):
     assert torch.equal(idx, B.ws_view(ws, cfg, "topk_idx"))
     a, b = few.double(), out.double()
     assert float((a - b).norm() / a.norm()) <= 1e-2
+
+
+def test_one_workspace_for_every_batch_size(B):
+    """A decode loop's workspace, of the largest batch, serves the smaller ones and other weight types."""
+    big = make(B, "bf16", 16, 256, 64, 4, 256, seed=37)
+    for kind, T in (("bf16", 16), ("mxfp4", 1), ("fp8", 9), ("bf16", 3), ("mxfp4", 16), ("bf16", 16)):
+        p = make(B, kind, T, 256, 64, 4, 256, seed=38 + T)
+        p["ws"] = big["ws"]
+        call(B, p)
+        check(B, p)
