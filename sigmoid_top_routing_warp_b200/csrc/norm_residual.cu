@@ -47,8 +47,26 @@ namespace {
 
 constexpr int kNrMaxH = 16384;
 constexpr int kNrWideThreads = 512;
-constexpr int kNrBwdThreads = 320; // of a block of the backward pass: one or two 8-value vectors each
-constexpr int kNrBwdBlocks = 148;   // row walkers of the backward pass, one partial sum each
+constexpr int kNrWideSmem = 220 << 10;   // for its rows
+constexpr int kNrBwdThreads = 384; // of a block of the backward pass at most: one or two 8-value vectors each
+constexpr int kNrBwdShort = 2560;  // columns up to which they have one
+constexpr int kNrBwdBlocks = 148;   // row walkers of the backward pass, one partial sum each; several times as
+                                    // many for short rows
+
+// Threads of a block of the backward pass, and most blocks of it.  A block works
+// on one row at a time and waits for its sum, so an SM gets as many as 640
+// threads hold, up to eight: 8192 rows of 2560 / 1024 / 256 columns take 62 / 34 /
+// 22 us, with one block an SM 83 / 65 / 58.  Two vectors a thread from 2560 columns
+// on: 2560 with two 80 us and with one 82 in one block an SM, 1024 67 and 63.
+int bwd_threads(int H) {
+    const int vecs = H / 8;
+    return ((H <= kNrBwdShort ? vecs : (vecs + 1) / 2) + 31) / 32 * 32;
+}
+int bwd_blocks(int H) {
+    if (H > kNrBwdShort) return kNrBwdBlocks;
+    const int n = 640 / bwd_threads(H);
+    return kNrBwdBlocks * (n < 8 ? n : 8);
+}
 
 struct NrArgs {
     const uint16_t *h, *y, *gamma_post, *gate, *gamma_pre;
@@ -65,25 +83,6 @@ struct NrArgs {
     float* part;                       // [blocks][2][H]
     int blocks;
 };
-
-__device__ __forceinline__ void unpack8(const uint4& v, float* f) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = __uint_as_float(w[i] << 16);
-        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-}
-
-__device__ __forceinline__ uint4 pack8(const float* f) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t*>(&b);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
 
 __device__ __forceinline__ const uint4* vec(const uint16_t* p, size_t row, int H) {
     return reinterpret_cast<const uint4*>(p + row * H);
@@ -400,92 +399,148 @@ __global__ void __launch_bounds__(kNrBwdThreads) norm_residual_bwd_kernel(const 
     }
 }
 
-// Rows longer than the registers hold (above 5120 columns): two passes over a
-// row, the second one from L1 and L2, and the column sums in shared memory
-// [2][H], each thread at its own columns.
+// Rows of more than 6144 columns, up to 512 threads: only the column sums stay
+// in registers.  A row stays in shared memory until its second pass, which
+// computes the first one's values again (128 registers a thread hold no more),
+// and the columns' weights come from L1.  ST rows are there or on their way.
+// 4096 x 8192: 117 us (403 MB, 62 us of copies), 131 in 1024 threads with half the
+// vectors, 230 with both passes from L2; 2048 x 16384: 140.
+template <int NV, int ST, bool TOKEN>
 __global__ void __launch_bounds__(kNrWideThreads) norm_residual_bwd_wide_kernel(const NrArgs p) {
     let_dependents_launch();
-    extern __shared__ float col[];
+    extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float sh[2][3 * 32];
-    const int nvec = p.H / 8;
+    constexpr int NT = TOKEN ? 5 : 4;                 // tensors of a row: y, h, dh_out, du, gate
+    const int nthr = blockDim.x, nvec = p.H / 8;
     const float inv_h = 1.0f / (float)p.H;
-    for (int i = threadIdx.x; i < 2 * p.H; i += blockDim.x) col[i] = 0.0f;
-    __syncthreads();
-    const uint4 zero = make_uint4(0, 0, 0, 0);
-    const uint4 one = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
-    int half = 0;
-    for (size_t t = blockIdx.x; t < (size_t)p.T; t += gridDim.x) {
-        const float rp = p.rstd_in[t], rq = p.du ? p.rstd_in[p.T + t] : 0.0f;
-        float y[8], h[8], d[8], u[8], g[8], wp[8], wq[8];
-        auto load = [&](int c) {
-            unpack8(vec(p.y, t, p.H)[c], y);
-            unpack8(vec(p.h, t, p.H)[c], h);
-            unpack8(vec(p.dh_out, t, p.H)[c], d);
-            unpack8(p.du ? vec(p.du, t, p.H)[c] : zero, u);
-            unpack8(p.gate_mode == MOE_GATE_NONE ? one : vec(p.gate, p.gate_mode == MOE_GATE_TOKEN ? t : 0, p.H)[c],
-                    g);
-            unpack8(__ldg(vec(p.gamma_post, 0, p.H) + c), wp);
-            unpack8(p.du ? __ldg(vec(p.gamma_pre, 0, p.H) + c) : zero, wq);
-        };
-        float s[3] = {0.0f, 0.0f, 0.0f};
-        for (int c = threadIdx.x; c < nvec; c += blockDim.x) {
-            load(c);
+    const uint32_t mine = (uint32_t)__cvta_generic_to_shared(smem) + threadIdx.x * 16;
+    auto place = [&](int st, int k, int i) { return mine + ((st * NT + k) * NV + i) * nthr * 16; };
+    auto fetch = [&](size_t t, int st) {
+        if (t < (size_t)p.T) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float w = g[j] * (wp[j] * (y[j] * rp));
-                const float hn = fmaf(p.a, h[j], w) * rq;
-                const float q = u[j] * wq[j];
-                s[0] = fmaf(q, hn, s[0]);
-                s[1] = fmaf(w, fmaf(rq, q, d[j]), s[1]);
-                s[2] = fmaf(w, hn, s[2]);
+            for (int i = 0; i < NV; ++i) {
+                const int c = threadIdx.x + i * nthr;
+                const bool ok = c < nvec;
+                const int cc = ok ? c : 0;
+                copy16(place(st, 0, i), vec(p.y, t, p.H) + cc, ok);
+                copy16(place(st, 1, i), vec(p.h, t, p.H) + cc, ok);
+                copy16(place(st, 2, i), vec(p.dh_out, t, p.H) + cc, ok);
+                copy16(place(st, 3, i), (p.du ? vec(p.du, t, p.H) : vec(p.y, t, p.H)) + cc, ok && p.du);
+                if (TOKEN) copy16(place(st, 4, i), vec(p.gate, t, p.H) + cc, ok);
             }
         }
+        copies_close();
+    };
+    size_t t = blockIdx.x;
+    const size_t step = gridDim.x;
+#pragma unroll
+    for (int k = 0; k < ST; ++k) fetch(t + k * step, k);
+    F2 sp[NV][4], sq[NV][4];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sp[i][j] = sq[i][j] = f2(0.0f, 0.0f);
+    const F2 a2 = f2(p.a, p.a);
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    int st = 0, half = 0;
+    for (; t < (size_t)p.T; t += step) {
+        const float rp = __ldg(p.rstd_in + t), rq = p.du ? __ldg(p.rstd_in + p.T + t) : 0.0f;
+        const F2 rp2 = f2(rp, rp), rq2 = f2(rq, rq);
+        // a vector of the row: both passes take the same values from it
+        auto values = [&](int i, auto use) {
+            const int c = threadIdx.x + i * nthr;
+            const bool ok = c < nvec;
+            const uint4 w1 = ok ? __ldg(vec(p.gamma_post, 0, p.H) + c) : zero;
+            const uint4 w2 = ok && p.du ? __ldg(vec(p.gamma_pre, 0, p.H) + c) : zero;
+            uint4 gr;
+            if (TOKEN)
+                gr = lds128(place(st, 4, i));
+            else
+                gr = ok && p.gate_mode == MOE_GATE_CHANNEL ? __ldg(vec(p.gate, 0, p.H) + c)
+                                                           : make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
+            const uint4 yr = lds128(place(st, 0, i)), hr = lds128(place(st, 1, i)), dr = lds128(place(st, 2, i)),
+                        ur = lds128(place(st, 3, i));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const F2 g = widen(word(gr, j)), wg = widen(word(w1, j));
+                const F2 yn = widen(word(yr, j)) * rp2, w = g * (wg * yn);
+                const F2 hn = fma2(a2, widen(word(hr, j)), w) * rq2;
+                const F2 u = widen(word(ur, j)), q = u * widen(word(w2, j));
+                use(j, g, wg, yn, w, hn, u, q, fma2(rq2, q, widen(word(dr, j))));
+            }
+        };
+        copies_left<ST - 1>();
+        F2 x0 = f2(0.0f, 0.0f), x1 = x0, x2 = x0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            values(i, [&](int j, F2, F2, F2, F2 w, F2 hn, F2 u, F2 q, F2 dq) {
+                x0 = fma2(q, hn, x0);
+                x1 = fma2(w, dq, x1);
+                x2 = fma2(w, hn, x2);
+                sq[i][j] = fma2(u, hn, sq[i][j]);
+            });
+        float s[3] = {total(x0), total(x1), total(x2)};
         block_sum(s, sh[half]);
         half ^= 1;
-        const float c1 = s[0] * inv_h;
-        const float c2 = (s[1] - rq * c1 * s[2]) * inv_h;
-        for (int c = threadIdx.x; c < nvec; c += blockDim.x) {
-            float odh[8], ody[8], odg[8];
-            load(c);
+        const float c1 = s[0] * inv_h, c2 = (s[1] - rq * c1 * s[2]) * inv_h;
+        const F2 k1 = f2(-rq * c1, -rq * c1), k2 = f2(-c2, -c2);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float yn = y[j] * rp;
-                const float hn = fmaf(p.a, h[j], g[j] * (wp[j] * yn)) * rq;
-                const float D = fmaf(rq, fmaf(u[j], wq[j], -hn * c1), d[j]);
-                const float Dg = D * g[j];
-                odh[j] = p.a * D;
-                ody[j] = rp * fmaf(Dg, wp[j], -yn * c2);
-                odg[j] = D * (wp[j] * yn);
-                col[8 * c + j] += (p.gate_mode == MOE_GATE_TOKEN ? Dg : D) * yn;
-                col[p.H + 8 * c + j] += u[j] * hn;
-            }
-            reinterpret_cast<uint4*>(p.dh + t * p.H)[c] = pack8(odh);
-            reinterpret_cast<uint4*>(p.dy + t * p.H)[c] = pack8(ody);
-            if (p.gate_mode == MOE_GATE_TOKEN)
-                reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.dgate) + t * p.H)[c] = pack8(odg);
+        for (int i = 0; i < NV; ++i) {
+            const int c = threadIdx.x + i * nthr;
+            uint32_t odh[4], ody[4], odg[4];
+            values(i, [&](int j, F2 g, F2 wg, F2 yn, F2, F2 hn, F2, F2, F2 dq) {
+                const F2 D = fma2(hn, k1, dq);
+                const F2 Dg = D * g;
+                odh[j] = narrow(a2 * D);
+                ody[j] = narrow(rp2 * fma2(yn, k2, Dg * wg));
+                if (TOKEN) odg[j] = narrow(D * (wg * yn));
+                // a gate per channel is a factor of the whole column
+                sp[i][j] = fma2(TOKEN ? Dg : D, yn, sp[i][j]);
+            });
+            if (c >= nvec) continue;
+            reinterpret_cast<uint4*>(p.dh + t * p.H)[c] = make_uint4(odh[0], odh[1], odh[2], odh[3]);
+            reinterpret_cast<uint4*>(p.dy + t * p.H)[c] = make_uint4(ody[0], ody[1], ody[2], ody[3]);
+            if (TOKEN)
+                reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.dgate) + t * p.H)[c] =
+                    make_uint4(odg[0], odg[1], odg[2], odg[3]);
+        }
+        fetch(t + ST * step, st);
+        if (ST > 1) st = st == ST - 1 ? 0 : st + 1;
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = threadIdx.x + i * nthr;
+        if (c >= nvec) continue;
+        float* base = p.part + (size_t)blockIdx.x * 2 * p.H + 8 * c;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float x, y;
+            split(sp[i][j], x, y);
+            *reinterpret_cast<float2*>(base + 2 * j) = make_float2(x, y);
+            split(sq[i][j], x, y);
+            *reinterpret_cast<float2*>(base + p.H + 2 * j) = make_float2(x, y);
         }
     }
-    __syncthreads();
-    for (int i = threadIdx.x; i < 2 * p.H; i += blockDim.x) p.part[(size_t)blockIdx.x * 2 * p.H + i] = col[i];
 }
 
 // Column sums of the per-block partials in block order, in binary64:
 // blockIdx.y 0 gives dgamma_post and a channel gate's dgate, 1 dgamma_pre.
-__global__ void __launch_bounds__(256) norm_residual_cols_kernel(const NrArgs p) {
-    __shared__ double sh[8][33];
+template <int NW>   // warps, each with a share of the partials
+__global__ void __launch_bounds__(NW * 32) norm_residual_cols_kernel(const NrArgs p) {
+    __shared__ double sh[NW][33];
     const int which = blockIdx.y;
     const int col = blockIdx.x * 32 + (threadIdx.x & 31), w = threadIdx.x >> 5;
     after_primary();
     double s = 0.0;
     if (col < p.H) {
 #pragma unroll 8
-        for (int b = w; b < p.blocks; b += 8) s += (double)p.part[((size_t)b * 2 + which) * p.H + col];
+        for (int b = w; b < p.blocks; b += NW) s += (double)p.part[((size_t)b * 2 + which) * p.H + col];
     }
     sh[w][threadIdx.x & 31] = s;
     __syncthreads();
     if (w != 0 || col >= p.H) return;
 #pragma unroll
-    for (int i = 1; i < 8; ++i) s += sh[i][threadIdx.x];
+    for (int i = 1; i < NW; ++i) s += sh[i][threadIdx.x];
     if (which == 1) {
         p.dgamma_pre[col] = (float)s;
     } else if (p.gate_mode == MOE_GATE_CHANNEL) {
@@ -584,12 +639,28 @@ moe_status_t run_forward(const NrArgs& p, cudaStream_t s) {
 
 template <int NV, bool TOKEN>
 moe_status_t launch_backward(const NrArgs& p, cudaStream_t s) {
-    const int threads = ((p.H / 8 + NV - 1) / NV + 31) / 32 * 32;
+    const int threads = bwd_threads(p.H);
     const int smem = kNrStages * (TOKEN ? 5 : 4) * NV * threads * 16;
     const cudaError_t e = cudaFuncSetAttribute(norm_residual_bwd_kernel<NV, TOKEN>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return nfail(MOE_ERR_CUDA, "norm_residual backward: %s", cudaGetErrorString(e));
     norm_residual_bwd_kernel<NV, TOKEN><<<p.blocks, threads, smem, s>>>(p);
+    return MOE_OK;
+}
+
+// Two rows in shared memory where they fit, up to 11 or 13 thousand columns.
+template <bool TOKEN>
+moe_status_t launch_backward_wide(const NrArgs& p, cudaStream_t s) {
+    const int nv = p.H <= 16 * kNrWideThreads ? 2 : 4;
+    const int threads = ((p.H / 8 + nv - 1) / nv + 31) / 32 * 32;
+    const int row = (TOKEN ? 5 : 4) * nv * threads * 16;
+    const int st = 2 * row <= kNrWideSmem ? 2 : 1;
+    auto* kernel = nv == 2 ? norm_residual_bwd_wide_kernel<2, 2, TOKEN>
+                   : st == 2 ? norm_residual_bwd_wide_kernel<4, 2, TOKEN>
+                             : norm_residual_bwd_wide_kernel<4, 1, TOKEN>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, st * row);
+    if (e != cudaSuccess) return nfail(MOE_ERR_CUDA, "norm_residual backward: %s", cudaGetErrorString(e));
+    kernel<<<p.blocks, threads, st * row, s>>>(p);
     return MOE_OK;
 }
 
@@ -643,7 +714,7 @@ moe_status_t moe_norm_residual(const moe_config_t* cfg, const void* h, const voi
 size_t moe_norm_residual_workspace_size(const moe_config_t* cfg) {
     moe::api_clear_error();
     if (check_shape(cfg) != MOE_OK) return 0;
-    return (size_t)kNrBwdBlocks * 2 * cfg->H * 4;
+    return (size_t)bwd_blocks(cfg->H) * 2 * cfg->H * 4;
 }
 
 moe_status_t moe_norm_residual_backward(const moe_config_t* cfg, const void* h, const void* y,
@@ -688,7 +759,7 @@ moe_status_t moe_norm_residual_backward(const moe_config_t* cfg, const void* h, 
                 return nfail(MOE_ERR_INVALID_ARG, "%s overlaps another output", o.name);
     }
     NR_TRY(need(ws, "workspace", 256));
-    const size_t bytes = (size_t)kNrBwdBlocks * 2 * cfg->H * 4;
+    const size_t bytes = (size_t)bwd_blocks(cfg->H) * 2 * cfg->H * 4;
     if (ws_bytes < bytes)
         return nfail(MOE_ERR_WORKSPACE, "workspace too small, %s %lld bytes", "needs", (long long)bytes);
     NrArgs p = {};
@@ -710,34 +781,33 @@ moe_status_t moe_norm_residual_backward(const moe_config_t* cfg, const void* h, 
     p.dgamma_post = dgamma_post;
     p.dgamma_pre = dgamma_pre;
     p.part = static_cast<float*>(ws);
-    p.blocks = cfg->T < kNrBwdBlocks ? cfg->T : kNrBwdBlocks;
+    // eight rows of a block and more, where that leaves a block for every SM
+    p.blocks = cfg->T / 8 < bwd_blocks(cfg->H) ? cfg->T / 8 : bwd_blocks(cfg->H);
+    if (p.blocks < kNrBwdBlocks) p.blocks = cfg->T < kNrBwdBlocks ? cfg->T : kNrBwdBlocks;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (p.T > 0) {
         const bool token = gate_mode == MOE_GATE_TOKEN;
-        if (p.H <= 8 * kNrBwdThreads) {
+        if (p.H <= kNrBwdShort) {
             NR_TRY((token ? launch_backward<1, true>(p, s) : launch_backward<1, false>(p, s)));
         } else if (p.H <= 16 * kNrBwdThreads) {
             NR_TRY((token ? launch_backward<2, true>(p, s) : launch_backward<2, false>(p, s)));
         } else {
-            const int smem = 2 * p.H * 4;
-            const cudaError_t e = cudaFuncSetAttribute(norm_residual_bwd_wide_kernel,
-                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-            if (e != cudaSuccess) return nfail(MOE_ERR_CUDA, "norm_residual backward: %s", cudaGetErrorString(e));
-            norm_residual_bwd_wide_kernel<<<p.blocks, kNrWideThreads, smem, s>>>(p);
+            NR_TRY((token ? launch_backward_wide<true>(p, s) : launch_backward_wide<false>(p, s)));
         }
         NR_TRY(launched("norm_residual backward launch: %s"));
     }
     // with no rows the sums are zero
     cudaLaunchConfig_t cols = {};
     cols.gridDim = dim3((p.H + 31) / 32, dgamma_pre ? 2 : 1);
-    cols.blockDim = dim3(256);
+    const bool many = p.blocks > kNrBwdBlocks;
+    cols.blockDim = dim3(many ? 1024 : 256);
     cols.stream = s;
     cudaLaunchAttribute early = {};
     early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     early.val.programmaticStreamSerializationAllowed = 1;
     cols.attrs = &early;
     cols.numAttrs = p.T > 0 ? 1 : 0;
-    const cudaError_t e = cudaLaunchKernelEx(&cols, norm_residual_cols_kernel, p);
+    const cudaError_t e = cudaLaunchKernelEx(&cols, many ? norm_residual_cols_kernel<32> : norm_residual_cols_kernel<8>, p);
     if (e != cudaSuccess) return nfail(MOE_ERR_CUDA, "norm_residual column-sum launch: %s", cudaGetErrorString(e));
     return MOE_OK;
 }

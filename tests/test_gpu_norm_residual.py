@@ -273,3 +273,16 @@ def test_offsets_beyond_32_bits(B):
     torch.cuda.synchronize()
     assert not any(bool(o[n][:-last].any()) for n in ("dh", "dy", "dgate"))
     check_backward(d, last, H, "token", 0.5, r2, {n: v[-last:] if v.dim() == 2 else v for n, v in o.items()})
+
+
+@pytest.mark.parametrize("T,H", [(2400, 64), (1500, 264), (1201, 2560), (310, 5136), (320, 6144), (305, 6152),
+                                 (300, 8200), (299, 12000)])
+@pytest.mark.parametrize("gate", MODES)
+def test_many_rows(B, T, H, gate):
+    """More rows than blocks at every number of blocks an SM and every row length class."""
+    d = make(T, H, gate, gate != "channel", seed=7)
+    h_out, u, rstd = forward(B, d, T, H, gate, 0.75)
+    got = backward(B, d, T, H, gate, 0.75, rstd)
+    torch.cuda.synchronize()
+    check_forward(d, T, H, 0.75, h_out, u, rstd)
+    check_backward(d, T, H, gate, 0.75, rstd, got)
