@@ -27,7 +27,8 @@
 //             second one's start hidden behind the first (27 us without that)
 // Tried and not kept: the next row's loads issued across the sum (126-140 us
 // for the backward, registers), four rows in flight, 256-byte L2 fetches and
-// streaming stores (no change), column sums by blocks of 1024 threads (+2 us).
+// streaming stores (no change), column sums of 148 partials by blocks of 1024
+// threads (+2 us), pairs of rows with one sum in 640 threads (121 us).
 #include "moe.h"
 #include "kernels.cuh"
 
