@@ -48,11 +48,11 @@
 // copy, 6.53 TB/s):
 //   bf16   1 token 87 us (65): HBM, and 10 us until the choice is known, in
 //          which only the shared expert's weights can be fetched; a cooperative
-//          launch is 6 us by itself.  16 tokens 649 us (596): HBM, with four
-//          stages in flight; without the products the stream took 593
+//          launch is 6 us by itself.  16 tokens, 78 experts, 649 us (571): HBM
+//          with four stages in flight; without the products the stream took 593
 //   FP8    1 token 61 us (33): the same 16 us, then half the consumers'
 //          instructions; without the products 55
-//   MXFP4  4 tokens 118 us (58): the consumers' instructions, 340 of a warp for
+//   MXFP4  4 tokens, 30 experts, 118 us (60): the consumers' instructions, 340 of a warp for
 //          a stage, 64 of them conversions, where HBM leaves time for 370;
 //          without the products 91
 //   H = 512, I = 128, 32 experts, 1 token: 18.7 us: the launch, two grid
