@@ -197,9 +197,14 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
+# what torch.cuda.current_device and current_stream ask, without the objects around it
+_current_device, _raw_stream = (getattr(torch._C, n, None) for n in ("_cuda_getDevice",
+                                                                     "_cuda_getCurrentRawStream"))
+
+
 def _stream(stream) -> int:
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return _raw_stream(_current_device())
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -425,7 +430,7 @@ def _complain(where, name, t, dtype, numel):
 def _look(where, args):
     """Pointers of `args`, each (name, tensor or None, dtype, elements); the C
     ABI says which of them may be NULL."""
-    dev = torch.cuda.current_device() if torch.cuda.is_initialized() else -2
+    dev = _current_device() if torch.cuda.is_initialized() else -2
     out = []
     for name, t, dtype, numel in args:
         if t is None:
@@ -502,8 +507,8 @@ def moe_norm_residual(cfg, h, y, gamma_post, h_out, eps, gate=None, gate_mode=MO
         ("gate", gate, _BF16, n if gate_mode == MOE_GATE_TOKEN else H),
         ("gamma_pre", gamma_pre, _BF16, H), ("h_out", h_out, _BF16, n), ("u", u, _BF16, n),
         ("rstd", rstd, _F32, 2 * T)))
-    _check(_lib.moe_norm_residual(ctypes.byref(cfg.c()), *p[:4], gate_mode, res_scale, eps, *p[4:],
-                                  _stream(stream)), "moe_norm_residual")
+    _check(_lib.moe_norm_residual(ctypes.byref(MoeConfigC(T, H)), *p[:4], gate_mode, res_scale, eps,
+                                  *p[4:], _stream(stream)), "moe_norm_residual")
 
 
 def norm_residual_workspace_size(cfg: MoeConfig) -> int:
@@ -534,7 +539,7 @@ def moe_norm_residual_backward(cfg, h, y, gamma_post, rstd, dh_out, dh, dy, dgam
         ("dgate", dgate, _BF16 if gate_mode == MOE_GATE_TOKEN else _F32, ng),
         ("dgamma_post", dgamma_post, _F32, H), ("dgamma_pre", dgamma_pre, _F32, H),
         ("workspace", ws, _U8, ws.numel())))
-    _check(_lib.moe_norm_residual_backward(ctypes.byref(cfg.c()), *p[:4], gate_mode, res_scale,
+    _check(_lib.moe_norm_residual_backward(ctypes.byref(MoeConfigC(T, H)), *p[:4], gate_mode, res_scale,
                                            *p[4:], ws.numel(), _stream(stream)),
            "moe_norm_residual_backward")
 
