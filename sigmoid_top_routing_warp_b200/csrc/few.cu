@@ -730,6 +730,10 @@ struct Source {
         const int lane = threadIdx.x & 31;
         const uint32_t dst = ring.stage(), bar = ring.w + 8 * ring.slot;
         if (lane == 0) {
+            // A narrow stage's activations stood where this stage's boxes land
+            // (off_x): ordinary writes, which the barriers alone do not order
+            // before the copies' writes.
+            moe::fence_async_smem();
             expect_bytes(bar, (kn + kBox - 1) / kBox * kBoxBytes);
             for (int k = 0; k < kn; k += kBox)
                 box_load(dst + k / kBox * kBoxBytes, map, bar, byte_of(k0 + k), 0, piece_of(k0 + k), 0, group, policy);
