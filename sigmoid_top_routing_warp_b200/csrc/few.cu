@@ -1167,10 +1167,10 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
                                  },
                                  [](int) { return true; });
         }
-        // no copy may still be in flight when the block leaves
-        if (!ok)
-            for (int i = 0; i < a.n_stages; ++i)
-                if (issued >> i & 1u) bar_wait_slow(ring.w + 8 * i, last_phase >> i & 1u, abort_flag, a.status, true);
+        // No copy may still be in flight when the block leaves: the consumers
+        // may have given up, on the activations, after the last copy was issued.
+        for (int i = 0; i < a.n_stages; ++i)
+            if (issued >> i & 1u) bar_wait_slow(ring.w + 8 * i, last_phase >> i & 1u, abort_flag, a.status, true);
     } else if (warp > 2 * kWarps) {
         // ---------------------------------------------------------- activation producers
         const int feeder = warp - 2 * kWarps - 1;
