@@ -378,6 +378,7 @@ moe_status_t moe_norm_residual(const moe_config_t* cfg, const void* h, const voi
  *   ws          moe_norm_residual_workspace_size bytes, 256-byte aligned, no
  *               zero-fill needed
  * All outputs are overwritten; the column sums are taken in a fixed order.
+ * Without gamma_pre no gradient depends on h: its values are not read.
  * T = 0 writes zeros to dgamma_post, dgamma_pre and a channel dgate.        */
 size_t moe_norm_residual_workspace_size(const moe_config_t* cfg);
 moe_status_t moe_norm_residual_backward(const moe_config_t* cfg, const void* h, const void* y,

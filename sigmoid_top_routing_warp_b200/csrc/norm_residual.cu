@@ -17,14 +17,17 @@
 // mean(p yn) needs D, which needs mean(q hn); expanding D makes both come out
 // of one reduction over three sums:
 //   sum(p yn) = sum(w (dh' + rq q)) - rq mean(q hn) sum(w hn),   w = g gamma_post yn
+// Without the norm after the update D = dh', and h has no part in anything.
 //
 // Both are bound by HBM and by the latency of a row's sums (load, sum over the
 // block, store), which rows copied ahead into shared memory hide in part:
 //   forward   8192 x 5120, gate per token: 82 us for 420 MB, 5.1 TB/s (a copy
 //             runs at 6.53); 4 x 5120: 8 us, a launch
-//   backward  8192 x 5120, gate per channel: 107-110 us for 503 MB, 4.6-4.7 TB/s;
-//             777 x 4096, gate per token: 22 us for 51 MB, two launches, the
-//             second one's start hidden behind the first (27 us without that)
+//   backward  8192 x 5120, gate per channel: 98 us for 503 MB, 5.1 TB/s, 74 us
+//             for 336 MB without the norm after the update (97 when it read h
+//             all the same); 777 x 4096, gate per token: 22 us for 51 MB, two
+//             launches, the second one's start hidden behind the first (27 us
+//             without that)
 // Tried and not kept: the next row's loads issued across the sum (126-140 us
 // for the backward, registers), four rows in flight, 256-byte L2 fetches and
 // streaming stores (no change), column sums of 148 partials by blocks of 1024
@@ -269,17 +272,23 @@ __global__ void __launch_bounds__(THREADS, 1280 / THREADS) norm_residual_kernel(
     }
 }
 
+// Tensors of a row that the backward pass reads: y, dh_out, with the norm after
+// the update h and du, with a gate per token the gate.
+constexpr int row_tensors(bool token, bool pre) { return 2 + (pre ? 2 : 0) + (token ? 1 : 0); }
+
 // Persistent blocks, NV 8-value vectors of the row per thread; a thread owns
 // the same columns in every row, so the column sums stay in its registers and
 // leave as one partial per block.  A gate per channel and no gate are constant
 // down a column, so sum(D yn) alone gives both dgamma_post (times g) and dgate
-// (times gamma_post); with a gate per token it is sum(D g yn).
-template <int NV, bool TOKEN>
+// (times gamma_post); with a gate per token it is sum(D g yn).  Without the
+// norm after the update (PRE) D is dh' alone: h is not read, and an infinity or
+// a NaN in it reaches no gradient.
+template <int NV, bool TOKEN, bool PRE>
 __global__ void __launch_bounds__(kNrBwdThreads) norm_residual_bwd_kernel(const NrArgs p) {
     let_dependents_launch();
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float sh[2][3 * 32];
-    constexpr int NT = TOKEN ? 5 : 4;                 // tensors of a row: y, h, dh_out, du, gate
+    constexpr int NT = row_tensors(TOKEN, PRE), kGate = NT - 1;   // of a row: y, dh_out, with PRE h and du, gate
     const int nthr = blockDim.x, nvec = p.H / 8;
     const float inv_h = 1.0f / (float)p.H;
     const uint32_t mine = (uint32_t)__cvta_generic_to_shared(smem) + threadIdx.x * 16;
@@ -292,10 +301,12 @@ __global__ void __launch_bounds__(kNrBwdThreads) norm_residual_bwd_kernel(const 
                 const bool ok = c < nvec;
                 const int cc = ok ? c : 0;
                 copy16(place(st, 0, i), vec(p.y, t, p.H) + cc, ok);
-                copy16(place(st, 1, i), vec(p.h, t, p.H) + cc, ok);
-                copy16(place(st, 2, i), vec(p.dh_out, t, p.H) + cc, ok);
-                copy16(place(st, 3, i), (p.du ? vec(p.du, t, p.H) : vec(p.y, t, p.H)) + cc, ok && p.du);
-                if (TOKEN) copy16(place(st, 4, i), vec(p.gate, t, p.H) + cc, ok);
+                copy16(place(st, 1, i), vec(p.dh_out, t, p.H) + cc, ok);
+                if (PRE) {
+                    copy16(place(st, 2, i), vec(p.h, t, p.H) + cc, ok);
+                    copy16(place(st, 3, i), vec(p.du, t, p.H) + cc, ok);
+                }
+                if (TOKEN) copy16(place(st, kGate, i), vec(p.gate, t, p.H) + cc, ok);
             }
         }
         copies_close();
@@ -313,7 +324,7 @@ __global__ void __launch_bounds__(kNrBwdThreads) norm_residual_bwd_kernel(const 
         const uint4 zero = make_uint4(0, 0, 0, 0);
         const uint4 one = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
         const uint4 w1 = ok ? __ldg(vec(p.gamma_post, 0, p.H) + c) : zero;
-        const uint4 w2 = ok && p.du ? __ldg(vec(p.gamma_pre, 0, p.H) + c) : zero;
+        const uint4 w2 = PRE && ok ? __ldg(vec(p.gamma_pre, 0, p.H) + c) : zero;
         const uint4 gc = ok && p.gate_mode == MOE_GATE_CHANNEL ? __ldg(vec(p.gate, 0, p.H) + c) : one;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -324,44 +335,59 @@ __global__ void __launch_bounds__(kNrBwdThreads) norm_residual_bwd_kernel(const 
     }
     const F2 a2 = f2(p.a, p.a);
     int st = 0, half = 0;
-    float rp_next = __ldg(p.rstd_in + t), rq_next = p.du ? __ldg(p.rstd_in + p.T + t) : 0.0f;
+    float rp_next = __ldg(p.rstd_in + t), rq_next = PRE ? __ldg(p.rstd_in + p.T + t) : 0.0f;
     for (; t < (size_t)p.T; t += step) {
         const float rp = rp_next, rq = rq_next;
         const F2 rp2 = f2(rp, rp), rq2 = f2(rq, rq);
         copies_left<1>();
         if (t + step < (size_t)p.T) {
             rp_next = __ldg(p.rstd_in + t + step);
-            rq_next = p.du ? __ldg(p.rstd_in + p.T + t + step) : 0.0f;
+            rq_next = PRE ? __ldg(p.rstd_in + p.T + t + step) : 0.0f;
         }
         F2 yn[NV][4], hn[NV][4], dq[NV][4];           // dq: dh' + rq q
         uint4 gr[NV];
         F2 x0 = f2(0.0f, 0.0f), x1 = x0, x2 = x0;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const uint4 yr = lds128(place(st, 0, i)), hr = lds128(place(st, 1, i)), dr = lds128(place(st, 2, i)),
-                        ur = lds128(place(st, 3, i));
-            if (TOKEN) gr[i] = lds128(place(st, 4, i));
+            const uint4 yr = lds128(place(st, 0, i)), dr = lds128(place(st, 1, i));
+            uint4 hr, ur;
+            if (PRE) {
+                hr = lds128(place(st, 2, i));
+                ur = lds128(place(st, 3, i));
+            }
+            if (TOKEN) gr[i] = lds128(place(st, kGate, i));
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 yn[i][j] = widen(word(yr, j)) * rp2;
                 F2 w = wp[i][j] * yn[i][j];
                 if (TOKEN) w = widen(word(gr[i], j)) * w;
-                hn[i][j] = fma2(a2, widen(word(hr, j)), w) * rq2;
-                const F2 u = widen(word(ur, j));
-                const F2 q = u * wq[i][j];
-                dq[i][j] = fma2(rq2, q, widen(word(dr, j)));
-                x0 = fma2(q, hn[i][j], x0);
+                dq[i][j] = widen(word(dr, j));
+                if (PRE) {
+                    hn[i][j] = fma2(a2, widen(word(hr, j)), w) * rq2;
+                    const F2 u = widen(word(ur, j));
+                    const F2 q = u * wq[i][j];
+                    dq[i][j] = fma2(rq2, q, dq[i][j]);
+                    x0 = fma2(q, hn[i][j], x0);
+                    x2 = fma2(w, hn[i][j], x2);
+                    sq[i][j] = fma2(u, hn[i][j], sq[i][j]);
+                }
                 x1 = fma2(w, dq[i][j], x1);
-                x2 = fma2(w, hn[i][j], x2);
-                sq[i][j] = fma2(u, hn[i][j], sq[i][j]);
             }
         }
         fetch(t + 2 * step, st == 0 ? kNrStages - 1 : st - 1);
         st = st == kNrStages - 1 ? 0 : st + 1;
-        float s[3] = {total(x0), total(x1), total(x2)};
+        float s[PRE ? 3 : 1] = {total(x1)};
+        if constexpr (PRE) {
+            s[1] = total(x0);
+            s[2] = total(x2);
+        }
         block_sum(s, sh[half]);
         half ^= 1;
-        const float c1 = s[0] * inv_h, c2 = (s[1] - rq * c1 * s[2]) * inv_h;
+        float c1 = 0.0f, c2 = s[0] * inv_h;
+        if constexpr (PRE) {
+            c1 = s[1] * inv_h;
+            c2 = (s[0] - rq * c1 * s[2]) * inv_h;
+        }
         const F2 k1 = f2(-rq * c1, -rq * c1), k2 = f2(-c2, -c2);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -369,7 +395,7 @@ __global__ void __launch_bounds__(kNrBwdThreads) norm_residual_bwd_kernel(const 
             uint32_t odh[4], ody[4], odg[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const F2 D = fma2(hn[i][j], k1, dq[i][j]);
+                const F2 D = PRE ? fma2(hn[i][j], k1, dq[i][j]) : dq[i][j];
                 const F2 Dg = TOKEN ? D * widen(word(gr[i], j)) : D;
                 odh[j] = narrow(a2 * D);
                 ody[j] = narrow(rp2 * fma2(yn[i][j], k2, Dg * wp[i][j]));
@@ -394,8 +420,10 @@ __global__ void __launch_bounds__(kNrBwdThreads) norm_residual_bwd_kernel(const 
             float x, y;
             split(sp[i][j], x, y);
             *reinterpret_cast<float2*>(base + 2 * j) = make_float2(x, y);
-            split(sq[i][j], x, y);
-            *reinterpret_cast<float2*>(base + p.H + 2 * j) = make_float2(x, y);
+            if (PRE) {
+                split(sq[i][j], x, y);
+                *reinterpret_cast<float2*>(base + p.H + 2 * j) = make_float2(x, y);
+            }
         }
     }
 }
@@ -404,14 +432,15 @@ __global__ void __launch_bounds__(kNrBwdThreads) norm_residual_bwd_kernel(const 
 // in registers.  A row stays in shared memory until its second pass, which
 // computes the first one's values again (128 registers a thread hold no more),
 // and the columns' weights come from L1.  ST rows are there or on their way.
-// 4096 x 8192: 117 us (403 MB, 62 us of copies), 131 in 1024 threads with half the
-// vectors, 230 with both passes from L2; 2048 x 16384: 140.
-template <int NV, int ST, bool TOKEN>
+// 4096 x 8192: 113 us (403 MB, 62 us of copies), 131 in 1024 threads with half the
+// vectors, 230 with both passes from L2; 2048 x 16384: 126. Without the norm after
+// the update 85 and 74.
+template <int NV, int ST, bool TOKEN, bool PRE>
 __global__ void __launch_bounds__(kNrWideThreads) norm_residual_bwd_wide_kernel(const NrArgs p) {
     let_dependents_launch();
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float sh[2][3 * 32];
-    constexpr int NT = TOKEN ? 5 : 4;                 // tensors of a row: y, h, dh_out, du, gate
+    constexpr int NT = row_tensors(TOKEN, PRE), kGate = NT - 1;   // of a row: y, dh_out, with PRE h and du, gate
     const int nthr = blockDim.x, nvec = p.H / 8;
     const float inv_h = 1.0f / (float)p.H;
     const uint32_t mine = (uint32_t)__cvta_generic_to_shared(smem) + threadIdx.x * 16;
@@ -424,10 +453,12 @@ __global__ void __launch_bounds__(kNrWideThreads) norm_residual_bwd_wide_kernel(
                 const bool ok = c < nvec;
                 const int cc = ok ? c : 0;
                 copy16(place(st, 0, i), vec(p.y, t, p.H) + cc, ok);
-                copy16(place(st, 1, i), vec(p.h, t, p.H) + cc, ok);
-                copy16(place(st, 2, i), vec(p.dh_out, t, p.H) + cc, ok);
-                copy16(place(st, 3, i), (p.du ? vec(p.du, t, p.H) : vec(p.y, t, p.H)) + cc, ok && p.du);
-                if (TOKEN) copy16(place(st, 4, i), vec(p.gate, t, p.H) + cc, ok);
+                copy16(place(st, 1, i), vec(p.dh_out, t, p.H) + cc, ok);
+                if (PRE) {
+                    copy16(place(st, 2, i), vec(p.h, t, p.H) + cc, ok);
+                    copy16(place(st, 3, i), vec(p.du, t, p.H) + cc, ok);
+                }
+                if (TOKEN) copy16(place(st, kGate, i), vec(p.gate, t, p.H) + cc, ok);
             }
         }
         copies_close();
@@ -445,29 +476,38 @@ __global__ void __launch_bounds__(kNrWideThreads) norm_residual_bwd_wide_kernel(
     const uint4 zero = make_uint4(0, 0, 0, 0);
     int st = 0, half = 0;
     for (; t < (size_t)p.T; t += step) {
-        const float rp = __ldg(p.rstd_in + t), rq = p.du ? __ldg(p.rstd_in + p.T + t) : 0.0f;
+        const float rp = __ldg(p.rstd_in + t), rq = PRE ? __ldg(p.rstd_in + p.T + t) : 0.0f;
         const F2 rp2 = f2(rp, rp), rq2 = f2(rq, rq);
         // a vector of the row: both passes take the same values from it
         auto values = [&](int i, auto use) {
             const int c = threadIdx.x + i * nthr;
             const bool ok = c < nvec;
             const uint4 w1 = ok ? __ldg(vec(p.gamma_post, 0, p.H) + c) : zero;
-            const uint4 w2 = ok && p.du ? __ldg(vec(p.gamma_pre, 0, p.H) + c) : zero;
+            const uint4 w2 = PRE && ok ? __ldg(vec(p.gamma_pre, 0, p.H) + c) : zero;
             uint4 gr;
             if (TOKEN)
-                gr = lds128(place(st, 4, i));
+                gr = lds128(place(st, kGate, i));
             else
                 gr = ok && p.gate_mode == MOE_GATE_CHANNEL ? __ldg(vec(p.gate, 0, p.H) + c)
                                                            : make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
-            const uint4 yr = lds128(place(st, 0, i)), hr = lds128(place(st, 1, i)), dr = lds128(place(st, 2, i)),
-                        ur = lds128(place(st, 3, i));
+            const uint4 yr = lds128(place(st, 0, i)), dr = lds128(place(st, 1, i));
+            uint4 hr, ur;
+            if (PRE) {
+                hr = lds128(place(st, 2, i));
+                ur = lds128(place(st, 3, i));
+            }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const F2 g = widen(word(gr, j)), wg = widen(word(w1, j));
                 const F2 yn = widen(word(yr, j)) * rp2, w = g * (wg * yn);
-                const F2 hn = fma2(a2, widen(word(hr, j)), w) * rq2;
-                const F2 u = widen(word(ur, j)), q = u * widen(word(w2, j));
-                use(j, g, wg, yn, w, hn, u, q, fma2(rq2, q, widen(word(dr, j))));
+                F2 hn = f2(0.0f, 0.0f), u = hn, q = hn, dq = widen(word(dr, j));
+                if (PRE) {
+                    hn = fma2(a2, widen(word(hr, j)), w) * rq2;
+                    u = widen(word(ur, j));
+                    q = u * widen(word(w2, j));
+                    dq = fma2(rq2, q, dq);
+                }
+                use(j, g, wg, yn, w, hn, u, q, dq);
             }
         };
         copies_left<ST - 1>();
@@ -475,22 +515,32 @@ __global__ void __launch_bounds__(kNrWideThreads) norm_residual_bwd_wide_kernel(
 #pragma unroll
         for (int i = 0; i < NV; ++i)
             values(i, [&](int j, F2, F2, F2, F2 w, F2 hn, F2 u, F2 q, F2 dq) {
-                x0 = fma2(q, hn, x0);
                 x1 = fma2(w, dq, x1);
-                x2 = fma2(w, hn, x2);
-                sq[i][j] = fma2(u, hn, sq[i][j]);
+                if (PRE) {
+                    x0 = fma2(q, hn, x0);
+                    x2 = fma2(w, hn, x2);
+                    sq[i][j] = fma2(u, hn, sq[i][j]);
+                }
             });
-        float s[3] = {total(x0), total(x1), total(x2)};
+        float s[PRE ? 3 : 1] = {total(x1)};
+        if constexpr (PRE) {
+            s[1] = total(x0);
+            s[2] = total(x2);
+        }
         block_sum(s, sh[half]);
         half ^= 1;
-        const float c1 = s[0] * inv_h, c2 = (s[1] - rq * c1 * s[2]) * inv_h;
+        float c1 = 0.0f, c2 = s[0] * inv_h;
+        if constexpr (PRE) {
+            c1 = s[1] * inv_h;
+            c2 = (s[0] - rq * c1 * s[2]) * inv_h;
+        }
         const F2 k1 = f2(-rq * c1, -rq * c1), k2 = f2(-c2, -c2);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = threadIdx.x + i * nthr;
             uint32_t odh[4], ody[4], odg[4];
             values(i, [&](int j, F2 g, F2 wg, F2 yn, F2, F2 hn, F2, F2, F2 dq) {
-                const F2 D = fma2(hn, k1, dq);
+                const F2 D = PRE ? fma2(hn, k1, dq) : dq;
                 const F2 Dg = D * g;
                 odh[j] = narrow(a2 * D);
                 ody[j] = narrow(rp2 * fma2(yn, k2, Dg * wg));
@@ -518,8 +568,10 @@ __global__ void __launch_bounds__(kNrWideThreads) norm_residual_bwd_wide_kernel(
             float x, y;
             split(sp[i][j], x, y);
             *reinterpret_cast<float2*>(base + 2 * j) = make_float2(x, y);
-            split(sq[i][j], x, y);
-            *reinterpret_cast<float2*>(base + p.H + 2 * j) = make_float2(x, y);
+            if (PRE) {
+                split(sq[i][j], x, y);
+                *reinterpret_cast<float2*>(base + p.H + 2 * j) = make_float2(x, y);
+            }
         }
     }
 }
@@ -638,31 +690,40 @@ moe_status_t run_forward(const NrArgs& p, cudaStream_t s) {
     return launch_forward<1, kNrStages, 1024, TOKEN>(p, threads, s);
 }
 
-template <int NV, bool TOKEN>
+template <int NV, bool TOKEN, bool PRE>
 moe_status_t launch_backward(const NrArgs& p, cudaStream_t s) {
     const int threads = bwd_threads(p.H);
-    const int smem = kNrStages * (TOKEN ? 5 : 4) * NV * threads * 16;
-    const cudaError_t e = cudaFuncSetAttribute(norm_residual_bwd_kernel<NV, TOKEN>,
+    const int smem = kNrStages * row_tensors(TOKEN, PRE) * NV * threads * 16;
+    const cudaError_t e = cudaFuncSetAttribute(norm_residual_bwd_kernel<NV, TOKEN, PRE>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return nfail(MOE_ERR_CUDA, "norm_residual backward: %s", cudaGetErrorString(e));
-    norm_residual_bwd_kernel<NV, TOKEN><<<p.blocks, threads, smem, s>>>(p);
+    norm_residual_bwd_kernel<NV, TOKEN, PRE><<<p.blocks, threads, smem, s>>>(p);
     return MOE_OK;
 }
 
-// Two rows in shared memory where they fit, up to 11 or 13 thousand columns.
-template <bool TOKEN>
+// Two rows in shared memory where they fit, up to 11 or 13 thousand columns
+// (without the norm after the update they always do: three tensors of 16384
+// columns are 96 KB).
+template <bool TOKEN, bool PRE>
 moe_status_t launch_backward_wide(const NrArgs& p, cudaStream_t s) {
     const int nv = p.H <= 16 * kNrWideThreads ? 2 : 4;
     const int threads = ((p.H / 8 + nv - 1) / nv + 31) / 32 * 32;
-    const int row = (TOKEN ? 5 : 4) * nv * threads * 16;
-    const int st = 2 * row <= kNrWideSmem ? 2 : 1;
-    auto* kernel = nv == 2 ? norm_residual_bwd_wide_kernel<2, 2, TOKEN>
-                   : st == 2 ? norm_residual_bwd_wide_kernel<4, 2, TOKEN>
-                             : norm_residual_bwd_wide_kernel<4, 1, TOKEN>;
+    const int row = row_tensors(TOKEN, PRE) * nv * threads * 16;
+    const int st = !PRE || 2 * row <= kNrWideSmem ? 2 : 1;
+    auto* kernel = nv == 2 ? norm_residual_bwd_wide_kernel<2, 2, TOKEN, PRE> : norm_residual_bwd_wide_kernel<4, 2, TOKEN, PRE>;
+    if constexpr (PRE)
+        if (st == 1) kernel = norm_residual_bwd_wide_kernel<4, 1, TOKEN, PRE>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, st * row);
     if (e != cudaSuccess) return nfail(MOE_ERR_CUDA, "norm_residual backward: %s", cudaGetErrorString(e));
     kernel<<<p.blocks, threads, st * row, s>>>(p);
     return MOE_OK;
+}
+
+template <bool TOKEN, bool PRE>
+moe_status_t run_backward(const NrArgs& p, cudaStream_t s) {
+    if (p.H <= kNrBwdShort) return launch_backward<1, TOKEN, PRE>(p, s);
+    if (p.H <= 16 * kNrBwdThreads) return launch_backward<2, TOKEN, PRE>(p, s);
+    return launch_backward_wide<TOKEN, PRE>(p, s);
 }
 
 }  // namespace
@@ -788,13 +849,10 @@ moe_status_t moe_norm_residual_backward(const moe_config_t* cfg, const void* h, 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (p.T > 0) {
         const bool token = gate_mode == MOE_GATE_TOKEN;
-        if (p.H <= kNrBwdShort) {
-            NR_TRY((token ? launch_backward<1, true>(p, s) : launch_backward<1, false>(p, s)));
-        } else if (p.H <= 16 * kNrBwdThreads) {
-            NR_TRY((token ? launch_backward<2, true>(p, s) : launch_backward<2, false>(p, s)));
-        } else {
-            NR_TRY((token ? launch_backward_wide<true>(p, s) : launch_backward_wide<false>(p, s)));
-        }
+        if (du)
+            NR_TRY((token ? run_backward<true, true>(p, s) : run_backward<false, true>(p, s)));
+        else
+            NR_TRY((token ? run_backward<true, false>(p, s) : run_backward<false, false>(p, s)));
         NR_TRY(launched("norm_residual backward launch: %s"));
     }
     // with no rows the sums are zero

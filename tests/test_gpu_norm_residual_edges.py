@@ -1,0 +1,48 @@
+"""The norms around a block, with gate and residual scale, where values are not finite."""
+import math
+
+import pytest
+import torch
+
+from test_gpu_norm_residual import MODES, backward, check_backward, forward, make
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def B():
+    from sigmoid_top_routing_warp_b200 import binding
+    return binding
+
+
+@pytest.mark.parametrize("H", [264, 2568, 6152, 9000, 16384])
+@pytest.mark.parametrize("gate", MODES)
+def test_without_the_next_norm_h_reaches_no_gradient(B, H, gate):
+    """D is dh' alone then: an infinity or a NaN in h leaves every gradient as the formula has it."""
+    T = 5
+    d = make(T, H, gate, False, seed=11)
+    _, _, rstd = forward(B, d, T, H, gate, 0.75)
+    d["h"][1, 3] = math.inf
+    d["h"][2, H - 1] = -math.inf
+    d["h"][4, 77] = math.nan
+    got = backward(B, d, T, H, gate, 0.75, rstd)
+    torch.cuda.synchronize()
+    check_backward(d, T, H, gate, 0.75, rstd, got)
+
+
+@pytest.mark.parametrize("H", [264, 2568, 6152])
+def test_non_finite_rows_stay_in_their_rows(B, H):
+    """With the next norm an infinity in h or in a gradient belongs to the gradients of its row and to
+    the sums over the rows."""
+    T = 7
+    d = make(T, H, "token", True, seed=12)
+    _, _, rstd = forward(B, d, T, H, "token", 1.0)
+    clean = backward(B, d, T, H, "token", 1.0, rstd)
+    d["h"][2, 5] = math.inf
+    d["du"][4, 6] = math.nan
+    got = backward(B, d, T, H, "token", 1.0, rstd)
+    torch.cuda.synchronize()
+    for n in ("dh", "dy", "dgate"):
+        for t in (0, 1, 3, 5, 6):
+            assert torch.equal(got[n][t], clean[n][t])
+        assert not bool(got[n][2].isfinite().any()) and not bool(got[n][4].isfinite().any())
