@@ -312,6 +312,8 @@ moe_status_t moe_forward_block(const moe_config_t* cfg, const void* h, const voi
  *     4-bit weights), every sum is fp32, and out is rounded once.  Where two
  *     keys lie within fp32 rounding of each other moe_route may choose
  *     differently;
+ *   - a SwiGLU output beyond binary32's range is an infinity, and the outputs
+ *     that it reaches are what its weights make of it (0 times infinity: NaN);
  *   - with 8- and 4-bit weights a token is multiplied as binary16 scaled by a
  *     power of two of its own: a value below 2^-28 of the token's largest is
  *     off by up to 2^-39 of the largest.

@@ -104,6 +104,7 @@ constexpr int kBox = 256;                        // K columns of one tensor copy
 constexpr int kBoxBytes = 8192;                  // its bytes, for every weight type
 constexpr int kSlice = 64;                       // K columns of a warp in a stage
 constexpr int kMaxStages = 8;
+constexpr float kBf16Max = 0x1.fep+127f;
 constexpr int kBarWord = moe::kSchedFirstWord;   // grid barriers (2) and the exit count, in the status block
 
 // Per weight type: rows of a unit, bits of a weight, bytes of a stage's scales
@@ -1497,9 +1498,10 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
 #pragma unroll
                         for (int q = 1; q < MT; ++q) top = max(top, top_sh[q][tile][2 * t + j]);
                         const uint32_t lift = min(268u - (top >> 23), 253u);
-                        // head and tail: together 22 significand bits
+                        // head and tail: together 22 significand bits; an infinity has no tail
                         const float x = v[j] * __uint_as_float(lift << 23);
-                        const __half hi = __float2half_rn(x), lo = __float2half_rn(x - __half2float(hi));
+                        const __half hi = __float2half_rn(x);
+                        const __half lo = __float2half_rn(isinf(x) ? 0.0f : x - __half2float(hi));
                         const size_t pair = act.base + c, at = pair * a.ld_act + f;
                         a.act_hi[at] = __half_as_ushort(hi);
                         a.act_lo[at] = __half_as_ushort(lo);
@@ -1511,9 +1513,13 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
                     for (int j = 0; j < 2; ++j) {
                         const int c = 8 * tile + 2 * t + j;
                         if (c >= count) continue;
-                        // head and tail: together 16 significand bits
-                        const __nv_bfloat16 hi = __float2bfloat16_rn(v[j]);
-                        const __nv_bfloat16 lo = __float2bfloat16_rn(v[j] - __bfloat162float(hi));
+                        // head and tail: together 16 significand bits.  Above bf16's largest
+                        // value the tail takes the rest; an infinity has no tail, and a NaN
+                        // is in the tail at least.
+                        const bool inf = isinf(v[j]);
+                        const float top = fminf(fmaxf(v[j], -kBf16Max), kBf16Max);
+                        const __nv_bfloat16 hi = __float2bfloat16_rn(inf ? v[j] : top);
+                        const __nv_bfloat16 lo = __float2bfloat16_rn(inf ? 0.0f : v[j] - __bfloat162float(hi));
                         const size_t at = (size_t)(act.base + c) * a.ld_act + f;
                         a.act_hi[at] = __bfloat16_as_ushort(hi);
                         a.act_lo[at] = __bfloat16_as_ushort(lo);

@@ -1,10 +1,12 @@
 """The few-token layer (moe_forward_few) where its inputs or its shape reach an edge:
 stages of several widths in one slot of its ring, a call that
-gives up."""
+gives up, SwiGLU outputs at the end of their range."""
+import math
+
 import pytest
 import torch
 
-from test_gpu_few import KINDS, call, check, make
+from test_gpu_few import KINDS, call, check, make, reference
 
 pytestmark = pytest.mark.gpu
 
@@ -53,3 +55,57 @@ def test_a_stalled_call_leaves_nothing_behind(B, kind):
     call(B, p)
     check(B, p)
     assert torch.equal(p["out"], first)
+
+
+@pytest.mark.parametrize("T", [1, 3, 6, 12])
+@pytest.mark.parametrize("n_shared", [0, 1])
+@pytest.mark.parametrize("kind,end", [("bf16", "finite"), ("bf16", "infinite"), ("fp8", "infinite"),
+                                      ("mxfp4", "infinite")])
+def test_swiglu_outputs_at_the_end_of_their_range(B, kind, T, n_shared, end):
+    """One feature of token 0's SwiGLU output is just below 2^128, above bf16's largest value with bf16
+    weights, or infinite: the outputs are the formula's, an infinity times a weight its sign's infinity."""
+    H, I, f, col, e = 256, 128, 5, 6, 7
+    bias = torch.zeros(32, device="cuda")
+    bias[e] = 5.0
+    p = make(B, kind, T, H, 32, 1, I, n_shared=n_shared, bias=bias, seed=73)
+    p["w_router"].zero_()
+    stored, scale, vals = p["w13"]
+    pack = 2 if kind == "mxfp4" else 1
+    stored[:, :, col // pack] = 0                    # (its neighbour's codes too, for MXFP4)
+    vals[:, :, col:col + pack] = 0
+    if n_shared:
+        p["w13s"][0][:, col // pack] = 0
+        p["w13s"][2][:, col:col + pack] = 0
+    if kind == "bf16":
+        for row, v in ((f, 181.0 / 128.0), (I + f, 181.0 / 256.0)):      # 181^2 / 2^14 is above 2 - 2^-8
+            stored[:, row, col] = v
+            vals[:, row, col] = v
+    elif kind == "fp8":
+        stored[:, (f, I + f), col] = 0x38            # 1.0
+        vals[:, (f, I + f), col] = scale[:, (0, 1), 0].cpu().double()
+    else:
+        stored[:, (f, I + f), col // 2] = 0x02       # 1.0 in the lower half
+        vals[:, (f, I + f), col] = torch.exp2(scale[:, (f, I + f), col // 32].cpu().double() - 127.0)
+    unit = float(vals[e, f, col] * vals[e, I + f, col])
+    p["x"][0] = 0
+    n = math.ceil((128.0 - math.log2(unit)) / 2.0) - 1       # the largest with unit * 4^n below 2^128
+    p["x"][0, col] = 2.0 ** (n if end == "finite" else n + 1)
+    a = unit * float(p["x"][0, col]) ** 2
+    assert (2.0 ** 126 <= a < 2.0 ** 128) if end == "finite" else a >= 2.0 ** 128
+    if kind == "bf16" and end == "finite":
+        assert a > float(torch.finfo(torch.bfloat16).max)
+    call(B, p)
+    torch.cuda.synchronize()
+    B.moe_check_device_status(p["ws"])
+    assert p["idx"].cpu().tolist() == [[e]] * T
+    out, tol, _, _ = reference(p)
+    got = p["out"].cpu().double()
+    if end == "infinite":
+        # 0 times infinity is a NaN; the shared expert's part is zero
+        w2 = p["w2"][2][e, :, f]
+        want = torch.where(w2 == 0, torch.full_like(w2, math.nan), torch.sign(w2) * math.inf)
+        assert torch.equal(got[0].isnan(), want.isnan())
+        assert torch.equal(got[0][~want.isnan()], want[~want.isnan()])
+        got, out, tol = got[1:], out[1:], tol[1:]
+    err = (got - out).abs()
+    assert bool((err <= tol).all()), float((err / tol).max())
