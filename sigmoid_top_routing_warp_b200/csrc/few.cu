@@ -105,6 +105,11 @@ constexpr int kBoxBytes = 8192;                  // its bytes, for every weight 
 constexpr int kSlice = 64;                       // K columns of a warp in a stage
 constexpr int kMaxStages = 8;
 constexpr float kBf16Max = 0x1.fep+127f;
+// Phase 2's sums over 8- and 4-bit weights are held times 2^-kDownShift: a sum
+// of codes times a lifted output reaches 2^24 times the output (2^15 by 448 by
+// a few terms) before it meets the weights' scale, and must not overflow there.
+// (An output is lifted by at most 2^102 then: off by 2^-127 at most for it.)
+constexpr int kDownShift = 24;
 constexpr int kBarWord = moe::kSchedFirstWord;   // grid barriers (2) and the exit count, in the status block
 
 // Per weight type: rows of a unit, bits of a weight, bytes of a stage's scales
@@ -1497,7 +1502,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
                         uint32_t top = top_sh[0][tile][2 * t + j];
 #pragma unroll
                         for (int q = 1; q < MT; ++q) top = max(top, top_sh[q][tile][2 * t + j]);
-                        const uint32_t lift = min(268u - (top >> 23), 253u);
+                        const uint32_t lift = min(268u - (top >> 23), 253u - kDownShift);
                         // head and tail: together 22 significand bits; an infinity has no tail
                         const float x = v[j] * __uint_as_float(lift << 23);
                         const __half hi = __float2half_rn(x);
@@ -1506,7 +1511,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
                         a.act_hi[at] = __half_as_ushort(hi);
                         a.act_lo[at] = __half_as_ushort(lo);
                         if (m == 0 && g == 0)
-                            a.ainv[pair * (a.ld_act / NF) + f0 / NF] = __uint_as_float((254u - lift) << 23);
+                            a.ainv[pair * (a.ld_act / NF) + f0 / NF] = __uint_as_float((254u - kDownShift - lift) << 23);
                     }
                 } else {
 #pragma unroll
@@ -1586,7 +1591,8 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
                         s.w += __shfl_down_sync(0xffffffffu, s.w, 2);
                     }
                     const int r = rd / NT * 16 + g, c0 = rd % NT * 8 + 2 * t;
-                    const float v[4] = {s.x, s.y, s.z, s.w};
+                    constexpr float kUp = F::kInvBytes ? (float)(1 << kDownShift) : 1.0f;
+                    const float v[4] = {s.x * kUp, s.y * kUp, s.z * kUp, s.w * kUp};
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const int tok = c0 + (j & 1), row = r + (j >> 1) * 8;
