@@ -305,13 +305,15 @@ moe_status_t moe_forward_block(const moe_config_t* cfg, const void* h, const voi
  *   - dtype may also be MOE_DTYPE_MXFP4_BLOCK32, and activations stay bf16
  *     for every weight type (no moe_quantize_act step: nothing here is bound
  *     by the matrix rate);
- *   - nothing is rounded between the steps: logits, scores, the choice and the
- *     routing weights are computed in binary64 (topk_w is rounded to fp32
- *     once; equal keys take the lower expert, NaN keys rank below numbers),
- *     the SwiGLU outputs are carried with 16 significand bits (22 with 8- and
- *     4-bit weights), every sum is fp32, and out is rounded once.  Where two
- *     keys lie within fp32 rounding of each other moe_route may choose
- *     differently;
+ *   - logits, scores, the choice and the routing weights are computed in
+ *     binary64 (a product of x and the router beyond binary32's range counts
+ *     as infinite; topk_w is rounded to fp32 once; equal keys take the lower
+ *     expert, NaN keys rank below numbers).  Where two keys lie within fp32
+ *     rounding of each other moe_route may choose differently;
+ *   - the expert products' sums are fp32 and out is rounded once; between the
+ *     two products the SwiGLU outputs are rounded to 16 significand bits, a
+ *     head and a tail in bf16 (to 22 with 8- and 4-bit weights, binary16),
+ *     where moe_forward rounds them to 8;
  *   - a SwiGLU output beyond binary32's range is an infinity, and the outputs
  *     that it reaches are what its weights make of it (0 times infinity: NaN);
  *   - with 8- and 4-bit weights a token is multiplied as binary16 scaled by a

@@ -1,6 +1,6 @@
 """The few-token layer (moe_forward_few) where its inputs or its shape reach an edge:
 stages of several widths in one slot of its ring, a call that
-gives up, SwiGLU outputs at the end of their range."""
+gives up, SwiGLU outputs at the end of their range, logits that cancel or tie."""
 import math
 
 import pytest
@@ -109,3 +109,41 @@ def test_swiglu_outputs_at_the_end_of_their_range(B, kind, T, n_shared, end):
         got, out, tol = got[1:], out[1:], tol[1:]
     err = (got - out).abs()
     assert bool((err <= tol).all()), float((err / tol).max())
+
+
+@pytest.mark.parametrize("T", [1, 3, 9])
+@pytest.mark.parametrize("H", [384, 5120])
+def test_weights_of_cancelling_channels(B, T, H):
+    """Two channels of +-4096 cancel in every logit: the choice and its weights are binary64's, rounded
+    once (a binary64 sum of H products is off by H * 2^-53 of their magnitudes, about 2^-30 here)."""
+    p = make(B, "bf16", T, H, 32, 4, 128, seed=79 + T)
+    for a, b in ((8, 9), (40, 300), (H - 1, H - 7)):
+        p["x"][:, a] = 4096.0
+        p["x"][:, b] = -4096.0
+        p["w_router"][:, b] = p["w_router"][:, a]
+    call(B, p)
+    torch.cuda.synchronize()
+    x, wr = p["x"].cpu().double(), p["w_router"].cpu().double()
+    slack = float(H * 2.0 ** -53 * (x.abs() @ wr.abs().T).max())
+    assert slack < 2.0 ** -28
+    _, _, idx, w = reference(p)
+    assert torch.equal(p["idx"].cpu(), idx)
+    # d(score)/score is at most d(logit), once more in the sum
+    err = (p["w"].cpu().double() - w).abs()
+    assert bool((err <= (2.0 ** -24 + 2 * slack + 2.0 ** -48) * w).all()), float((err / w).max())
+
+
+@pytest.mark.parametrize("H", [256, 5120])
+def test_permuted_router_rows_tie(B, H):
+    """Experts whose products are the same in another order have equal keys: the lower ones are chosen."""
+    p = make(B, "bf16", 2, H, 32, 5, 128, bias=torch.zeros(32, device="cuda"), seed=83)
+    g = torch.Generator(device="cuda").manual_seed(89)
+    row = p["w_router"][0].clone()
+    for e in range(32):
+        p["w_router"][e] = row[torch.randperm(H, generator=g, device="cuda")]
+    p["x"][0] = 171.0 / 128.0
+    p["x"][1] = -201.0 / 128.0
+    call(B, p)
+    torch.cuda.synchronize()
+    assert p["idx"].cpu().tolist() == [[0, 1, 2, 3, 4]] * 2
+    assert bool((p["w"] == p["w"][0, 0]).all())
