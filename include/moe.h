@@ -307,8 +307,9 @@ moe_status_t moe_forward_block(const moe_config_t* cfg, const void* h, const voi
  *     by the matrix rate);
  *   - logits, scores, the choice and the routing weights are computed in
  *     binary64 (a product of x and the router beyond binary32's range counts
- *     as infinite; topk_w is rounded to fp32 once; equal keys take the lower
- *     expert, NaN keys rank below numbers).  Where two keys lie within fp32
+ *     as infinite, a logit below -708 as -708, where moe_route stops at -86;
+ *     topk_w is rounded to fp32 once; equal keys take the lower expert, NaN
+ *     keys rank below numbers).  Where two keys lie within fp32
  *     rounding of each other moe_route may choose differently;
  *   - the expert products' sums are fp32 and out is rounded once; between the
  *     two products the SwiGLU outputs are rounded to 16 significand bits, a

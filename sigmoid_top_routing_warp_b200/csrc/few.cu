@@ -1354,7 +1354,9 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
                     for (int j = 0; j < 4; ++j) {
                         const int i = rid + j * kTeam;
                         if (i >= nt * a.E) continue;
-                        const double s = 1.0 / (1.0 + exp(-l[j]));
+                        // at -708 exp still has a finite value: scores stay positive, so
+                        // that a sum of chosen ones can be divided by (a NaN passes)
+                        const double s = 1.0 / (1.0 + exp(l[j] < -708.0 ? 708.0 : -l[j]));
                         S.scores[i] = s;
                         S.keys[i] = sortable(s + (double)bias[j]);
                     }

@@ -1,6 +1,7 @@
 """The few-token layer (moe_forward_few) where its inputs or its shape reach an edge:
 stages of several widths in one slot of its ring, a call that
-gives up, SwiGLU outputs at the end of their range, logits that cancel or tie."""
+gives up, SwiGLU outputs at the end of their range, logits that cancel, tie
+or leave no score."""
 import math
 
 import pytest
@@ -147,3 +148,25 @@ def test_permuted_router_rows_tie(B, H):
     torch.cuda.synchronize()
     assert p["idx"].cpu().tolist() == [[0, 1, 2, 3, 4]] * 2
     assert bool((p["w"] == p["w"][0, 0]).all())
+
+
+@pytest.mark.parametrize("norm", [True, False])
+def test_a_token_whose_scores_all_vanish(B, norm):
+    """Every logit below -709, where a score underflows to zero in binary64: equal weights with
+    norm_topk_prob, as moe_forward has them, zero without; the other tokens as ever."""
+    p = make(B, "bf16", 3, 256, 32, 4, 128, bias=torch.zeros(32, device="cuda"), seed=97, n_shared=0,
+             norm_topk_prob=norm)
+    p["w_router"][:, 0] = -1.0
+    p["x"][1] = 0
+    p["x"][1, 0] = 1024.0
+    call(B, p)
+    torch.cuda.synchronize()
+    assert p["idx"][1].cpu().tolist() == [0, 1, 2, 3]
+    assert p["w"][1].cpu().tolist() == ([0.25] * 4 if norm else [0.0] * 4)
+    c = p["cfg"]
+    ws, out = B.alloc_workspace(c), torch.empty_like(p["out"])
+    B.moe_forward(c, p["x"], p["w_router"], p["bias"], p["w13"][0], p["w2"][0], None, None, out, ws)
+    torch.cuda.synchronize()
+    assert torch.equal(B.ws_view(ws, c, "topk_idx"), p["idx"])
+    a, b = p["out"].double(), out.double()
+    assert bool(a.isfinite().all()) and float((a - b).norm() / b.norm()) <= 1e-2
