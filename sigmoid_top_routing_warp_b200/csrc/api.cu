@@ -196,6 +196,12 @@ EncodeTiledFn encode_fn() {
             q == cudaDriverEntryPointSuccess)
             fn = reinterpret_cast<EncodeTiledFn>(p);
     }
+    // The driver wants a context, which a host thread has from its first runtime
+    // call that needs one; a map may come before that.  Choosing the current
+    // device again gives the thread its context.
+    thread_local bool bound = false;
+    int dev = 0;
+    if (fn && !bound) bound = cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess;
     return fn;
 }
 
