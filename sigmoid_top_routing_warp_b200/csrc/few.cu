@@ -1808,7 +1808,9 @@ moe_status_t launch_few(FewArgs& a, cudaStream_t s) {
     if (e == cudaSuccess) {
         size_t smem = 0;
         FEW_TRY((few_smem<DT, NT>(a, optin - kStaticSmem, &smem)));
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        // the kernel's limit is the process's: always the same one, or a call of
+        // another size in another thread could lower it before this launch
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, optin - kStaticSmem);
         if (e == cudaSuccess) {
             void* args[] = {&a};
             const int grid = sms < kMaxBlocks ? sms : kMaxBlocks;

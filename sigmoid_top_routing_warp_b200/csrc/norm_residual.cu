@@ -662,13 +662,22 @@ moe_status_t launched(const char* what) {
     return nfail(MOE_ERR_CUDA, what, cudaGetErrorString(e));
 }
 
+// A kernel's limit of dynamic shared memory is the process's: always the most
+// that its variant takes, or a call of another size in another thread could
+// lower it between this and the launch.
+template <class Kernel>
+cudaError_t smem_limit(Kernel* kernel, int most) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+}
+
 template <int NV, int ST, int THREADS, bool TOKEN>
 moe_status_t launch_forward(const NrArgs& p, int threads, cudaStream_t s) {
     auto* kernel = norm_residual_kernel<NV, ST, THREADS, TOKEN>;
-    const int smem = ST * (TOKEN ? 3 : 2) * NV * threads * 16;
+    constexpr int per_thread = ST * (TOKEN ? 3 : 2) * NV * 16;
+    const int smem = per_thread * threads;
     int sms = 0, fit = 1;
     NR_TRY(moe::api_sm_count(&sms));
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = smem_limit(kernel, per_thread * THREADS);
     if (e == cudaSuccess && p.T > sms) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kernel, threads, smem);
     if (e != cudaSuccess) return nfail(MOE_ERR_CUDA, "norm_residual: %s", cudaGetErrorString(e));
     const int most = sms * (fit > 0 ? fit : 1);
@@ -693,9 +702,9 @@ moe_status_t run_forward(const NrArgs& p, cudaStream_t s) {
 template <int NV, bool TOKEN, bool PRE>
 moe_status_t launch_backward(const NrArgs& p, cudaStream_t s) {
     const int threads = bwd_threads(p.H);
-    const int smem = kNrStages * row_tensors(TOKEN, PRE) * NV * threads * 16;
-    const cudaError_t e = cudaFuncSetAttribute(norm_residual_bwd_kernel<NV, TOKEN, PRE>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    constexpr int per_thread = kNrStages * row_tensors(TOKEN, PRE) * NV * 16;
+    const int smem = per_thread * threads;
+    const cudaError_t e = smem_limit(norm_residual_bwd_kernel<NV, TOKEN, PRE>, per_thread * kNrBwdThreads);
     if (e != cudaSuccess) return nfail(MOE_ERR_CUDA, "norm_residual backward: %s", cudaGetErrorString(e));
     norm_residual_bwd_kernel<NV, TOKEN, PRE><<<p.blocks, threads, smem, s>>>(p);
     return MOE_OK;
@@ -713,7 +722,7 @@ moe_status_t launch_backward_wide(const NrArgs& p, cudaStream_t s) {
     auto* kernel = nv == 2 ? norm_residual_bwd_wide_kernel<2, 2, TOKEN, PRE> : norm_residual_bwd_wide_kernel<4, 2, TOKEN, PRE>;
     if constexpr (PRE)
         if (st == 1) kernel = norm_residual_bwd_wide_kernel<4, 1, TOKEN, PRE>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, st * row);
+    const cudaError_t e = smem_limit(kernel, kNrWideSmem);
     if (e != cudaSuccess) return nfail(MOE_ERR_CUDA, "norm_residual backward: %s", cudaGetErrorString(e));
     kernel<<<p.blocks, threads, st * row, s>>>(p);
     return MOE_OK;
