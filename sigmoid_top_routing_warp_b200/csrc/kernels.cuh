@@ -21,6 +21,17 @@ constexpr int kStatusWords = 64;
 constexpr int kSchedFirstWord = 16;
 cudaError_t reset_claim_counters(int* status, cudaStream_t s);
 
+// A caller's buffer (n bytes; NULL or empty: none), for checks of the arguments.
+struct Span {
+    const void* p;
+    size_t n;
+    const char* name;
+};
+inline bool overlap(const Span& a, const Span& b) {
+    const char *p = static_cast<const char*>(a.p), *q = static_cast<const char*>(b.p);
+    return p && q && a.n && b.n && p < q + b.n && q < p + a.n;
+}
+
 // ---------------------------------------------------------------- router
 struct RouteArgs {
     const float* logits;  // [n_split, T, E]: logits, or K-slice partials summed in order

@@ -137,6 +137,13 @@ moe_status_t mx_check(const void* x, const void* q, const void* scale, int32_t r
             return moe::api_fail(MOE_ERR_INVALID_ARG, msg);
         }
     }
+    const size_t n = (size_t)rows * cols;
+    const moe::Span span[] = {{x, 2 * n, "x"}, {q, n / 2, "q"}, {scale, n / 32, "scale"}};
+    for (int i = 0; i < 3; ++i)
+        if (moe::overlap(span[i], span[(i + 1) % 3])) {
+            snprintf(msg, sizeof(msg), "%s overlaps %s", span[i].name, span[(i + 1) % 3].name);
+            return moe::api_fail(MOE_ERR_INVALID_ARG, msg);
+        }
     return MOE_OK;
 }
 
