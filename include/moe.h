@@ -332,6 +332,7 @@ moe_status_t moe_forward_block(const moe_config_t* cfg, const void* h, const voi
  *   ws        moe_few_workspace_size bytes, 256-byte aligned, zero-filled
  *             before its first use (every completed call leaves its counters
  *             at zero; after an error moe_check_device_status clears them)
+ * What the call writes overlaps no other buffer of it, but for out over x.
  * The result does not depend on scheduling: no float atomics, fixed order.
  * The launch is cooperative (its blocks wait for one another, with a bounded
  * wait), so it needs the whole GPU to itself while it starts; it can be

@@ -1712,6 +1712,39 @@ moe_status_t few_check(const moe_config_t* c) {
     return MOE_OK;
 }
 
+// What the call writes may overlap nothing else but out x.
+moe_status_t few_apart(const moe_config_t* c, const void* x, const void* w_router, const float* bias, const void* w13,
+                       const void* s13, const void* w2, const void* s2, const void* w13s, const void* s13s,
+                       const void* w2s, const void* s2s, const void* out, const int32_t* idx, const float* w,
+                       const void* ws, size_t ws_bytes) {
+    const size_t n = (size_t)c->T * c->H * 2, Is = (size_t)c->n_shared * c->I, nk = (size_t)c->T * c->k * 4;
+    const size_t routed = (size_t)c->E * c->H * c->I, shared = (size_t)c->H * Is;   // elements of a down projection
+    auto stored = [&](size_t v) {
+        return c->dtype == MOE_DTYPE_BF16 ? 2 * v : c->dtype == MOE_DTYPE_MXFP4_BLOCK32 ? v / 2 : v;
+    };
+    auto scales = [&](size_t v) { return c->dtype == MOE_DTYPE_MXFP4_BLOCK32 ? v / 32 : v / (128 * 128) * 4; };
+    const moe::Span in[] = {{x, n, "x"},
+                            {w_router, (size_t)c->E * c->H * 2, "w_router"},
+                            {bias, (size_t)c->E * 4, "bias"},
+                            {w13, stored(2 * routed), "w13"},
+                            {s13, scales(2 * routed), "w13_scale"},
+                            {w2, stored(routed), "w2"},
+                            {s2, scales(routed), "w2_scale"},
+                            {w13s, stored(2 * shared), "w13s"},
+                            {s13s, scales(2 * shared), "w13s_scale"},
+                            {w2s, stored(shared), "w2s"},
+                            {s2s, scales(shared), "w2s_scale"}};
+    const moe::Span outs[] = {{out, n, "out"}, {idx, nk, "topk_idx"}, {w, nk, "topk_w"}, {ws, ws_bytes, "the workspace"}};
+    for (const moe::Span& o : outs) {
+        for (const moe::Span& i : in)
+            if (moe::overlap(o, i) && !(&o == outs && &i == in && o.p == i.p))
+                return ffail(MOE_ERR_INVALID_ARG, "%s overlaps a buffer of the call", o.name);
+        for (const moe::Span& q : outs)
+            if (&q > &o && moe::overlap(o, q)) return ffail(MOE_ERR_INVALID_ARG, "%s overlaps a buffer of the call", o.name);
+    }
+    return MOE_OK;
+}
+
 // Tensor maps of a matrix stored in bytes, rows of `rb` bytes, all of five
 // dimensions.  A box of 256 columns lands as 128-byte pieces of 8 rows (1024
 // bytes, 128-byte swizzle), the pieces along K inside 8-row groups:
@@ -1855,11 +1888,6 @@ moe_status_t moe_forward_few(const moe_config_t* cfg, const void* x, const void*
     FEW_TRY(need(w13, "w13", 16));
     FEW_TRY(need(w2, "w2", 16));
     FEW_TRY(need(out, "out", 16));
-    // out is written when every block has read its tokens
-    const uintptr_t xp = reinterpret_cast<uintptr_t>(x), op = reinterpret_cast<uintptr_t>(out);
-    const size_t bytes = (size_t)cfg->T * cfg->H * 2;
-    if (xp != op && xp < op + bytes && op < xp + bytes)
-        return moe::api_fail(MOE_ERR_INVALID_ARG, "out must be x or not overlap it");
     if (topk_idx) FEW_TRY(need(topk_idx, "topk_idx", 4));
     if (topk_w) FEW_TRY(need(topk_w, "topk_w", 4));
     const bool shared = cfg->n_shared > 0;
@@ -1883,6 +1911,9 @@ moe_status_t moe_forward_few(const moe_config_t* cfg, const void* x, const void*
     const FewLayout L = few_layout(cfg);
     if (ws_bytes < L.total)
         return ffail(MOE_ERR_WORKSPACE, "workspace has too few bytes, %s %lld", "needs", (long long)L.total);
+    // out may be x: it is written when every block has read its tokens
+    FEW_TRY(few_apart(cfg, x, w_router, bias, w13, w13_scale, w2, w2_scale, shared ? w13s : nullptr, w13s_scale,
+                      shared ? w2s : nullptr, w2s_scale, out, topk_idx, topk_w, ws, L.total));
     FewArgs a;
     memset(&a, 0, sizeof(a));
     a.x = static_cast<const uint16_t*>(x);
