@@ -649,11 +649,22 @@ moe_status_t check_common(const moe_config_t* c, const void* h, const void* y, c
     return MOE_OK;
 }
 
-// An output over an input is fine where both start at the same address and the
-// documentation allows it; any other overlap is refused.
-bool overlap(const void* p, size_t pb, const void* q, size_t qb) {
-    const char *a = static_cast<const char*>(p), *b = static_cast<const char*>(q);
-    return a && b && a < b + qb && b < a + pb;
+// An output, and the input that it may be: an overlap with anything else is
+// refused, and with that input one that does not start where it does.
+struct Out {
+    moe::Span s;
+    const void* may;
+};
+template <int NI, int NO>
+moe_status_t apart(const moe::Span (&in)[NI], const Out (&outs)[NO]) {
+    for (const Out& o : outs) {
+        for (const moe::Span& i : in)
+            if (moe::overlap(o.s, i) && !(i.p == o.may && i.p == o.s.p))
+                return nfail(MOE_ERR_INVALID_ARG, "%s overlaps an input", o.s.name);
+        for (const Out& q : outs)
+            if (&q != &o && moe::overlap(o.s, q.s)) return nfail(MOE_ERR_INVALID_ARG, "%s overlaps another output", o.s.name);
+    }
+    return MOE_OK;
 }
 
 moe_status_t launched(const char* what) {
@@ -756,14 +767,15 @@ moe_status_t moe_norm_residual(const moe_config_t* cfg, const void* h, const voi
         NR_TRY(need(gamma_pre, "gamma_pre", 16));
         NR_TRY(need(u, "u", 16));
     }
-    const size_t n = (size_t)cfg->T * cfg->H * 2;
-    if (overlap(u, n, h, n) || overlap(u, n, h_out, n) || (u != y && overlap(u, n, y, n)))
-        return moe::api_fail(MOE_ERR_INVALID_ARG, "u overlaps h, h_out or part of y");
-    if ((h_out != h && overlap(h_out, n, h, n)) || overlap(h_out, n, y, n))
-        return moe::api_fail(MOE_ERR_INVALID_ARG, "h_out overlaps y or part of h");
-    if (gate_mode == MOE_GATE_TOKEN && (overlap(h_out, n, gate, n) || overlap(u, n, gate, n)))
-        return moe::api_fail(MOE_ERR_INVALID_ARG, "h_out or u overlaps the gate");
     if (rstd) NR_TRY(need(rstd, "rstd", 4));
+    const size_t row = (size_t)cfg->H * 2, n = cfg->T * row;
+    const moe::Span in[] = {{h, n, "h"},
+                            {y, n, "y"},
+                            {gamma_post, row, "gamma_post"},
+                            {gate, gate_mode == MOE_GATE_TOKEN ? n : row, "gate"},
+                            {gamma_pre, row, "gamma_pre"}};
+    const Out outs[] = {{{h_out, n, "h_out"}, h}, {{u, n, "u"}, y}, {{rstd, (size_t)cfg->T * (u ? 8 : 4), "rstd"}, nullptr}};
+    NR_TRY(apart(in, outs));
     NrArgs p = {};
     p.h = static_cast<const uint16_t*>(h);
     p.y = static_cast<const uint16_t*>(y);
@@ -816,23 +828,27 @@ moe_status_t moe_norm_residual_backward(const moe_config_t* cfg, const void* h, 
     if (gate_mode == MOE_GATE_NONE && dgate)
         return moe::api_fail(MOE_ERR_INVALID_ARG, "dgate given with MOE_GATE_NONE");
     if (gate_mode == MOE_GATE_CHANNEL || (gate_mode == MOE_GATE_TOKEN && rows)) NR_TRY(need(dgate, "dgate", 16));
-    const size_t n = (size_t)cfg->T * cfg->H * 2;
-    const void* token_gate = gate_mode == MOE_GATE_TOKEN ? gate : nullptr;
-    const void* token_dgate = gate_mode == MOE_GATE_TOKEN ? dgate : nullptr;
-    const struct { const void* p; const char* name; const void* may; } outs[] = {
-        {dh, "dh", dh_out}, {dy, "dy", du}, {token_dgate, "dgate", token_gate}};
-    for (const auto& o : outs) {
-        for (const void* in : {h, y, dh_out, du, token_gate})
-            if (in != o.may ? overlap(o.p, n, in, n) : o.p != in && overlap(o.p, n, in, n))
-                return nfail(MOE_ERR_INVALID_ARG, "%s overlaps an input", o.name);
-        for (const auto& q : outs)
-            if (&q != &o && overlap(o.p, n, q.p, n))
-                return nfail(MOE_ERR_INVALID_ARG, "%s overlaps another output", o.name);
-    }
     NR_TRY(need(ws, "workspace", 256));
     const size_t bytes = (size_t)bwd_blocks(cfg->H) * 2 * cfg->H * 4;
     if (ws_bytes < bytes)
         return nfail(MOE_ERR_WORKSPACE, "workspace too small, %s %lld bytes", "needs", (long long)bytes);
+    const bool token = gate_mode == MOE_GATE_TOKEN;
+    const size_t row = (size_t)cfg->H * 2, n = cfg->T * row;
+    const moe::Span in[] = {{h, n, "h"},
+                            {y, n, "y"},
+                            {gamma_post, row, "gamma_post"},
+                            {gate, token ? n : row, "gate"},
+                            {gamma_pre, row, "gamma_pre"},
+                            {rstd, (size_t)cfg->T * (gamma_pre ? 8 : 4), "rstd"},
+                            {dh_out, n, "dh_out"},
+                            {gamma_pre ? du : nullptr, n, "du"}};
+    const Out outs[] = {{{dh, n, "dh"}, dh_out},
+                        {{dy, n, "dy"}, du},
+                        {{dgate, token ? n : 2 * row, "dgate"}, token ? gate : nullptr},
+                        {{dgamma_post, 2 * row, "dgamma_post"}, nullptr},
+                        {{dgamma_pre, 2 * row, "dgamma_pre"}, nullptr},
+                        {{ws, bytes, "workspace"}, nullptr}};
+    NR_TRY(apart(in, outs));
     NrArgs p = {};
     p.h = static_cast<const uint16_t*>(h);
     p.y = static_cast<const uint16_t*>(y);
@@ -857,7 +873,6 @@ moe_status_t moe_norm_residual_backward(const moe_config_t* cfg, const void* h, 
     if (p.blocks < kNrBwdBlocks) p.blocks = cfg->T < kNrBwdBlocks ? cfg->T : kNrBwdBlocks;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (p.T > 0) {
-        const bool token = gate_mode == MOE_GATE_TOKEN;
         if (du)
             NR_TRY((token ? run_backward<true, true>(p, s) : run_backward<false, true>(p, s)));
         else

@@ -69,3 +69,62 @@ def test_few(B, dtype):
                 s = call(**{o: p})
                 assert refused(B, s) and any(w in B.get_last_error() for w in (words[o], words.get(other, "?"))), \
                     (o, other, p - base[other], B.get_last_error())
+
+
+def every_overlap(B, call, base, size, aligns, may):
+    """Each output (aligns: its alignment) over the ends of each other buffer, but for where it may start."""
+    for o, align in aligns.items():
+        for other in base:
+            if other == o or base[other] is None or base[o] is None:
+                continue
+            spots = {base[other], (base[other] + size[other] - 1) // align * align,
+                     base[other] - (size[o] - 1) // align * align}
+            if may.get(o) == other:
+                spots.discard(base[other])
+            for p in spots:
+                assert refused(B, call(**{o: p})), (o, other, p - base[other], B.get_last_error())
+
+
+def place(size):
+    base, at = {}, 1 << 30
+    for name, n in size.items():
+        base[name] = at if n else None
+        at += (n + 2 * MB) // MB * MB
+    return base
+
+
+@pytest.mark.parametrize("mode", [0, 1, 2])
+@pytest.mark.parametrize("pre", [True, False])
+def test_norms(B, mode, pre):
+    T, H = 6, 512
+    n, row, fp = T * H * 2, H * 2, H * 4
+    c = B.MoeConfig(T=T, H=H, E=32, k=1, I=128)
+    cc = c.c()
+    gate = {0: 0, 1: row, 2: n}[mode]
+    rstd = T * (8 if pre else 4)
+    size = dict(h=n, y=n, gamma_post=row, gate=gate, gamma_pre=row * pre, h_out=n, u=n * pre, rstd=rstd)
+    base = place(size)
+
+    def forward(**over):
+        a = {**base, **over}
+        return B.lib().moe_norm_residual(ctypes.byref(cc), a["h"], a["y"], a["gamma_post"], a["gate"], mode, 1.0,
+                                         1e-6, a["gamma_pre"], a["h_out"], a["u"], a["rstd"], None)
+
+    every_overlap(B, forward, base, size, {"h_out": 16, "u": 16, "rstd": 4}, {"h_out": "h", "u": "y"})
+    size = dict(h=n, y=n, gamma_post=row, gate=gate, gamma_pre=row * pre, rstd=rstd, dh_out=n, du=n * pre, dh=n,
+                dy=n, dgate={0: 0, 1: fp, 2: n}[mode], dgamma_post=fp, dgamma_pre=fp * pre,
+                ws=B.norm_residual_workspace_size(c))
+    base2 = place(size)
+
+    def backward(**over):
+        a = {**base2, **over}
+        return B.lib().moe_norm_residual_backward(
+            ctypes.byref(cc), a["h"], a["y"], a["gamma_post"], a["gate"], mode, 1.0, a["gamma_pre"], a["rstd"],
+            a["dh_out"], a["du"], a["dh"], a["dy"], a["dgate"], a["dgamma_post"], a["dgamma_pre"], a["ws"],
+            size["ws"], None)
+
+    may = {"dh": "dh_out", "dy": "du"}
+    if mode == 2:
+        may["dgate"] = "gate"
+    every_overlap(B, backward, base2, size, {"dh": 16, "dy": 16, "dgate": 16, "dgamma_post": 16, "dgamma_pre": 16,
+                                             "ws": 256}, may)
