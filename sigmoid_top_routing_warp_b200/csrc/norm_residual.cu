@@ -596,11 +596,12 @@ __global__ void __launch_bounds__(NW * 32) norm_residual_cols_kernel(const NrArg
     for (int i = 1; i < NW; ++i) s += sh[i][threadIdx.x];
     if (which == 1) {
         p.dgamma_pre[col] = (float)s;
-    } else if (p.gate_mode == MOE_GATE_CHANNEL) {
+    } else if (p.gate_mode == MOE_GATE_CHANNEL && p.blocks > 0) {   // (of no rows an infinite factor makes nothing)
         p.dgamma_post[col] = (float)(s * (double)__uint_as_float((uint32_t)p.gate[col] << 16));
         static_cast<float*>(p.dgate)[col] = (float)(s * (double)__uint_as_float((uint32_t)p.gamma_post[col] << 16));
     } else {
         p.dgamma_post[col] = (float)s;
+        if (p.gate_mode == MOE_GATE_CHANNEL) static_cast<float*>(p.dgate)[col] = (float)s;
     }
 }
 

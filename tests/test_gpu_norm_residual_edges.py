@@ -46,3 +46,14 @@ def test_non_finite_rows_stay_in_their_rows(B, H):
         for t in (0, 1, 3, 5, 6):
             assert torch.equal(got[n][t], clean[n][t])
         assert not bool(got[n][2].isfinite().any()) and not bool(got[n][4].isfinite().any())
+
+
+def test_no_rows_leave_zero_sums(B):
+    """With no rows the sums are zero whatever the gate and the weights are."""
+    H = 64
+    d = make(0, H, "channel", True)
+    d["gate"][3], d["gate"][5], d["gamma_post"][7] = math.inf, math.nan, -math.inf
+    got = backward(B, d, 0, H, "channel", 1.0, torch.empty((2, 0), device="cuda"))
+    torch.cuda.synchronize()
+    for n in ("dgamma_post", "dgamma_pre", "dgate"):
+        assert torch.equal(got[n], torch.zeros(H, device="cuda"))
