@@ -1,10 +1,12 @@
-"""The norms around a block, with gate and residual scale, where values are not finite."""
+"""The norms around a block, with gate and residual scale: values that are not finite, and more rows
+than any grid has blocks."""
 import math
 
 import pytest
 import torch
 
-from test_gpu_norm_residual import MODES, backward, check_backward, forward, make
+from test_gpu_norm_residual import (MODES, backward, cfg_of, check_backward, check_forward, forward,
+                                    make)
 
 pytestmark = pytest.mark.gpu
 
@@ -57,3 +59,22 @@ def test_no_rows_leave_zero_sums(B):
     torch.cuda.synchronize()
     for n in ("dgamma_post", "dgamma_pre", "dgate"):
         assert torch.equal(got[n], torch.zeros(H, device="cuda"))
+
+
+@pytest.mark.parametrize("T,H", [(9700, 64), (9603, 264), (9480, 512), (4801, 1288), (2401, 2560)])
+@pytest.mark.parametrize("gate", MODES)
+def test_rows_walked_at_several_blocks_an_sm(B, T, H, gate):
+    """Short rows get several blocks of an SM, each with eight rows at least in the backward pass: with
+    more rows than that every block walks on, forward too, and the workspace is used to its end and no
+    further."""
+    d = make(T, H, gate, gate != "none", seed=13)
+    h_out, u, rstd = forward(B, d, T, H, gate, 0.75)
+    cfg = cfg_of(B, T, H)
+    n = B.norm_residual_workspace_size(cfg)
+    assert T // 8 >= n // (8 * H) > 148              # rows of partial sums: two of H floats a block
+    room = torch.full((n + 4096,), 0xa5, dtype=torch.uint8, device="cuda")
+    got = backward(B, d, T, H, gate, 0.75, rstd, ws=room[:n])
+    torch.cuda.synchronize()
+    check_forward(d, T, H, 0.75, h_out, u, rstd)
+    check_backward(d, T, H, gate, 0.75, rstd, got)
+    assert bool((room[n:] == 0xa5).all())
