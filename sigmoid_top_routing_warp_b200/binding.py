@@ -414,32 +414,39 @@ def moe_backward(cfg, x, w_router, logits, topk_idx, topk_w, w13, w2, w13s, w2s,
 
 # The entry points below look their tensors over (type, size, dense layout,
 # current device) before they pass the pointers on: the C ABI sees none of it.
+# Addresses (ints) pass as they are, as in the calls above, and so do tensors of
+# torch's own type for what a byte holds.
 _BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+_BYTES = (_U8, torch.float8_e4m3fn, torch.float8_e8m0fnu, torch.float4_e2m1fn_x2)
 
 
-def _complain(where, name, t, dtype, numel):
-    if t.dtype is not dtype:
+def _look_again(where, name, t, dtype, numel, dev):
+    if isinstance(t, int):
+        return t
+    if t.dtype is not dtype and not (dtype is _U8 and t.dtype in _BYTES):
         raise TypeError("%s: %s must be %s, is %s" % (where, name, dtype, t.dtype))
     if t.numel() != numel:
         raise ValueError("%s: %s has %d elements, needs %d" % (where, name, t.numel(), numel))
     if not t.is_contiguous():
         raise ValueError("%s: %s must be dense and row-major" % (where, name))
-    raise ValueError("%s: %s must be on the current CUDA device" % (where, name))
+    if t.get_device() != dev:
+        raise ValueError("%s: %s must be on the current CUDA device" % (where, name))
+    return t.data_ptr()
 
 
 def _look(where, args):
-    """Pointers of `args`, each (name, tensor or None, dtype, elements); the C
-    ABI says which of them may be NULL."""
+    """Pointers of `args`, each (name, tensor, address or None, dtype, elements);
+    the C ABI says which of them may be NULL."""
     dev = _current_device() if torch.cuda.is_initialized() else -2
     out = []
     for name, t, dtype, numel in args:
         if t is None:
             out.append(None)
-            continue
-        if (t.dtype is not dtype or t.numel() != numel or not t.is_contiguous() or
-                t.get_device() != dev):
-            _complain(where, name, t, dtype, numel)
-        out.append(t.data_ptr())
+        elif (type(t) is int or t.dtype is not dtype or t.numel() != numel or
+              not t.is_contiguous() or t.get_device() != dev):
+            out.append(_look_again(where, name, t, dtype, numel, dev))
+        else:
+            out.append(t.data_ptr())
     return out
 
 

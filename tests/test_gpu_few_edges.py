@@ -170,3 +170,20 @@ def test_a_token_whose_scores_all_vanish(B, norm):
     assert torch.equal(B.ws_view(ws, c, "topk_idx"), p["idx"])
     a, b = p["out"].double(), out.double()
     assert bool(a.isfinite().all()) and float((a - b).norm() / b.norm()) <= 1e-2
+
+
+@pytest.mark.parametrize("kind", ["fp8", "mxfp4"])
+def test_weights_in_torchs_own_types(B, kind):
+    """e4m3 weights, e2m1 codes and e8m0 scales as tensors of those types, and addresses: the same bits."""
+    p = make(B, kind, 2, 256, 32, 2, 128, seed=103)
+    call(B, p)
+    first = p["out"].clone()
+    p["out"].zero_()
+    code = torch.float8_e4m3fn if kind == "fp8" else torch.float4_e2m1fn_x2
+    for n in ("w13", "w2", "w13s", "w2s"):
+        q, s, v = p[n]
+        p[n] = (q.view(code), s if kind == "fp8" else s.view(torch.float8_e8m0fnu), v)
+    bias, p["bias"] = p["bias"], p["bias"].data_ptr()
+    call(B, p)
+    torch.cuda.synchronize()
+    assert torch.equal(p["out"], first)
