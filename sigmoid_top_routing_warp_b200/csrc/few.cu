@@ -9,11 +9,11 @@
 //
 // Roles in a block (20 warps):
 //   warps 0-15  consumers, each with 64 columns of every stage: m16n8k16
-//               matrix instructions, 16 weight rows by 8 tokens; the tokens
-//               are the short side, so the 128-row tiles of tcgen05 would be
-//               coarse units to share out over 148 SMs (a decode token touches
-//               1728 16-row units but 216 of 128 rows), and 4- and 8-bit
-//               weights have to be widened in registers anyway.  Warps 8-15
+//               matrix instructions, 16 weight rows by 8 tokens.  The tokens
+//               are the short side; with a few of them the 128-row tiles of
+//               tcgen05 would be coarse units to share out over 148 SMs (a
+//               decode token touches 1728 16-row units but 216 of 128 rows),
+//               and 4- and 8-bit weights are widened in registers.  Warps 8-15
 //               first make the choice and the plan of touched experts, while
 //               warps 0-7 work on the shared expert, which needs neither
 //   warp 16     weight producer: tensor copies of the weights (and scales),
@@ -25,8 +25,10 @@
 //   R   half a block per expert's logits; grid barrier 0; then every block repeats
 //       the choice (T * E keys) and the plan
 //   1   units of nf SwiGLU features of one expert (nf gate rows, nf up rows,
-//       all of K): SiLU(g) * u * w leaves as a bf16 head and a bf16 tail (16
-//       significand bits) in the workspace; grid barrier 1
+//       all of K): SiLU(g) * u * w leaves as a bf16 head and a bf16 tail in the
+//       workspace; grid barrier 1.  Together they have 16 significand bits: off
+//       by 2^-17, 2^-8 of the outputs' own last rounding.  A third part would
+//       keep binary32's, with half as many rows again in every stage
 //   2   the output rows' sum over all (expert, k) as one long K axis, shared
 //       out evenly to 128 columns; a row block that two or more blocks share
 //       is joined by the last of them, in block order
@@ -44,18 +46,27 @@
 // outputs.
 //
 // What it takes and what bounds it (H = 5120, I = 1536, 256 experts, top 8 and
-// a shared one, cold L2; in brackets the weights' bytes at the rate of a plain
-// copy, 6.53 TB/s):
-//   bf16   1 token 87 us (65): HBM, and 10 us until the choice is known, in
+// a shared one, cold L2; in brackets the bytes of the weights that the timed
+// tokens touch at the rate of a plain copy, 6.53 TB/s):
+//   bf16   1 token 88 us (65): HBM, and 10 us until the choice is known, in
 //          which only the shared expert's weights can be fetched; a cooperative
-//          launch is 6 us by itself.  16 tokens, 78 experts, 649 us (571): HBM
-//          with four stages in flight; without the products the stream took 593
-//   FP8    1 token 61 us (33): the same 16 us, then half the consumers'
-//          instructions; without the products 55
-//   MXFP4  4 tokens, 30 experts, 118 us (60): the consumers' instructions, 340 of a warp for
-//          a stage, 64 of them conversions, where HBM leaves time for 370;
-//          without the products 91
-//   H = 512, I = 128, 32 experts, 1 token: 18.7 us: the launch, two grid
+//          launch is 6 us by itself.  16 tokens 659 to 722 us for 78 to 87
+//          experts (571 to 636), 5.7 TB/s: the consumers' share of a stage; on
+//          78 experts the stream took 593 us without the products (bytes under
+//          way are no bound: four stages of 148 blocks are 19 MB).  Tiles of 128
+//          rows are the better ones there: moe_forward takes 606 us for 79
+//          experts, this kernel 662
+//   FP8    1 token 63 us (33): 16 us of launch, router, choice and plan, 7 around
+//          grid barrier 1, then HBM and the consumers; without the products 55
+//   MXFP4  4 tokens, 28 to 31 experts, 117 to 126 us (56 to 61): the stream with
+//          its serial parts (the same 23 us) takes 91 without the products.  With
+//          them a warp issues 340 instructions for a stage, 64 of them
+//          conversions, and the schedulers issue in 49 % of the cycles: a warp
+//          waits for barriers and copies (a quarter of its time, and an eighth in
+//          the block's barriers), for the results of ld.shared, conversion and
+//          MMA that follow one another (a fifth), and for a busy scheduler or
+//          pipe (another fifth)
+//   H = 512, I = 128, 32 experts, 1 token: 20.5 us: the launch, two grid
 //          barriers of 2 us and code that comes from L2 in every launch
 // Tried and not kept: half stages that alternate between the teams (bf16 +4 %,
 // FP8 +12 %), looking at the next stage's barriers ahead (+2 %), two reduction

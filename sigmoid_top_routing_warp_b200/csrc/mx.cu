@@ -13,9 +13,10 @@
 //
 // Both directions only move bytes: 2 B read and 0.53 B written per value, or
 // the reverse.  163840 x 1536, there and back: 196 us for 1.27 GB, 6.5 TB/s, as
-// fast as a copy (a small matrix is two launches, 11 us).  The matrix is dense and a row is a multiple of 32, so it is
-// walked as one flat array: a lane owns 8 values (a 16-byte access on the
-// bf16 side, 4 bytes of codes), four lanes a block, and every lane keeps
+// fast as a copy (202 to 205 in a loop of calls; a small matrix is two launches,
+// 10 us).  The matrix is dense and a row is a multiple of 32, so it is walked as
+// one flat array: a lane owns 8 values (a 16-byte access on the bf16 side, 4
+// bytes of codes), four lanes a block, and every lane keeps
 // kMxVecs accesses in flight.
 #include "moe.h"
 #include "kernels.cuh"

@@ -59,9 +59,10 @@ constexpr int kNrBwdBlocks = 148;   // row walkers of the backward pass, one par
 
 // Threads of a block of the backward pass, and most blocks of it.  A block works
 // on one row at a time and waits for its sum, so an SM gets as many as 640
-// threads hold, up to eight: 8192 rows of 2560 / 1024 / 256 columns take 62 / 34 /
-// 22 us, with one block an SM 83 / 65 / 58.  Two vectors a thread from 2560 columns
-// on: 2560 with two 80 us and with one 82 in one block an SM, 1024 67 and 63.
+// threads hold, up to eight: 8192 rows of 2560 / 1024 / 256 columns take 58 / 33 /
+// 20 us (with one block an SM, before h was left out where it has no part, 83 /
+// 65 / 58, with several 62 / 34 / 22).  Two vectors a thread from 2560 columns on:
+// 2560 with two 80 us and with one 82 in one block an SM, 1024 67 and 63.
 int bwd_threads(int H) {
     const int vecs = H / 8;
     return ((H <= kNrBwdShort ? vecs : (vecs + 1) / 2) + 31) / 32 * 32;
@@ -432,9 +433,9 @@ __global__ void __launch_bounds__(kNrBwdThreads) norm_residual_bwd_kernel(const 
 // in registers.  A row stays in shared memory until its second pass, which
 // computes the first one's values again (128 registers a thread hold no more),
 // and the columns' weights come from L1.  ST rows are there or on their way.
-// 4096 x 8192: 113 us (403 MB, 62 us of copies), 131 in 1024 threads with half the
-// vectors, 230 with both passes from L2; 2048 x 16384: 126. Without the norm after
-// the update 85 and 74.
+// 4096 x 8192: 109 us (403 MB, 62 us of copies), 131 in 1024 threads with half the
+// vectors, 230 with both passes from L2; 2048 x 16384: 129. Without the norm after
+// the update 84 and 75.
 template <int NV, int ST, bool TOKEN, bool PRE>
 __global__ void __launch_bounds__(kNrWideThreads) norm_residual_bwd_wide_kernel(const NrArgs p) {
     let_dependents_launch();
