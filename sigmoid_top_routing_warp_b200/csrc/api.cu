@@ -186,22 +186,35 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
+typedef CUresult (*CtxGetCurrentFn)(CUcontext*);
+
+template <class Fn>
+Fn driver_fn(const char* name) {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint(name, &p, cudaEnableDefault, &q) != cudaSuccess || q != cudaDriverEntryPointSuccess)
+        return nullptr;
+    return reinterpret_cast<Fn>(p);
+}
+
 EncodeTiledFn encode_fn() {
     static EncodeTiledFn fn = nullptr;
+    static CtxGetCurrentFn get_ctx = nullptr;
     if (!fn) {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(p);
+        get_ctx = driver_fn<CtxGetCurrentFn>("cuCtxGetCurrent");
+        fn = driver_fn<EncodeTiledFn>("cuTensorMapEncodeTiled");
     }
     // The driver wants a context, which a host thread has from its first runtime
     // call that needs one; a map may come before that.  Choosing the current
-    // device again gives the thread its context.
+    // device again gives such a thread its context; a thread that has one (a
+    // caller's own, too) keeps it.
     thread_local bool bound = false;
-    int dev = 0;
-    if (fn && !bound) bound = cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess;
+    if (fn && get_ctx && !bound) {
+        CUcontext ctx = nullptr;
+        int dev = 0;
+        bound = get_ctx(&ctx) == CUDA_SUCCESS && ctx;
+        if (!bound) bound = cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess;
+    }
     return fn;
 }
 
