@@ -116,11 +116,12 @@ constexpr int kBoxBytes = 8192;                  // its bytes, for every weight 
 constexpr int kSlice = 64;                       // K columns of a warp in a stage
 constexpr int kMaxStages = 8;
 constexpr float kBf16Max = 0x1.fep+127f;
-// Phase 2's sums over 8- and 4-bit weights are held times 2^-kDownShift: a sum
-// of codes times a lifted output reaches 2^24 times the output (2^15 by 448 by
-// a few terms) before it meets the weights' scale, and must not overflow there.
-// (An output is lifted by at most 2^102 then: off by 2^-127 at most for it.)
-constexpr int kDownShift = 24;
+// Phase 2's sums over 8- and 4-bit weights are held times 2^-kDownShift.  A sum
+// of codes times lifted outputs is up to 2^30 (2^15 by 448, 16 columns, 4 sums) and
+// what undoes the lift up to 2^113, so it would overflow before it meets the
+// weights' scale.  At the other end an output is lifted by at most 2^110, and
+// what it and the sums lose is below bf16's smallest value, 2^-133.
+constexpr int kDownShift = 16;
 constexpr int kBarWord = moe::kSchedFirstWord;   // grid barriers (2) and the exit count, in the status block
 
 // Per weight type: rows of a unit, bits of a weight, bytes of a stage's scales

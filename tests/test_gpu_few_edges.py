@@ -187,3 +187,24 @@ def test_weights_in_torchs_own_types(B, kind):
     call(B, p)
     torch.cuda.synchronize()
     assert torch.equal(p["out"], first)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("T", [2, 7])
+def test_outputs_near_the_small_end(B, kind, T):
+    """Tokens so small that the outputs come near 2^-110: as exact as ever (and a binary32 sum of n terms
+    loses up to n halves of its smallest step, 2^-149, which is 2^-133 where the sums are held 2^-16
+    lower)."""
+    H, I = 512, 128
+    p = make(B, kind, T, H, 32, 2, I, seed=107)
+    p["w_router"].zero_()
+    p["x"][0] *= 2.0 ** -54
+    call(B, p)
+    torch.cuda.synchronize()
+    B.moe_check_device_status(p["ws"])
+    out, tol, idx, _ = reference(p)
+    assert torch.equal(p["idx"].cpu(), idx)
+    assert 2.0 ** -116 < float(out[0].abs().max()) < 2.0 ** -100
+    err = (p["out"].cpu().double() - out).abs()
+    tol = tol + 3 * I * 2.0 ** -133 if kind != "bf16" else tol + 3 * I * 2.0 ** -149
+    assert bool((err <= tol).all()), float((err / tol).max())
