@@ -20,6 +20,9 @@ moe_status_t fail(moe_status_t st, const char* fmt, ...) {
     va_start(ap, fmt);
     vsnprintf(g_err, sizeof(g_err), fmt, ap);
     va_end(ap);
+    // the runtime keeps an error until it is asked for: told here, it is not the
+    // next call's
+    if (st == MOE_ERR_CUDA) (void)cudaGetLastError();
     return st;
 }
 
