@@ -421,7 +421,7 @@ _BYTES = (_U8, torch.float8_e4m3fn, torch.float8_e8m0fnu, torch.float4_e2m1fn_x2
 
 
 def _look_again(where, name, t, dtype, numel, dev):
-    if isinstance(t, int):
+    if t is None or isinstance(t, int):
         return t
     if t.dtype is not dtype and not (dtype is _U8 and t.dtype in _BYTES):
         raise TypeError("%s: %s must be %s, is %s" % (where, name, dtype, t.dtype))
@@ -439,14 +439,17 @@ def _look(where, args):
     the C ABI says which of them may be NULL."""
     dev = _current_device() if torch.cuda.is_initialized() else -2
     out = []
-    for name, t, dtype, numel in args:
-        if t is None:
-            out.append(None)
-        elif (type(t) is int or t.dtype is not dtype or t.numel() != numel or
-              not t.is_contiguous() or t.get_device() != dev):
-            out.append(_look_again(where, name, t, dtype, numel, dev))
-        else:
-            out.append(t.data_ptr())
+    try:
+        for name, t, dtype, numel in args:
+            if t is None:
+                out.append(None)
+            elif (t.dtype is not dtype or t.numel() != numel or not t.is_contiguous() or
+                  t.get_device() != dev):
+                out.append(_look_again(where, name, t, dtype, numel, dev))
+            else:
+                out.append(t.data_ptr())
+    except AttributeError:      # an address among them
+        return [_look_again(where, *a, dev) for a in args]
     return out
 
 
